@@ -60,8 +60,12 @@ typedef enum {
 /* [V41] CSA2 paragraph: the three per-layer modes. */
 typedef enum { CSA2_FULL = 0, CSA2_REINDEX = 1, CSA2_REUSE = 2 } csa2_mode;
 
-/* Main-KV storage.  [R] FP4 主KV缓存: E2M1 codes + one E4M3 scale / 16 channels. */
-typedef enum { CSA2_KV_BF16 = 0, CSA2_KV_FP4 = 1 } csa2_kv_fmt;
+/* Main-KV storage.  [R] FP4 主KV缓存: E2M1 codes + one E4M3 scale / 16 channels.
+ * F16 (IEEE binary16) is a storage of the paged cache calls only. */
+typedef enum { CSA2_KV_BF16 = 0, CSA2_KV_FP4 = 1, CSA2_KV_F16 = 2 } csa2_kv_fmt;
+
+/* 16-bit type of the queries, keys and values of the head and paged calls. */
+typedef enum { CSA2_BF16 = 0, CSA2_F16 = 1 } csa2_dtype;
 
 /* Per-head activation of the indexer score: ReLU (the DSA form [V4] eq. 8 is
  * tied to) or none. */
@@ -302,6 +306,140 @@ csa2_status csa2_fp4_unpack(const uint8_t* codes, const uint8_t* scales, int64_t
                             void* x, csa2_stream stream);
 
 /* ------------------------------------------------------------------------ */
+/* (p) Uncompressed layers over a paged cache.  A layer that keeps every token
+ * (or a window of them) uncompressed stands beside the CSA2 layers; these four
+ * calls serve it: norms and position rotation of its queries and keys, writing
+ * its keys and values into a paged cache, attention of one new token per
+ * sequence, and attention of a prompt chunk.  The pages name the parts (RMSNorm
+ * on Q and K, rotary positions, the 128-token window branch) without formulas;
+ * the formulas are stated per call.
+ *
+ * Rows of heads: row (t, h) of D channels starts token_stride * t +
+ * head_stride * h elements after data; the channels of a row are adjacent.
+ * Strides are multiples of 8, data is 16-byte aligned; strides of 0 mean dense
+ * ([T, heads, D]). */
+typedef struct {
+  void* data;
+  int heads;
+  int64_t token_stride, head_stride;
+} csa2_heads;
+
+/* Position rotation of channels [offset, offset + 2 * half) of a row: pair i
+ * turns by the angle pos * inv_freq[i] (product and sine in 64 bits, sine and
+ * cosine rounded to f32):
+ *   (a, b) -> (a cos - b sin, b cos + a sin), every product and sum rounded to f32,
+ * with (a, b) = channels offset + (i, i + half), or offset + (2i, 2i + 1) when
+ * interleaved.  inverse != 0 turns by the negative angle (an output that was
+ * attended over rotated shared rows is turned back with it).
+ *   inv_freq f32 [half] (device)
+ * Requires half % 8 == 0, offset % 8 == 0, offset + 2 * half <= D. */
+typedef struct {
+  const float* inv_freq;
+  int half, offset, interleaved, inverse;
+} csa2_rope;
+
+/* RMS norm and position rotation of queries and keys in one pass.
+ *   y = x * rsqrt(mean(x^2) + eps) * weight   (per row; weight f32 [D], NULL: y = x)
+ *   out = rotate(y, positions[t])             (rope NULL: out = y)
+ * f32 arithmetic, rounded once.  q or k may be NULL (then its out is not read).
+ * q_out / k_out have q's / k's heads; an out may be exactly its input (in
+ * place), else it must not overlap any input.
+ *   positions int32 [T], any value; NULL allowed when rope is NULL
+ * Requires D % 8 == 0, 8 <= D <= 512, weights 16-byte aligned.  Errors: CSA2_ERR_INVALID. */
+csa2_status csa2_qk_norm_rope(csa2_dtype dtype, const csa2_heads* q, const float* q_weight,
+                              const csa2_heads* q_out, const csa2_heads* k, const float* k_weight,
+                              const csa2_heads* k_out, int64_t T, int D, float eps,
+                              const int32_t* positions, const csa2_rope* rope, csa2_stream stream);
+
+/* A paged cache: n_pages pages of page_size tokens, heads rows of dim channels
+ * per token.  Token j of sequence b lives in slot j % page_size of page
+ * table[b * table_stride + j / page_size].
+ *   k, v    row (page, slot, head) starts page_stride * page + token_stride *
+ *           slot + head_stride * head channels after the base; strides of 0 mean
+ *           dense [n_pages, page_size, heads, dim].  v = NULL: values are the
+ *           key rows (shared K = V, as in eq. (9)).  v has k's strides.
+ *   fmt     BF16, F16: 16-bit rows, strides multiples of 8.  FP4: the base is
+ *           uint8 codes (a stride of s channels is s / 2 bytes of codes and s / 16
+ *           bytes of k_scales / v_scales), strides multiples of 32.
+ *   table   int32 [B, max_pages], rows table_stride apart (0: max_pages)
+ *   lens    int32 [B]: tokens in the cache, the newest included
+ *   max_len a bound of lens[] the caller knows, or 0: max_pages * page_size.
+ *           It only sets into how many chunks a decode launch is cut; a longer
+ *           sequence is still attended whole (its last chunk takes the rest).
+ * page_size is a power of two up to 65536.  A length outside [0, max_pages *
+ * page_size] or a table entry outside [0, n_pages) that a call needs is
+ * recorded as CSA2_ERR_BOUNDS; the length is clamped, the page's tokens are
+ * skipped.  Table entries past a sequence's length are never read. */
+typedef struct {
+  csa2_kv_fmt fmt;
+  void *k, *v;
+  uint8_t *k_scales, *v_scales;
+  int64_t n_pages, page_stride, token_stride, head_stride;
+  int page_size, heads, dim;
+  int B, max_pages;
+  int64_t table_stride;
+  const int32_t* table;
+  const int32_t* lens;
+  int64_t max_len;
+} csa2_paged_kv;
+
+/* Appends keys and values: row t of k (turned to position pos[t], rope NULL:
+ * as it is) and of v go to token pos[t] of sequence seq[t].  The result is
+ * rounded once to the cache's 16-bit type; an FP4 cache takes csa2_fp4_pack of
+ * that rounded row.  seq[t] = -1 skips the row (a padded batch).  cache->lens
+ * is not read.  Two rows of one call must not name the same token.
+ *   k, v   dtype rows, heads == cache->heads, D == cache->dim; v NULL for a
+ *          shared cache (cache->v NULL)
+ *   seq, pos int32 [T]
+ * dtype is F16 for an F16 cache, else BF16.  Requires dim % 8 == 0 and <= 512;
+ * FP4: dim % 32 == 0, rope half % 16 == 0 and offset % 16 == 0.  A sequence
+ * outside [-1, B), a position outside the table's row or a page outside the
+ * pool is recorded as CSA2_ERR_BOUNDS and the row skipped. */
+csa2_status csa2_paged_append(csa2_dtype dtype, const csa2_heads* k, const csa2_heads* v,
+                              const int32_t* seq, const int32_t* pos, int64_t T,
+                              const csa2_rope* rope, const csa2_paged_kv* cache,
+                              csa2_stream stream);
+
+/* Attention of one new token per sequence over the paged cache.  Query b sits
+ * at position p = lens[b] - 1 and sees token j <= p when p - j < window
+ * (window = 0: always) or j < sinks (the first tokens that stay visible):
+ *   out[b,h,:] = sum_j softmax_j(scale * q[b,h] . k[j, h / (Hq / heads)]) v[j, ...]
+ *   lse[b,h]   = log sum_j exp(scale * q . k)
+ * A sequence of length 0 gives out = 0 and lse = -inf.  Dot products, softmax
+ * statistics and sums in f32, the weights rounded to the 16-bit type for the
+ * product with the values, out rounded once.  FP4 rows are dequantised exactly.
+ * The visible tokens are cut into chunks that run side by side and are joined
+ * in order.  chunk > 0 (a multiple of 64) fixes their length: a query's bits
+ * then depend on its own sequence only (lens[b] <= max_len); chunk = 0 lets the library choose it
+ * from B, heads and max_len.
+ *   q    rows of the cache's 16-bit type (bf16 for FP4), heads a multiple of
+ *        cache->heads
+ *   out  [B, Hq, dim] dense      lse f32 [B, Hq] or NULL
+ * Requires dim in {64, 128, 256, 512}, window >= 0, sinks >= 0.
+ * workspace: csa2_paged_decode_attn_workspace(...) bytes (0: NULL allowed), on
+ * the current device. */
+size_t csa2_paged_decode_attn_workspace(const csa2_paged_kv* cache, int Hq, int window, int sinks,
+                                        int chunk);
+csa2_status csa2_paged_decode_attn(const csa2_heads* q, const csa2_paged_kv* cache, float scale,
+                                   int window, int sinks, int chunk, void* out, float* lse,
+                                   void* workspace, size_t workspace_bytes, csa2_stream stream);
+
+/* Attention of a prompt chunk over the paged cache: sequence b's new tokens are
+ * rows cu_q[b] .. cu_q[b+1] of q, the last of them at position lens[b] - 1 (the
+ * keys and values of all of them already appended).  Each query sees tokens as
+ * in csa2_paged_decode_attn from its own position; a query whose position would
+ * be negative (more rows than lens[b]) sees nothing.  Rows outside every
+ * sequence (behind cu_q[B]) are left as they were.  The bits of a query do not
+ * depend on the other sequences or on where the prompt was cut into chunks.
+ *   q    rows of the cache's 16-bit type    cu_q int32 [B + 1], ascending, cu_q[B] <= T
+ *   out [T, Hq, dim] dense        lse f32 [T, Hq] or NULL
+ * Requires dim in {64, 128, 256, 512}.  A cu_q that descends or leaves [0, T]
+ * is recorded as CSA2_ERR_BOUNDS and its sequence skipped. */
+csa2_status csa2_paged_window_attn(const csa2_heads* q, const int32_t* cu_q, int64_t T,
+                                   const csa2_paged_kv* cache, float scale, int window, int sinks,
+                                   void* out, float* lse, csa2_stream stream);
+
+/* ------------------------------------------------------------------------ */
 /* (a6) Layer-mode driver.  [V41] CSA2 paragraph: Full builds its KV and
  * indexer K, runs the indexer and picks its own top-k; Reindex reuses the
  * previous main KV and indexer K but scores its own queries; Reuse reuses
@@ -370,8 +508,8 @@ const char* csa2_last_error(void);
 csa2_status csa2_device_error(csa2_stream stream);
 /* Kernel launches issued by this library since the last reset, per kind:
  * 0 compress, 1 index scores (all entries), 2 top-k, 3 attention, 4 attention
- * combine, 5 fp4 pack, 6 fp4 unpack, 7 other (memsets), 8 index scores inside
- * a pool.  Returns the number of kinds. */
+ * combine, 5 fp4 pack, 6 fp4 unpack, 7 other (memsets, head norms, cache
+ * append), 8 index scores inside a pool.  Returns the number of kinds. */
 int csa2_launch_counts(int64_t* counts, int n);
 void csa2_reset_launch_counts(void);
 /* Per-kind device time of this library's kernels (instrumentation).  While

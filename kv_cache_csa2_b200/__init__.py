@@ -17,11 +17,13 @@ __all__ = [
     "csa2_sparse_attn", "csa2_sparse_attn_swa", "csa2_dense_attn", "csa2_compress_hca",
     "csa2_index_scores_fp4", "csa2_index_topk_fp4",
     "csa2_fp4_pack", "csa2_fp4_unpack", "Group", "csa2_device_error",
+    "KV_F16", "Rope", "PagedKv", "csa2_qk_norm_rope", "csa2_paged_append", "csa2_paged_decode_attn",
+    "csa2_paged_window_attn",
     "launch_counts", "reset_launch_counts", "set_fault", "set_device_wait", "EXPORTED_SYMBOLS",
 ]
 
 FULL, REINDEX, REUSE = 0, 1, 2
-KV_BF16, KV_FP4 = 0, 1
+KV_BF16, KV_FP4, KV_F16 = 0, 1, 2
 ACT_RELU, ACT_IDENTITY = 0, 1
 _MODE = {"full": FULL, "reindex": REINDEX, "reuse": REUSE, FULL: FULL, REINDEX: REINDEX,
          REUSE: REUSE}
@@ -44,6 +46,23 @@ class CSA2LayerIO(ctypes.Structure):
                 ("w_index", _P), ("q_attn", _P), ("out", _P), ("lse", _P),
                 ("swa_kv", _P), ("swa_rows", _I64), ("swa_end", _P), ("swa_window", _I)]
 
+
+class CSA2Heads(ctypes.Structure):
+    _fields_ = [("data", _P), ("heads", _I), ("token_stride", _I64), ("head_stride", _I64)]
+
+
+class CSA2Rope(ctypes.Structure):
+    _fields_ = [("inv_freq", _P), ("half", _I), ("offset", _I), ("interleaved", _I), ("inverse", _I)]
+
+
+class CSA2PagedKv(ctypes.Structure):
+    _fields_ = [("fmt", _I), ("k", _P), ("v", _P), ("k_scales", _P), ("v_scales", _P), ("n_pages", _I64),
+                ("page_stride", _I64), ("token_stride", _I64), ("head_stride", _I64), ("page_size", _I),
+                ("heads", _I), ("dim", _I), ("B", _I), ("max_pages", _I), ("table_stride", _I64),
+                ("table", _P), ("lens", _P), ("max_len", _I64)]
+
+
+_HEADS, _ROPE, _PAGED = ctypes.POINTER(CSA2Heads), ctypes.POINTER(CSA2Rope), ctypes.POINTER(CSA2PagedKv)
 
 # name -> (restype, argtypes); every symbol include/csa2.h declares
 _SIGS = {
@@ -69,6 +88,11 @@ _SIGS = {
     "csa2_compress_hca": (_I, [_P, _P, _P, _I, _I64, _I, _I, _P, _I64, _P]),
     "csa2_fp4_pack": (_I, [_P, _I64, _I, _P, _P, _P]),
     "csa2_fp4_unpack": (_I, [_P, _P, _I64, _I, _P, _P]),
+    "csa2_qk_norm_rope": (_I, [_I, _HEADS, _P, _HEADS, _HEADS, _P, _HEADS, _I64, _I, _F, _P, _ROPE, _P]),
+    "csa2_paged_append": (_I, [_I, _HEADS, _HEADS, _P, _P, _I64, _ROPE, _PAGED, _P]),
+    "csa2_paged_decode_attn_workspace": (_SZ, [_PAGED, _I, _I, _I, _I]),
+    "csa2_paged_decode_attn": (_I, [_HEADS, _PAGED, _F, _I, _I, _I, _P, _P, _P, _SZ, _P]),
+    "csa2_paged_window_attn": (_I, [_HEADS, _P, _I64, _PAGED, _F, _I, _I, _P, _P, _P]),
     "csa2_group_create": (_I, [ctypes.POINTER(_P), ctypes.POINTER(CSA2GroupDesc)]),
     "csa2_group_layer": (_I, [_P, _I, ctypes.POINTER(CSA2LayerIO), _P]),
     "csa2_group_selection": (_I, [_P, ctypes.POINTER(_P), ctypes.POINTER(_P)]),
@@ -378,6 +402,270 @@ def csa2_fp4_unpack(codes, scales, stream=None):
     x = torch.empty(*codes.shape[:-1], D, dtype=torch.bfloat16, device=codes.device)
     _check(lib().csa2_fp4_unpack(_ptr(codes), _ptr(scales), rows, D, _ptr(x), _stream(stream)))
     return x
+
+
+# ------------------------------------------------------------------ (p)
+# The calls of this part run on their tensors' device and, with `stream`, on
+# that stream: results and scratch memory are then allocated for it, and the
+# inputs are marked as in use by it.
+
+def _run_on(fn, tensors, stream, args, kw):
+    """None when the current device and stream already are the call's, else
+    (its result,) from a call made with them current."""
+    torch = _torch()
+    dev = None
+    for t in tensors:
+        if t is None:
+            continue
+        if not t.is_cuda:
+            raise ValueError(f"{fn.__name__}: expected CUDA tensors, got one on {t.device}")
+        if dev is None:
+            dev = t.get_device()
+        elif t.get_device() != dev:
+            raise ValueError(f"{fn.__name__}: tensors on devices {dev} and {t.get_device()}")
+    if stream is not None:
+        if dev is not None and stream.device.index != dev:
+            raise ValueError(f"{fn.__name__}: a stream of device {stream.device.index} with tensors on {dev}")
+        if stream != torch.cuda.current_stream(dev):
+            for t in tensors:
+                if t is not None:
+                    t.record_stream(stream)
+        with torch.cuda.stream(stream):
+            return (fn(*args, **kw),)
+    if dev is not None and dev != torch.cuda.current_device():
+        with torch.cuda.device(dev):
+            return (fn(*args, **kw),)
+    return None
+
+
+def _rows(t, name, dtype=None):
+    """csa2_heads of a [T, heads, D] tensor with adjacent channels."""
+    torch = _torch()
+    if t is None:
+        raise ValueError(f"{name} is required")
+    if t.dim() != 3 or (t.dtype != dtype if dtype is not None else t.dtype not in (torch.bfloat16, torch.float16)):
+        raise ValueError(f"{name}: expected {dtype or 'bfloat16 or float16'} [T, heads, D], got {t.dtype} "
+                         f"{tuple(t.shape)}")
+    T, H, D = t.shape
+    ts, hs, cs = t.stride()
+    if H <= 1:
+        hs = D
+    if T <= 1:
+        ts = H * hs
+    if (cs != 1 and D > 1) or ts <= 0 or hs <= 0:
+        raise ValueError(f"{name}: channels must be adjacent and rows distinct, got strides {t.stride()}")
+    return CSA2Heads(t.data_ptr(), H, ts, hs)
+
+
+def _ints(t, name, shape):
+    torch = _torch()
+    if t is None or t.dtype != torch.int32 or tuple(t.shape) != shape or not t.is_contiguous():
+        got = None if t is None else (t.dtype, tuple(t.shape))
+        raise ValueError(f"{name}: expected contiguous int32 {shape}, got {got}")
+    return t
+
+
+class Rope:
+    """A position rotation: pair i of channels [offset, offset + 2 * half) turns
+    by pos * inv_freq[i] (inv_freq f32 CUDA [half]); pairs (i, i + half), or
+    neighbours when interleaved; inverse turns back."""
+
+    def __init__(self, inv_freq, offset: int = 0, interleaved: bool = False, inverse: bool = False):
+        torch = _torch()
+        _need(inv_freq, torch.float32, 1, "inv_freq")
+        self.inv_freq = inv_freq
+        self.desc = CSA2Rope(inv_freq.data_ptr(), inv_freq.numel(), offset, int(interleaved), int(inverse))
+
+
+class PagedKv:
+    """A paged cache: k (and v; None: values are the key rows) [n_pages,
+    page_size, heads, D] bf16 / f16 with adjacent channels, or uint8 FP4 codes
+    [n_pages, page_size, heads, D/2] with scales [n_pages, page_size, heads, D/16];
+    table int32 [B, max_pages], lens int32 [B] (device; the program updates them
+    in place).  max_len: a bound of lens it knows (0: what the table holds)."""
+
+    def __init__(self, k, table, lens, v=None, k_scales=None, v_scales=None, max_len: int = 0):
+        torch = _torch()
+        if k is None or k.dim() != 4 or not k.is_cuda:
+            raise ValueError("k: expected a CUDA tensor [n_pages, page_size, heads, D]")
+        fmts = {torch.bfloat16: KV_BF16, torch.float16: KV_F16, torch.uint8: KV_FP4}
+        if k.dtype not in fmts:
+            raise ValueError(f"k: unknown cache type {k.dtype}")
+        fmt = fmts[k.dtype]
+        fp4 = fmt == KV_FP4
+        if v is k:
+            v, v_scales = None, None
+        n_pages, page, heads, width = k.shape
+        dim = 2 * width if fp4 else width
+        strides = self._strides(k, "k", 2 if fp4 else 1, dim)
+        if v is not None and (v.dtype != k.dtype or v.shape != k.shape or self._strides(v, "v", 2 if fp4 else 1, dim) != strides):
+            raise ValueError("v: type, shape and strides must be k's")
+        for s, x, name in ((k_scales, k, "k_scales"), (v_scales, v, "v_scales")):
+            if (s is not None) != (fp4 and x is not None):
+                raise ValueError(f"{name}: scales belong to an FP4 cache's rows, and only to them")
+            if s is not None and (s.dtype != torch.uint8 or tuple(s.shape) != (n_pages, page, heads, dim // 16) or
+                                  self._strides(s, name, 16, dim) != strides):
+                raise ValueError(f"{name}: expected uint8 [n_pages, page_size, heads, D/16] laid out like {name[0]}")
+        if table is None or table.dtype != torch.int32 or table.dim() != 2 or (table.shape[1] > 1 and table.stride(1) != 1):
+            raise ValueError("table: expected int32 [B, max_pages]")
+        B, max_pages = table.shape
+        _ints(lens, "lens", (B,))
+        if B > 1 and table.stride(0) < max_pages:
+            raise ValueError("table: rows overlap")
+        self.k, self.v, self.k_scales, self.v_scales, self.table, self.lens = k, v, k_scales, v_scales, table, lens
+        self.tensors = (k, v, k_scales, v_scales, table, lens)
+        if len({t.get_device() for t in self.tensors if t is not None}) != 1:
+            raise ValueError("the cache's tensors must be on one device")
+        self.dtype = torch.bfloat16 if fp4 else k.dtype
+        self.heads, self.dim, self.B = heads, dim, B
+        self.desc = CSA2PagedKv(fmt, k.data_ptr(), None if v is None else v.data_ptr(),
+                                None if k_scales is None else k_scales.data_ptr(),
+                                None if v_scales is None else v_scales.data_ptr(), n_pages, strides[0], strides[1],
+                                strides[2], page, heads, dim, B, max_pages,
+                                table.stride(0) if B > 1 else max_pages, table.data_ptr(), lens.data_ptr(), max_len)
+
+    @staticmethod
+    def _strides(t, name, unit, dim):
+        """(page, token, head) strides in channels; dimensions of one element count as dense."""
+        n, page, heads, width = t.shape
+        st = [x * unit for x in t.stride()]
+        if heads <= 1:
+            st[2] = dim
+        if page <= 1:
+            st[1] = heads * st[2]
+        if n <= 1:
+            st[0] = page * st[1]
+        if (width > 1 and t.stride(3) != 1) or min(st[:3]) < dim:
+            raise ValueError(f"{name}: channels must be adjacent and rows distinct, got strides {t.stride()}")
+        return tuple(st[:3])
+
+
+_DTYPE_ID = {}
+
+
+def _dtype_id(dtype):
+    if not _DTYPE_ID:
+        torch = _torch()
+        _DTYPE_ID.update({torch.bfloat16: 0, torch.float16: 1})
+    return _DTYPE_ID[dtype]
+
+
+def _weight(w, name, D):
+    if w is not None:
+        _need(w, _torch().float32, 1, name)
+        if w.numel() != D:
+            raise ValueError(f"{name}: {w.numel()} values for rows of {D}")
+    return _ptr(w)
+
+
+def csa2_qk_norm_rope(q, k, positions=None, q_weight=None, k_weight=None, eps: float = 1e-6, rope=None, q_out=None,
+                      k_out=None, stream=None):
+    """RMS norm of every head row (weight f32 [D] or None) and its rotation to
+    positions[t] (int32 [T]); q, k [T, heads, D] bf16 / f16 (either may be None).
+    q_out / k_out may be q / k (in place).  Returns (q_out, k_out)."""
+    done = _run_on(csa2_qk_norm_rope, (q, k, positions, q_weight, k_weight, q_out, k_out, rope and rope.inv_freq),
+                   stream, (q, k, positions, q_weight, k_weight, eps, rope, q_out, k_out), {})
+    if done:
+        return done[0]
+    torch = _torch()
+    x = q if q is not None else k
+    if x is None:
+        raise ValueError("csa2_qk_norm_rope: neither q nor k given")
+    T, _, D = x.shape if x.dim() == 3 else (0, 0, 0)
+    args = []
+    outs = []
+    for t, w, out, name in ((q, q_weight, q_out, "q"), (k, k_weight, k_out, "k")):
+        if t is None:
+            args += [None, None, None]
+            outs.append(None)
+            continue
+        rows = _rows(t, name, x.dtype)
+        if t.shape[0] != T or t.shape[2] != D:
+            raise ValueError(f"{name}: {tuple(t.shape)} beside {T} rows of {D} channels")
+        if out is None:
+            out = torch.empty(t.shape, dtype=t.dtype, device=t.device)
+        elif out.shape != t.shape:
+            raise ValueError(f"{name}_out: {tuple(out.shape)} for {name} {tuple(t.shape)}")
+        args += [ctypes.byref(rows), _weight(w, name + "_weight", D), ctypes.byref(_rows(out, name + "_out", x.dtype))]
+        outs.append(out)
+    if positions is not None:
+        _ints(positions, "positions", (T,))
+    _check(lib().csa2_qk_norm_rope(_dtype_id(x.dtype), *args, T, D, eps, _ptr(positions),
+                                   None if rope is None else ctypes.byref(rope.desc), _stream()))
+    return outs[0], outs[1]
+
+
+def csa2_paged_append(cache, k, v, seq, pos, rope=None, stream=None):
+    """Write rows k (rotated to pos when `rope`), v [T, heads, D] to tokens pos[t] of
+    sequences seq[t] (int32 [T]; seq -1: skip) of a PagedKv; v None for a shared cache."""
+    done = _run_on(csa2_paged_append, (k, v, seq, pos, rope and rope.inv_freq) + cache.tensors, stream,
+                   (cache, k, v, seq, pos, rope), {})
+    if done:
+        return done[0]
+    kr = _rows(k, "k", cache.dtype)
+    T = k.shape[0]
+    if k.shape[2] != cache.dim or (v is not None and v.shape != k.shape):
+        raise ValueError(f"k, v: {tuple(k.shape)}, {None if v is None else tuple(v.shape)} for a cache of width {cache.dim}")
+    vr = None if v is None else ctypes.byref(_rows(v, "v", cache.dtype))
+    _ints(seq, "seq", (T,))
+    _ints(pos, "pos", (T,))
+    _check(lib().csa2_paged_append(_dtype_id(cache.dtype), ctypes.byref(kr), vr, _ptr(seq), _ptr(pos), T,
+                                   None if rope is None else ctypes.byref(rope.desc), ctypes.byref(cache.desc),
+                                   _stream()))
+
+
+def _attn_out(q, out, lse):
+    torch = _torch()
+    if out is None:
+        out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+    elif out.dtype != q.dtype or out.shape != q.shape or not out.is_contiguous():
+        raise ValueError(f"out: expected contiguous {q.dtype} {tuple(q.shape)}")
+    if lse is None:
+        lse = torch.empty(q.shape[:2], dtype=torch.float32, device=q.device)
+    elif lse.dtype != torch.float32 or lse.shape != q.shape[:2] or not lse.is_contiguous():
+        raise ValueError(f"lse: expected contiguous float32 {tuple(q.shape[:2])}")
+    return out, lse
+
+
+def csa2_paged_decode_attn(q, cache, scale: float, window: int = 0, sinks: int = 0, chunk: int = 0, out=None, lse=None,
+                           stream=None):
+    """Attention of one new token per sequence (q [B, Hq, D], at position lens[b] - 1)
+    over a PagedKv: the last `window` tokens (0: all) and the first `sinks`."""
+    done = _run_on(csa2_paged_decode_attn, (q, out, lse) + cache.tensors, stream,
+                   (q, cache, scale, window, sinks, chunk, out, lse), {})
+    if done:
+        return done[0]
+    rows = _rows(q, "q", cache.dtype)
+    B, Hq, D = q.shape
+    if B != cache.B or D != cache.dim:
+        raise ValueError(f"q: {tuple(q.shape)} for a cache of {cache.B} sequences of width {cache.dim}")
+    out, lse = _attn_out(q, out, lse)
+    L = lib()
+    desc = ctypes.byref(cache.desc)
+    nb = L.csa2_paged_decode_attn_workspace(desc, Hq, window, sinks, chunk)
+    ws = _workspace(nb, q.device)
+    _check(L.csa2_paged_decode_attn(ctypes.byref(rows), desc, scale, window, sinks, chunk, _ptr(out), _ptr(lse),
+                                    _ptr(ws), nb, _stream()))
+    return out, lse
+
+
+def csa2_paged_window_attn(q, cu_q, cache, scale: float, window: int = 0, sinks: int = 0, out=None, lse=None,
+                           stream=None):
+    """Causal attention of a prompt chunk: sequence b's new tokens are rows
+    cu_q[b]..cu_q[b+1] of q [T, Hq, D], the last at position lens[b] - 1."""
+    done = _run_on(csa2_paged_window_attn, (q, cu_q, out, lse) + cache.tensors, stream,
+                   (q, cu_q, cache, scale, window, sinks, out, lse), {})
+    if done:
+        return done[0]
+    rows = _rows(q, "q", cache.dtype)
+    T, _, D = q.shape
+    if D != cache.dim:
+        raise ValueError(f"q: {tuple(q.shape)} for a cache of width {cache.dim}")
+    _ints(cu_q, "cu_q", (cache.B + 1,))
+    out, lse = _attn_out(q, out, lse)
+    _check(lib().csa2_paged_window_attn(ctypes.byref(rows), _ptr(cu_q), T, ctypes.byref(cache.desc), scale, window,
+                                        sinks, _ptr(out), _ptr(lse), _stream()))
+    return out, lse
 
 
 # ------------------------------------------------------------------ (a6)

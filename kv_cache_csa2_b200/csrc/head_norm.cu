@@ -1,0 +1,169 @@
+// RMS norm and position rotation of query and key heads in one pass:
+//   y = x * rsqrt(mean(x^2) + eps) * weight, then the rotated pairs turn by
+//   positions[t] * inv_freq.
+// HBM-bound (each channel is read and written once, two bytes each way).  A CTA
+// takes a block of tokens: it requests its first rows, computes the tokens'
+// angles once for all heads into shared memory, and then runs over the
+// (token, head) rows; a group of lanes holds a row, the norm is a shuffle sum.
+#include <algorithm>
+
+#include "common.cuh"
+#include "launchers.h"
+#include "paged.h"
+#include "rope.cuh"
+
+namespace csa2 {
+namespace {
+using namespace rope;
+
+constexpr int kThreads = 256;
+
+struct Side {
+  const uint16_t* in;
+  uint16_t* out;
+  const float* weight;               // null: no norm
+  int64_t in_t, in_h, out_t, out_h;  // strides in elements
+};
+
+struct Params {
+  Side q, k;
+  const int32_t* positions;
+  int64_t T;
+  int Hq, H, D, items, lanes;        // H = query plus key heads; lanes per row (power of two)
+  int tokens, rows_cta;              // tokens per CTA, rows per CTA (grid.y cuts a token's heads)
+  float eps;
+  RopeArgs rope;
+};
+
+template <class T>
+__global__ void __launch_bounds__(kThreads) head_norm_kernel(const Params p) {
+  extern __shared__ float2 cs[];                                   // [tokens][half]
+  const int64_t t0 = static_cast<int64_t>(blockIdx.x) * p.tokens;
+  const int nt = static_cast<int>(min(static_cast<int64_t>(p.tokens), p.T - t0));
+  const int per_pass = kThreads / p.lanes;
+  const int sub = threadIdx.x & (p.lanes - 1);
+  const int r_end = min(nt * p.H, static_cast<int>(blockIdx.y + 1) * p.rows_cta);
+  int r = blockIdx.y * p.rows_cta + threadIdx.x / p.lanes;
+  Item it = item_at(sub, p.D, p.rope.half, p.rope.offset);
+  if (sub >= p.items) it.c0 = it.c1 = it.freq = -1;
+
+  uint4 v0, v1;
+  int tl = 0, head = 0;
+  auto request = [&](int row) {
+    v0 = v1 = make_uint4(0, 0, 0, 0);
+    if (row >= r_end) return;
+    tl = row / p.H;
+    head = row - tl * p.H;
+    const uint16_t* src = head < p.Hq ? p.q.in + (t0 + tl) * p.q.in_t + head * p.q.in_h
+                                      : p.k.in + (t0 + tl) * p.k.in_t + (head - p.Hq) * p.k.in_h;
+    if (it.c0 >= 0) v0 = *reinterpret_cast<const uint4*>(src + it.c0);
+    if (it.c1 >= 0) v1 = *reinterpret_cast<const uint4*>(src + it.c1);
+  };
+  pdl_wait();
+  request(r);
+  if (p.rope.inv_freq) {
+    for (int i = threadIdx.x; i < nt * p.rope.half; i += kThreads) {
+      const int t = i / p.rope.half, f = i - t * p.rope.half;
+      cs[i] = angle_of(__ldg(p.positions + t0 + t), __ldg(p.rope.inv_freq + f), p.rope.inverse);
+    }
+    __syncthreads();
+  }
+  // all lanes of a warp stay in the loop together (the shuffles need them)
+  for (int base = blockIdx.y * p.rows_cta; base < r_end; base += per_pass, r += per_pass) {
+    float x0[8], x1[8];
+    unpack8<T>(v0, x0);
+    unpack8<T>(v1, x1);
+    const bool live = r < r_end, is_q = head < p.Hq;
+    const int my_t = tl, my_h = head;
+    const float* w = is_q ? p.q.weight : p.k.weight;
+    float sum = 0.0f;
+#pragma unroll
+    for (int u = 0; u < 8; ++u) sum += x0[u] * x0[u] + x1[u] * x1[u];
+    for (int o = p.lanes >> 1; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    // a row is read whole by its lanes before any of them stores (the shuffle
+    // above), so an output may be its input
+    request(r + per_pass);
+    if (!live) continue;
+    if (w) {
+      const float inv = rsqrtf(sum / static_cast<float>(p.D) + p.eps);
+      if (it.c0 >= 0) {
+        const float4 a = __ldg(reinterpret_cast<const float4*>(w + it.c0));
+        const float4 b = __ldg(reinterpret_cast<const float4*>(w + it.c0) + 1);
+        const float g[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+#pragma unroll
+        for (int u = 0; u < 8; ++u) x0[u] = __fmul_rn(__fmul_rn(x0[u], inv), g[u]);
+      }
+      if (it.c1 >= 0) {
+        const float4 a = __ldg(reinterpret_cast<const float4*>(w + it.c1));
+        const float4 b = __ldg(reinterpret_cast<const float4*>(w + it.c1) + 1);
+        const float g[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+#pragma unroll
+        for (int u = 0; u < 8; ++u) x1[u] = __fmul_rn(__fmul_rn(x1[u], inv), g[u]);
+      }
+    }
+    if (p.rope.inv_freq) rotate_item(x0, x1, it, p.rope.half, p.rope.interleaved, cs + my_t * p.rope.half);
+    uint16_t* dst = is_q ? p.q.out + (t0 + my_t) * p.q.out_t + my_h * p.q.out_h
+                         : p.k.out + (t0 + my_t) * p.k.out_t + (my_h - p.Hq) * p.k.out_h;
+    if (it.c0 >= 0) *reinterpret_cast<uint4*>(dst + it.c0) = pack8<T>(x0);
+    if (it.c1 >= 0) *reinterpret_cast<uint4*>(dst + it.c1) = pack8<T>(x1);
+  }
+}
+
+Side side_of(const HeadRows& in, const HeadRows& out, const float* weight) {
+  return Side{static_cast<const uint16_t*>(in.data), static_cast<uint16_t*>(out.data), weight,
+              in.token_stride, in.head_stride, out.token_stride, out.head_stride};
+}
+
+}  // namespace
+
+csa2_status launch_head_norm(csa2_dtype dtype, const HeadRows& q, const float* q_weight,
+                             const HeadRows& q_out, const HeadRows& k, const float* k_weight,
+                             const HeadRows& k_out, int64_t T, int D, float eps,
+                             const int32_t* positions, const RopeArgs& rope, cudaStream_t stream) {
+  Params p = {};
+  p.q = side_of(q, q_out, q_weight);
+  p.k = side_of(k, k_out, k_weight);
+  p.positions = positions;
+  p.T = T;
+  p.Hq = q.heads;
+  p.H = q.heads + k.heads;
+  p.D = D;
+  p.eps = eps;
+  p.rope = rope;
+  p.items = items_of(D, rope.half);
+  p.lanes = 1;
+  while (p.lanes < p.items) p.lanes *= 2;
+  const int per_pass = kThreads / p.lanes;
+  const int sms = sm_count();
+  // as many tokens per CTA (up to 4, whose angles are one per thread at 64
+  // pairs) as still leave four CTAs per SM; with fewer tokens than that, a
+  // token's heads are cut over grid.y
+  p.tokens = 4;
+  while (p.tokens > 1 && T / p.tokens < 4 * sms) p.tokens /= 2;
+  const int64_t gx = (T + p.tokens - 1) / p.tokens;
+  const int passes = (p.tokens * p.H + per_pass - 1) / per_pass;
+  int ny = 1;
+  if (gx < 2 * sms) ny = static_cast<int>(std::min<int64_t>(passes, (2 * sms + gx - 1) / gx));
+  p.rows_cta = (passes + ny - 1) / ny * per_pass;
+  ny = (p.tokens * p.H + p.rows_cta - 1) / p.rows_cta;
+  if (gx > 0x7fffffffLL) return fail(CSA2_ERR_UNSUPPORTED, "csa2_qk_norm_rope: too many tokens");
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(gx), static_cast<unsigned>(ny));
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = static_cast<size_t>(p.tokens) * rope.half * sizeof(float2);
+  cfg.stream = stream;
+  cudaLaunchAttribute at[1] = {pdl_attribute()};
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  begin_launch(stream);
+  const cudaError_t e = dtype == CSA2_F16 ? cudaLaunchKernelEx(&cfg, head_norm_kernel<__half>, p)
+                                          : cudaLaunchKernelEx(&cfg, head_norm_kernel<__nv_bfloat16>, p);
+  note_launch(LK_OTHER, 1, stream);
+  if (e != cudaSuccess) {
+    cudaGetLastError();
+    return fail(CSA2_ERR_CUDA, "csa2_qk_norm_rope: launch failed: %s", cudaGetErrorString(e));
+  }
+  return check_launch("csa2_qk_norm_rope");
+}
+
+}  // namespace csa2

@@ -1,0 +1,120 @@
+// Device code shared by the paged attention kernels: warp-level matrix
+// instructions on 16-bit types, exact FP4 dequantisation, and which tokens a
+// tile of query rows sees.
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_fp8.h>
+
+#include "common.cuh"
+#include "paged.h"
+#include "rope.cuh"
+#include "sm100.cuh"
+
+namespace csa2 {
+namespace paged {
+
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
+
+__device__ __forceinline__ float exp2_approx(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+__device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t a) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(a));
+}
+__device__ __forceinline__ void ldsm4t(uint32_t (&r)[4], uint32_t a) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(a));
+}
+
+// c[16 x 8] += a[16 x 16] b[16 x 8], f32 accumulation
+template <class T>
+__device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1);
+template <>
+__device__ __forceinline__ void mma16816<__nv_bfloat16>(float (&c)[4], const uint32_t (&a)[4], uint32_t b0,
+                                                        uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+template <>
+__device__ __forceinline__ void mma16816<__half>(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+// E4M3 scale code as a bf16 pair (exact; the NaN code stays NaN)
+__device__ __forceinline__ uint32_t scale_pair(uint32_t code) {
+  const __half_raw h = __nv_cvt_fp8_to_halfraw(static_cast<__nv_fp8_storage_t>(code), __NV_E4M3);
+  const float f = __half2float(*reinterpret_cast<const __half*>(&h));
+  return pack_bf16x2(f, f);
+}
+__device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b) {
+  const __nv_bfloat162 r =
+      __hmul2(*reinterpret_cast<__nv_bfloat162*>(&a), *reinterpret_cast<__nv_bfloat162*>(&b));
+  return *reinterpret_cast<const uint32_t*>(&r);
+}
+// 8 E2M1 codes (one word) times a scale: 8 bf16.  A code's three magnitude bits
+// at the top of a bf16's exponent-and-mantissa boundary are the value times
+// 2^-126 (subnormals included), so one exact product restores it.
+__device__ __forceinline__ uint4 dequant8(uint32_t w, uint32_t scale2) {
+  uint32_t o[4];
+#pragma unroll
+  for (int u = 0; u < 4; ++u) {
+    const uint32_t b = (w >> (8 * u)) & 0xffu;
+    const uint32_t t = b | (b << 12);
+    const uint32_t v = ((t & 0x00070007u) << 6) | ((t & 0x00080008u) << 12);
+    o[u] = mul_bf16x2(mul_bf16x2(v, 0x7e807e80u), scale2);
+  }
+  return make_uint4(o[0], o[1], o[2], o[3]);
+}
+
+// Length of sequence b, clamped to the table's row; the error word notes one
+// outside it.
+__device__ __forceinline__ int length_of(const PagedView& kv, int b, bool report) {
+  const int n = __ldg(kv.lens + b);
+  if (n >= 0 && n <= kv.capacity) return n;
+  if (report) raise_dev_error(kv.err, DEVERR_BOUNDS);
+  return n < 0 ? 0 : static_cast<int>(kv.capacity);
+}
+
+// Channel offset of token j of sequence b (head 0), or -1 when its page lies
+// outside the pool.
+__device__ __forceinline__ int64_t token_row(const PagedView& kv, int b, int j) {
+  const int page = __ldg(kv.table + b * kv.table_stride + (j >> kv.page_shift));
+  if (page < 0 || page >= kv.n_pages) {
+    raise_dev_error(kv.err, DEVERR_BOUNDS);
+    return -1;
+  }
+  return kv.row(page, j & ((1 << kv.page_shift) - 1), 0);
+}
+
+// Tokens [0, sinks) and [lo, hi) in one run of `total` slots: what the rows at
+// positions pmin .. pmax see together.
+struct Seen {
+  int lo, ns, total;
+  __device__ __forceinline__ Seen(int pmin, int pmax, int window, int sinks) {
+    pmin = max(pmin, 0);
+    lo = window > 0 && pmin >= window ? pmin + 1 - window : 0;
+    ns = min(sinks, lo);
+    total = pmax < 0 ? 0 : ns + (pmax + 1 - lo);
+  }
+  __device__ __forceinline__ int token(int slot) const { return slot < ns ? slot : slot - ns + lo; }
+};
+// window = 0: no window.  p - j < window as an unsigned difference is safe for
+// every p >= j >= 0.
+__device__ __forceinline__ bool sees(int p, int j, int window, int sinks) {
+  return j <= p && (window <= 0 || p - j < window || j < sinks);
+}
+
+}  // namespace paged
+}  // namespace csa2

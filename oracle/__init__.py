@@ -9,3 +9,6 @@ from .csa2_oracle import (  # noqa: F401
     run_group, FP4_BLOCK, swa_attn, lse_merge, sparse_attn_swa, compress_hca, dense_attn,
     index_scores_fp4,
 )
+from .paged_oracle import (  # noqa: F401
+    rotate, head_norm, paged_rows, causal_attn,
+)
