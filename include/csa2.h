@@ -415,7 +415,9 @@ csa2_status csa2_paged_append(csa2_dtype dtype, const csa2_heads* k, const csa2_
  *   q    rows of the cache's 16-bit type (bf16 for FP4), heads a multiple of
  *        cache->heads
  *   out  [B, Hq, dim] dense      lse f32 [B, Hq] or NULL
- * Requires dim in {64, 128, 256, 512}, window >= 0, sinks >= 0.
+ * Requires dim in {64, 128, 256, 512}, window >= 0, sinks >= 0; an FP4 cache:
+ * strides in multiples of 64, scales 4-byte aligned and as csa2_fp4_pack writes
+ * them (codes 0x00 .. 0x7e).
  * workspace: csa2_paged_decode_attn_workspace(...) bytes (0: NULL allowed), on
  * the current device. */
 size_t csa2_paged_decode_attn_workspace(const csa2_paged_kv* cache, int Hq, int window, int sinks,
@@ -433,7 +435,7 @@ csa2_status csa2_paged_decode_attn(const csa2_heads* q, const csa2_paged_kv* cac
  * depend on the other sequences or on where the prompt was cut into chunks.
  *   q    rows of the cache's 16-bit type    cu_q int32 [B + 1], ascending, cu_q[B] <= T
  *   out [T, Hq, dim] dense        lse f32 [T, Hq] or NULL
- * Requires dim in {64, 128, 256, 512}.  A cu_q that descends or leaves [0, T]
+ * Requires dim in {64, 128, 256, 512} and an FP4 cache as there.  A cu_q that descends or leaves [0, T]
  * is recorded as CSA2_ERR_BOUNDS and its sequence skipped. */
 csa2_status csa2_paged_window_attn(const csa2_heads* q, const int32_t* cu_q, int64_t T,
                                    const csa2_paged_kv* cache, float scale, int window, int sinks,

@@ -57,6 +57,11 @@ struct PagedAttn {
 size_t paged_decode_workspace(const PagedAttn& a, int64_t max_len, int chunk);
 csa2_status launch_paged_decode(const PagedAttn& a, int64_t max_len, int chunk, void* ws,
                                 cudaStream_t stream);
+// The decode launch for rows of up to 256 channels (paged_decode.cu); the caller
+// joins the chunks.
+bool paged_decode_stream_applies(const PagedAttn& a);
+csa2_status launch_paged_decode_stream(const PagedAttn& a, int chunk, int chunks, float* part_o, float2* part_ml,
+                                       cudaStream_t stream);
 csa2_status launch_paged_window(const PagedAttn& a, const int32_t* cu_q, int64_t T, cudaStream_t stream);
 
 }  // namespace csa2

@@ -107,6 +107,10 @@ csa2_status attn_of(const char* fn, const csa2_heads* q, int64_t T, const csa2_p
   CSA2_TRY(view_of(fn, cache, &a->kv, max_len));
   REQUIRE(cache->dim == 64 || cache->dim == 128 || cache->dim == 256 || cache->dim == 512,
           "%s: width %d must be 64, 128, 256 or 512", fn, cache->dim);
+  REQUIRE(cache->fmt != CSA2_KV_FP4 || ((a->kv.head_stride | a->kv.token_stride | a->kv.page_stride) % 64 == 0 &&
+                                        ((reinterpret_cast<uintptr_t>(a->kv.k_scales) |
+                                          reinterpret_cast<uintptr_t>(a->kv.v_scales)) & 3u) == 0),
+          "%s: an FP4 cache needs strides in multiples of 64 and 4-byte aligned scales", fn);
   REQUIRE(window >= 0 && sinks >= 0, "%s: negative window or sinks", fn);
   HeadRows rows;
   REQUIRE(q != nullptr, "%s: q is null", fn);

@@ -399,8 +399,35 @@ Params params_of(const PagedAttn& a) {
   return p;
 }
 
+template <class T, int D>
+csa2_status combine(const Params& p, cudaStream_t stream) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(p.kv.B * static_cast<int64_t>(p.Hq)));
+  cfg.blockDim = dim3(128);
+  cfg.stream = stream;
+  cudaLaunchAttribute at[1] = {pdl_attribute()};
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  begin_launch(stream);
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, paged_combine_kernel<T, D>, p);
+  note_launch(LK_COMBINE, 1, stream);
+  if (e != cudaSuccess) {
+    cudaGetLastError();
+    return fail(CSA2_ERR_CUDA, "paged attention: launch failed: %s", cudaGetErrorString(e));
+  }
+  return check_launch("paged attention: combine");
+}
+
+csa2_status dispatch_combine(const PagedAttn& a, const Params& p, cudaStream_t stream) {
+#define CSA2_COMBINE(D_) \
+  if (a.D == D_) return a.fmt == CSA2_KV_F16 ? combine<__half, D_>(p, stream) : combine<__nv_bfloat16, D_>(p, stream);
+  CSA2_COMBINE(64) CSA2_COMBINE(128) CSA2_COMBINE(256) CSA2_COMBINE(512)
+#undef CSA2_COMBINE
+  return CSA2_ERR_UNSUPPORTED;
+}
+
 template <class T, int D, bool FP4>
-csa2_status run(const Params& p, dim3 grid, bool combine, cudaStream_t stream) {
+csa2_status run(const Params& p, dim3 grid, cudaStream_t stream) {
   using L = Lay<D>;
   static PerDevice<int> opted;
   opted.get(+[]() -> int {
@@ -416,16 +443,8 @@ csa2_status run(const Params& p, dim3 grid, bool combine, cudaStream_t stream) {
   cfg.attrs = at;
   cfg.numAttrs = 1;
   begin_launch(stream);
-  cudaError_t e = cudaLaunchKernelEx(&cfg, paged_attn_kernel<T, D, FP4>, p);
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, paged_attn_kernel<T, D, FP4>, p);
   note_launch(LK_ATTN, 1, stream);
-  if (e == cudaSuccess && combine) {
-    cfg.gridDim = dim3(static_cast<unsigned>(p.kv.B * static_cast<int64_t>(p.Hq)));
-    cfg.blockDim = dim3(128);
-    cfg.dynamicSmemBytes = 0;
-    begin_launch(stream);
-    e = cudaLaunchKernelEx(&cfg, paged_combine_kernel<T, D>, p);
-    note_launch(LK_COMBINE, 1, stream);
-  }
   if (e != cudaSuccess) {
     cudaGetLastError();
     return fail(CSA2_ERR_CUDA, "paged attention: launch failed: %s", cudaGetErrorString(e));
@@ -433,12 +452,12 @@ csa2_status run(const Params& p, dim3 grid, bool combine, cudaStream_t stream) {
   return check_launch("paged attention");
 }
 
-csa2_status dispatch(const PagedAttn& a, const Params& p, dim3 grid, bool combine, cudaStream_t stream) {
+csa2_status dispatch(const PagedAttn& a, const Params& p, dim3 grid, cudaStream_t stream) {
 #define CSA2_PAGED(D_)                                                                            \
   if (a.D == D_)                                                                                  \
-    return a.fmt == CSA2_KV_FP4   ? run<__nv_bfloat16, D_, true>(p, grid, combine, stream)        \
-           : a.fmt == CSA2_KV_F16 ? run<__half, D_, false>(p, grid, combine, stream)              \
-                                  : run<__nv_bfloat16, D_, false>(p, grid, combine, stream);
+    return a.fmt == CSA2_KV_FP4   ? run<__nv_bfloat16, D_, true>(p, grid, stream)        \
+           : a.fmt == CSA2_KV_F16 ? run<__half, D_, false>(p, grid, stream)              \
+                                  : run<__nv_bfloat16, D_, false>(p, grid, stream);
   CSA2_PAGED(64) CSA2_PAGED(128) CSA2_PAGED(256) CSA2_PAGED(512)
 #undef CSA2_PAGED
   return CSA2_ERR_UNSUPPORTED;
@@ -487,9 +506,14 @@ csa2_status launch_paged_decode(const PagedAttn& a, int64_t max_len, int chunk, 
     p.part_o = static_cast<float*>(ws);
     p.part_ml = reinterpret_cast<float2*>(p.part_o + static_cast<size_t>(a.kv.B) * a.Hq * s.chunks * a.D);
   }
-  const dim3 grid(static_cast<unsigned>(s.chunks), static_cast<unsigned>(a.kv.heads * p.row_tiles),
-                  static_cast<unsigned>(a.kv.B));
-  return dispatch(a, p, grid, s.chunks > 1, stream);
+  if (paged_decode_stream_applies(a)) {
+    CSA2_TRY(launch_paged_decode_stream(a, s.chunk, s.chunks, p.part_o, p.part_ml, stream));
+  } else {
+    const dim3 grid(static_cast<unsigned>(s.chunks), static_cast<unsigned>(a.kv.heads * p.row_tiles),
+                    static_cast<unsigned>(a.kv.B));
+    CSA2_TRY(dispatch(a, p, grid, stream));
+  }
+  return s.chunks > 1 ? dispatch_combine(a, p, stream) : CSA2_OK;
 }
 
 csa2_status launch_paged_window(const PagedAttn& a, const int32_t* cu_q, int64_t T, cudaStream_t stream) {
@@ -501,7 +525,7 @@ csa2_status launch_paged_window(const PagedAttn& a, const int32_t* cu_q, int64_t
   // tiles of 16 (token, head) rows: at most one more per sequence than all rows need
   const int64_t tiles = (T * a.G + 15) / 16 + a.kv.B;
   if (tiles > 0x7fffffffLL) return fail(CSA2_ERR_UNSUPPORTED, "csa2_paged_window_attn: too many rows");
-  return dispatch(a, p, dim3(static_cast<unsigned>(tiles), static_cast<unsigned>(a.kv.heads)), false, stream);
+  return dispatch(a, p, dim3(static_cast<unsigned>(tiles), static_cast<unsigned>(a.kv.heads)), stream);
 }
 
 }  // namespace csa2
