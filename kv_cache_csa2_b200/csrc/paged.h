@@ -62,6 +62,9 @@ csa2_status launch_paged_decode(const PagedAttn& a, int64_t max_len, int chunk, 
 bool paged_decode_stream_applies(const PagedAttn& a);
 csa2_status launch_paged_decode_stream(const PagedAttn& a, int chunk, int chunks, float* part_o, float2* part_ml,
                                        cudaStream_t stream);
+// Prompt attention on the tensor cores, rows of 64 or 128 channels (paged_window.cu).
+bool paged_window_tc_applies(const PagedAttn& a);
+csa2_status launch_paged_window_tc(const PagedAttn& a, const int32_t* cu_q, int64_t T, cudaStream_t stream);
 csa2_status launch_paged_window(const PagedAttn& a, const int32_t* cu_q, int64_t T, cudaStream_t stream);
 
 }  // namespace csa2

@@ -1,0 +1,631 @@
+// Attention of a prompt chunk over a paged cache on the 5th-generation tensor
+// cores, rows of 64 or 128 channels: causal, with a sliding window and sinks.
+//
+// The query rows of a cache head are (token, head) pairs, head fastest, so that
+// the heads that share keys fill a tile together.  A CTA takes two tiles of 128
+// rows against tiles of 128 keys (one pass, running maximum and sum):
+//   warps 0-3, 4-7  softmax of row tile 0 / 1: one thread per row reads its
+//                   scores from TMEM, writes the weights back there as 16-bit
+//                   pairs (the next product's left operand), and at the end
+//                   divides and stores the output
+//   warp 8          issues S = Q K^T (M=128, N=128, K=D) and O += P V (M=128,
+//                   N=D, K=keys), tile 0 and 1 in turn, so that one tile's
+//                   softmax runs under the other's products
+//   warps 9-11      gather the key and value rows by page into the 128-byte
+//                   swizzled layout (cp.async; FP4 rows are dequantised on the way)
+// The output stays in TMEM; it is rescaled only when a row's maximum has grown
+// by more than 2^8 since its last reference (its weights then exceed 1 by at
+// most that, which neither type nor the f32 sums mind).
+//
+// Key tiles are aligned to 128 tokens and a tile's columns that no row of the
+// tile sees are skipped in blocks of 32, both of which leave a row's sums alone:
+// its bits depend on its own tokens only.
+//
+// Bound: 4 D flops per (row, key) on the tensor cores against one exponential,
+// 16 of which an SM does per clock: at D = 128 both take 1024 clocks per pair of
+// 128 x 128 tiles.
+#include <algorithm>
+#include <type_traits>
+
+#include "launchers.h"
+#include "paged_attn.cuh"
+
+namespace csa2 {
+namespace {
+using namespace paged;
+using namespace sm100;
+using rope::Num;
+
+constexpr int kThreads = 384;
+constexpr int KT = 128;                                // keys per tile
+constexpr int RT = 128;                                // rows per row tile
+constexpr int kBits = 8;                               // slots of the presence words
+constexpr float kLazy = 8.0f;                          // log2 growth of a maximum that O tolerates
+
+template <int D, bool SHARED>
+struct Lay {
+  static constexpr int BLK = 128 * 128;                // 64 channels of 128 rows
+  static constexpr int TILE = D / 64 * BLK;
+  static constexpr int KST = SHARED ? 4 : D == 64 ? 3 : 2;
+  static constexpr int VST = SHARED ? 0 : D == 64 ? 3 : 2;
+  static constexpr int Q = 0;
+  static constexpr int K = Q + 2 * TILE;
+  static constexpr int V = K + KST * TILE;
+  static constexpr int BAR = V + VST * TILE;
+  static constexpr int NBAR = 2 * KST + 2 * VST + 2 + 2 + 2 + 1;
+  static constexpr int BITS = BAR + NBAR * 8;
+  static constexpr int MISC = BITS + kBits * 4 * 4;
+  static constexpr int BYTES = MISC + 16 + 1024;
+};
+
+struct Params {
+  const uint16_t* q;
+  int64_t q_token, q_head;
+  uint16_t* out;
+  float* lse;
+  const int32_t* cu_q;
+  int64_t T;
+  float scale2;                      // |scale| * log2(e), at least the smallest normal
+  uint32_t flip;                     // 0x80008000 for a negative scale: q's signs turn
+  int Hq, G, window, sinks;
+  PagedView kv;
+};
+
+__device__ __forceinline__ void mma_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc,
+                                       uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
+      "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]),
+      "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+      : "memory");
+}
+
+template <class T>
+__host__ __device__ constexpr uint32_t idesc_of(int M, int N, bool b_mn) {
+  return std::is_same<T, __half>::value ? idesc_f16_f32(M, N, false, b_mn) : idesc_bf16_f32(M, N, false, b_mn);
+}
+
+// Row tiles of a CTA: the sequence, its rows, and what they see.
+struct Work {
+  int b, base, n_rows;               // sequence, position of its first new token, rows of this CTA (<= 256)
+  int64_t q_row0, r0;                // first q row of the sequence, first (token, head) row of the CTA
+  int sink_tiles, first_tile, tiles; // key tiles: the sinks', then from first_tile on
+  int lo, ns, pmax;                  // tokens loaded: [0, ns) and [lo, pmax]
+};
+
+__device__ __forceinline__ int tile_start(const Work& w, int j) {
+  return (j < w.sink_tiles ? j : j - w.sink_tiles + w.first_tile) * KT;
+}
+
+// Columns of a key tile that row tile w sees, in blocks of 32: [c0, c1).
+struct RowTile {
+  int lo, ns, pmax;
+  __device__ __forceinline__ RowTile(const Work& k, int w, int G, int window, int sinks) {
+    const int rows = min(RT, k.n_rows - w * RT);
+    lo = ns = 0;
+    pmax = -1;
+    if (rows > 0) {
+      const int64_t r = k.r0 + w * RT;
+      const int pmin = k.base + static_cast<int>(r / G);
+      pmax = k.base + static_cast<int>((r + rows - 1) / G);
+      const Seen s(pmin, pmax, window, sinks);
+      lo = s.lo;
+      ns = s.ns;
+    }
+  }
+  __device__ __forceinline__ void range(int j0, int& c0, int& c1) const {
+    c0 = c1 = 0;
+    if (pmax < 0) return;
+    const int a = max(j0, lo), e = min(j0 + KT - 1, pmax);
+    if (a <= e) {
+      c0 = (a - j0) >> 5;
+      c1 = ((e - j0) >> 5) + 1;
+    }
+    if (j0 < ns) {
+      c0 = 0;
+      c1 = max(c1, ((min(ns, j0 + KT) - 1 - j0) >> 5) + 1);
+    }
+  }
+};
+
+// The CTA's tile of 256 rows: tile `index` counted from the last sequence's last
+// (a prompt's late tiles see most, so they start first).  Every warp scans for
+// itself, 32 sequences at a time.
+__device__ bool locate(const Params& p, int64_t index, Work& w) {
+  const int lane = threadIdx.x & 31;
+  auto tiles_of = [&](int s, int& c0, int& c1) -> int64_t {
+    if (s >= p.kv.B) return 0;
+    c0 = __ldg(p.cu_q + s);
+    c1 = __ldg(p.cu_q + s + 1);
+    if (c0 < 0 || c1 < c0 || c1 > p.T) {
+      if (threadIdx.x < 32) raise_dev_error(p.kv.err, DEVERR_BOUNDS);
+      return 0;
+    }
+    return (static_cast<int64_t>(c1 - c0) * p.G + 2 * RT - 1) / (2 * RT);
+  };
+  for (int s0 = (p.kv.B - 1) & ~31; s0 >= 0; s0 -= 32) {
+    int c0 = 0, c1 = 0;
+    const int64_t mine = tiles_of(s0 + lane, c0, c1);
+    int64_t upto = mine;                               // tiles of this sequence and the later ones of the block
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int64_t x = __shfl_down_sync(0xffffffffu, upto, o);
+      if (lane + o < 32) upto += x;
+    }
+    const uint32_t hit = __ballot_sync(0xffffffffu, index < upto && index >= upto - mine);
+    if (hit) {
+      const int src = __ffs(hit) - 1;
+      const int64_t from_end = index - (__shfl_sync(0xffffffffu, upto, src) - __shfl_sync(0xffffffffu, mine, src));
+      const int64_t tile = __shfl_sync(0xffffffffu, mine, src) - 1 - from_end;
+      c0 = __shfl_sync(0xffffffffu, c0, src);
+      c1 = __shfl_sync(0xffffffffu, c1, src);
+      w.b = s0 + src;
+      w.q_row0 = c0;
+      w.r0 = tile * 2 * RT;
+      w.n_rows = static_cast<int>(min(static_cast<int64_t>(2 * RT), static_cast<int64_t>(c1 - c0) * p.G - w.r0));
+      w.base = length_of(p.kv, w.b, threadIdx.x == 0) - (c1 - c0);
+      const int pmin = w.base + static_cast<int>(w.r0 / p.G);
+      w.pmax = w.base + static_cast<int>((w.r0 + w.n_rows - 1) / p.G);
+      const Seen s(pmin, w.pmax, p.window, p.sinks);
+      w.lo = s.lo;
+      w.ns = s.ns;
+      w.sink_tiles = (s.ns + KT - 1) / KT;
+      w.first_tile = max(s.lo / KT, w.sink_tiles);
+      w.tiles = s.total == 0 ? 0 : w.sink_tiles + max(0, w.pmax / KT + 1 - w.first_tile);
+      return true;
+    }
+    index -= __shfl_sync(0xffffffffu, upto, 0);
+  }
+  return false;
+}
+
+template <class T, int D, bool FP4, bool SHARED>
+__global__ void __launch_bounds__(kThreads, 1) paged_window_kernel(const Params p) {
+  using L = Lay<D, SHARED>;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint64_t* bar = reinterpret_cast<uint64_t*>(smem + L::BAR);
+  uint64_t* k_full = bar;
+  uint64_t* k_empty = k_full + L::KST;
+  uint64_t* v_full = SHARED ? k_full : k_empty + L::KST;
+  uint64_t* v_empty = SHARED ? k_empty : v_full + L::VST;
+  uint64_t* s_full = bar + 2 * L::KST + 2 * L::VST;    // [2]
+  uint64_t* p_full = s_full + 2;
+  uint64_t* pv_done = p_full + 2;
+  uint64_t* all_done = pv_done + 2;
+  constexpr int VS = SHARED ? L::KST : L::VST;
+  uint32_t* bits = reinterpret_cast<uint32_t*>(smem + L::BITS);       // [kBits][4]: tokens present
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + L::MISC);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + L::MISC + 4);
+  uint8_t* sK = smem + L::K;
+  uint8_t* sV = SHARED ? sK : smem + L::V;
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int kvh = blockIdx.y;
+  pdl_wait();
+  Work wk;
+  if (!locate(p, blockIdx.x, wk)) return;              // the same answer in every warp
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < L::KST; ++i) {
+      mbar_init(k_full + i, 4);                        // one arrival per 32 tokens
+      mbar_init(k_empty + i, 1);
+    }
+    for (int i = 0; i < L::VST; ++i) {
+      mbar_init(v_full + i, 4);
+      mbar_init(v_empty + i, 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(s_full + i, 1);
+      mbar_init(p_full + i, 4);
+      mbar_init(pv_done + i, 1);
+    }
+    mbar_init(all_done, 1);
+    *abort_flag = 0;
+    fence_mbar_init();
+  }
+  if (warp == 8) {
+    tmem_alloc(tmem_slot, 512);
+    tmem_relinquish();
+  }
+  // q rows (zero past the last) into K-major swizzled tiles
+  for (int i = threadIdx.x; i < 2 * RT * (D / 8); i += kThreads) {
+    const int r = i / (D / 8), c = i % (D / 8);
+    uint4 v = make_uint4(0, 0, 0, 0);
+    if (r < wk.n_rows) {
+      const int64_t rr = wk.r0 + r, t = rr / p.G;
+      v = __ldg(reinterpret_cast<const uint4*>(p.q + (wk.q_row0 + t) * p.q_token +
+                                               (kvh * p.G + (rr - t * p.G)) * p.q_head) + c);
+      v.x ^= p.flip;
+      v.y ^= p.flip;
+      v.z ^= p.flip;
+      v.w ^= p.flip;
+    }
+    *reinterpret_cast<uint4*>(smem + L::Q + (r / RT) * L::TILE + (c / 8) * L::BLK + sw128_offset(r % RT, c % 8)) = v;
+  }
+  fence_proxy_async_smem();
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  // registers: 168 x 384 threads at launch = 208 x 256 (softmax) + 88 x 128 (the rest)
+  if (warp >= 8)
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
+  else
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
+  constexpr uint32_t O_COL = 256;                      // S / P of tile w at 128 w, O at 256 + 128 w
+
+  if (warp >= 9) {
+    // ------------------------------------------------------------ loaders
+    // unit u = (key tile u / 4, its 32 tokens u % 4); the three warps in turn
+    const int units = 4 * wk.tiles;
+    auto row_of = [&](int u) -> int64_t {
+      if (u >= units) return -1;
+      const int j = tile_start(wk, u >> 2) + (u & 3) * 32 + lane;
+      if (j > wk.pmax || (j < wk.lo && j >= wk.ns)) return -1;
+      const int64_t r = token_row(p.kv, wk.b, j);
+      return r < 0 ? -1 : r + kvh * p.kv.head_stride;
+    };
+    auto lost_of = [&](int u, int64_t row) {           // wanted, but its page is outside the pool
+      const int j = tile_start(wk, u >> 2) + (u & 3) * 32 + lane;
+      return row < 0 && j <= wk.pmax && (j >= wk.lo || j < wk.ns);
+    };
+    constexpr int HALVES = SHARED ? 1 : 2;
+    constexpr int CH = FP4 ? D / 32 : D / 8;           // 16-byte pieces of a row
+    uint64_t* waiting = nullptr;                       // copies issued, not yet announced
+    int64_t row = row_of(warp - 9);
+    bool ok = true;
+    for (int u = warp - 9; u < units && ok; u += 3) {
+      const int tile = u >> 2, r0 = (u & 3) * 32;
+      const int64_t next = row_of(u + 3);
+      const uint32_t lost = __ballot_sync(0xffffffffu, lost_of(u, row));
+#pragma unroll
+      for (int half = 0; half < HALVES; ++half) {
+        const int ring = half ? VS : L::KST, st = tile % ring;
+        uint8_t* dst = (half ? sV : sK) + st * L::TILE;
+        const uint8_t* src = half ? p.kv.v : p.kv.k;
+        uint64_t* full = (half ? v_full : k_full) + st;
+        uint64_t* empty = (half ? v_empty : k_empty) + st;
+        const uint32_t parity = ((tile / ring) & 1) ^ 1;
+        if (!FP4) {
+          // do not hold back what has landed while the stage is still in use
+          if (waiting && !__all_sync(0xffffffffu, mbar_try_wait(empty, parity))) {
+            cp_async_wait<0>();
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(waiting);
+            waiting = nullptr;
+          }
+          ok = mbar_wait(empty, parity, abort_flag, p.kv.err);
+          ok = __all_sync(0xffffffffu, ok);
+          if (!ok) break;
+#pragma unroll 8
+          for (int i = 0; i < CH; ++i) {
+            const int piece = i * 32 + lane, r = piece / CH, c = piece % CH;
+            const int64_t at = __shfl_sync(0xffffffffu, row, r);
+            cp_async_16(dst + (c / 8) * L::BLK + sw128_offset(r0 + r, c % 8), src + (at < 0 ? 0 : at * 2 + c * 16),
+                        at < 0 ? 0u : 16u);
+          }
+          cp_async_commit();
+          if (half == 0 && lane == 0) bits[(tile % kBits) * 4 + (u & 3)] = ~lost;
+          if (waiting) {
+            cp_async_wait<1>();
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(waiting);
+          }
+          waiting = full;
+        } else {
+          const uint8_t* sc = half ? p.kv.v_scales : p.kv.k_scales;
+          uint4 w[CH];
+          uint32_t s2[CH];
+#pragma unroll
+          for (int i = 0; i < CH; ++i) {
+            const int piece = i * 32 + lane, r = piece / CH, c = piece % CH;
+            const int64_t at = __shfl_sync(0xffffffffu, row, r);
+            w[i] = make_uint4(0, 0, 0, 0);
+            s2[i] = 0;
+            if (at >= 0) {
+              w[i] = __ldg(reinterpret_cast<const uint4*>(src + at / 2) + c);
+              s2[i] = __ldg(reinterpret_cast<const uint16_t*>(sc + at / 16) + c);
+            }
+          }
+          ok = mbar_wait(empty, parity, abort_flag, p.kv.err);
+          ok = __all_sync(0xffffffffu, ok);
+          if (!ok) break;
+#pragma unroll
+          for (int i = 0; i < CH; ++i) {
+            const int piece = i * 32 + lane, r = r0 + piece / CH, c = (piece % CH) * 4;
+            const uint32_t lo = scale_pair(s2[i] & 255u), hi = scale_pair(s2[i] >> 8);
+            uint8_t* d = dst + (c / 8) * L::BLK;
+            *reinterpret_cast<uint4*>(d + sw128_offset(r, c % 8)) = dequant8(w[i].x, lo);
+            *reinterpret_cast<uint4*>(d + sw128_offset(r, c % 8 + 1)) = dequant8(w[i].y, lo);
+            *reinterpret_cast<uint4*>(d + sw128_offset(r, c % 8 + 2)) = dequant8(w[i].z, hi);
+            *reinterpret_cast<uint4*>(d + sw128_offset(r, c % 8 + 3)) = dequant8(w[i].w, hi);
+          }
+          if (half == 0 && lane == 0) bits[(tile % kBits) * 4 + (u & 3)] = ~lost;
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(full);
+        }
+      }
+      row = next;
+    }
+    if (!FP4) {
+      cp_async_wait<0>();
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (waiting && lane == 0) mbar_arrive(waiting);
+    }
+  } else if (warp == 8) {
+    // ------------------------------------------------------------ products
+    if (lane == 0) {
+      constexpr uint32_t idesc_s = idesc_of<T>(128, KT, false), idesc_o = idesc_of<T>(128, D, true);
+      const RowTile rt[2] = {RowTile(wk, 0, p.G, p.window, p.sinks), RowTile(wk, 1, p.G, p.window, p.sinks)};
+      const uint32_t q0 = smem_u32(smem + L::Q), k0 = smem_u32(sK), v0 = smem_u32(sV);
+      uint32_t turns[2] = {0, 0};                      // weights consumed per row tile
+      bool started[2] = {false, false};
+      int k_seen = -1, v_seen = -1;                    // last tile whose arrival was waited for
+      bool ok = true;
+      auto active = [&](int w, int j, int& c0, int& c1) {
+        rt[w].range(tile_start(wk, j), c0, c1);
+        return c0 < c1;
+      };
+      auto scores = [&](int w, int j) {
+        if (k_seen < j) {
+          ok = ok && mbar_wait(k_full + j % L::KST, (j / L::KST) & 1, abort_flag, p.kv.err);
+          k_seen = j;
+          tc_fence_after();
+        }
+        if (!ok) return;
+        const uint32_t a = q0 + w * L::TILE, bk = k0 + (j % L::KST) * L::TILE;
+#pragma unroll
+        for (int kk = 0; kk < D / 16; ++kk)
+          mma_bf16(tmem + w * 128, desc_kmajor_sw128(a + (kk >> 2) * L::BLK + (kk & 3) * 32),
+                   desc_kmajor_sw128(bk + (kk >> 2) * L::BLK + (kk & 3) * 32), idesc_s, kk != 0);
+        mma_commit(s_full + w);
+      };
+      int c0, c1;
+      if (wk.tiles > 0) {
+        for (int w = 0; w < 2; ++w)
+          if (active(w, 0, c0, c1)) scores(w, 0);
+        if (!SHARED && ok) mma_commit(k_empty);
+      }
+      for (int j = 0; j < wk.tiles && ok; ++j) {
+        for (int w = 0; w < 2 && ok; ++w) {
+          if (active(w, j, c0, c1)) {
+            ok = mbar_wait(p_full + w, turns[w] & 1, abort_flag, p.kv.err);
+            ++turns[w];
+            if (ok && v_seen < j) {
+              ok = mbar_wait(v_full + j % VS, (j / VS) & 1, abort_flag, p.kv.err);
+              v_seen = j;
+            }
+            if (!ok) break;
+            tc_fence_after();
+            const uint32_t bv = v0 + (j % VS) * L::TILE;
+            for (int kk = 2 * c0; kk < 2 * c1; ++kk) { // 16 keys per product
+              mma_ts(tmem + O_COL + w * 128, tmem + w * 128 + kk * 8,
+                     desc_mnmajor_sw128(bv + kk * 2048, L::BLK, 1024), idesc_o, started[w]);
+              started[w] = true;
+            }
+            mma_commit(pv_done + w);
+          }
+          if (w == 1) mma_commit(v_empty + j % VS);    // both tiles are past this one's values
+          if (j + 1 < wk.tiles && active(w, j + 1, c0, c1)) scores(w, j + 1);
+          if (!SHARED && w == 1 && j + 1 < wk.tiles && ok) mma_commit(k_empty + (j + 1) % L::KST);
+        }
+      }
+      // completes once every product issued above has, also when a wait gave up
+      mma_commit(all_done);
+    }
+    __syncwarp();
+  } else {
+    // ------------------------------------------------------------ softmax and output
+    const int w = warp >> 2, quad = warp & 3;
+    const int r = quad * 32 + lane;                    // row of the tile = TMEM lane
+    const uint32_t lane_off = static_cast<uint32_t>(quad * 32) << 16;
+    const uint32_t s_at = tmem + lane_off + w * 128, o_at = tmem + lane_off + O_COL + w * 128;
+    const RowTile rt(wk, w, p.G, p.window, p.sinks);
+    const bool live = w * RT + r < wk.n_rows;
+    const int64_t rr = wk.r0 + w * RT + r, tok = rr / p.G;
+    const int pos = live ? wk.base + static_cast<int>(tok) : -1;
+    // tokens [win, pos] and [0, sink_end) are visible
+    const int win = p.window > 0 ? pos - p.window + 1 : 0;
+    const int sink_end = min(p.sinks, pos + 1);
+    float m = -INFINITY, l0 = 0.0f, l1 = 0.0f;
+    uint32_t turn = 0;
+    bool ok = true;
+    for (int j = 0; j < wk.tiles && ok; ++j) {
+      const int j0 = tile_start(wk, j);
+      int c0, c1;
+      rt.range(j0, c0, c1);
+      if (c0 >= c1) continue;
+      ok = mbar_wait(s_full + w, turn & 1, abort_flag, p.kv.err);
+      ok = __all_sync(0xffffffffu, ok);
+      if (!ok) break;
+      tc_fence_after();
+      float s[4][32];
+#pragma unroll
+      for (int c = 0; c < 4; ++c)
+        if (c >= c0 && c < c1) tmem_ld32(s_at + c * 32, reinterpret_cast<uint32_t(&)[32]>(s[c]));
+      tmem_wait_ld();
+      float mx = -INFINITY;
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        if (c < c0 || c >= c1) continue;
+        const int ja = j0 + c * 32;
+        const uint32_t here = *reinterpret_cast<volatile uint32_t*>(bits + (j % kBits) * 4 + c);
+        const bool whole = ja >= win && ja + 31 <= pos && here == 0xffffffffu;
+        if (!__all_sync(0xffffffffu, whole)) {
+          // bit i: token ja + i visible
+          auto upto = [](int n) -> uint32_t { return n <= 0 ? 0u : n >= 32 ? 0xffffffffu : (1u << n) - 1u; };
+          const uint32_t vis = ((upto(pos + 1 - ja) & ~upto(win - ja)) | upto(sink_end - ja)) & here;
+#pragma unroll
+          for (int i = 0; i < 32; ++i) s[c][i] = (vis >> i) & 1u ? s[c][i] : -INFINITY;
+        }
+#pragma unroll
+        for (int i = 0; i < 32; ++i) mx = fmaxf(mx, s[c][i]);
+      }
+      mx *= p.scale2;
+      // keep the old reference while the maximum has not outgrown it
+      const bool grow = mx > m + kLazy || (m == -INFINITY && mx > -INFINITY);
+      const bool scale_o = grow && m > -INFINITY;
+      if (__any_sync(0xffffffffu, scale_o)) {
+        const float f = scale_o ? exp2_approx(m - mx) : 1.0f;
+        l0 *= f;
+        l1 *= f;
+        ok = mbar_wait(pv_done + w, (turn - 1) & 1, abort_flag, p.kv.err);   // turn > 0: m is finite
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+        tc_fence_after();
+#pragma unroll
+        for (int c = 0; c < D / 32; ++c) {
+          uint32_t v[32];
+          tmem_ld32(o_at + c * 32, v);
+          tmem_wait_ld();
+#pragma unroll
+          for (int i = 0; i < 32; ++i) v[i] = __float_as_uint(__uint_as_float(v[i]) * f);
+          tmem_st32(o_at + c * 32, v);
+        }
+      }
+      if (grow) m = mx;
+      const float ref = m == -INFINITY ? 0.0f : m;
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        if (c < c0 || c >= c1) continue;
+        uint32_t pk[16];
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+          const float e0 = exp2_approx(fmaf(s[c][2 * i], p.scale2, -ref));
+          const float e1 = exp2_approx(fmaf(s[c][2 * i + 1], p.scale2, -ref));
+          l0 += e0;
+          l1 += e1;
+          pk[i] = Num<T>::down(e0, e1);
+        }
+        tmem_st16(s_at + c * 16, pk);
+      }
+      tmem_wait_st();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(p_full + w);
+      ++turn;
+    }
+    if (turn > 0 && ok) {
+      ok = mbar_wait(pv_done + w, (turn - 1) & 1, abort_flag, p.kv.err);
+      ok = __all_sync(0xffffffffu, ok);
+      tc_fence_after();
+    }
+    if (ok) {
+      const float l = l0 + l1;
+      const float inv = l > 0.0f ? 1.0f / l : (l == 0.0f ? 0.0f : l);
+      const int64_t at = (wk.q_row0 + tok) * p.Hq + kvh * p.G + (rr - tok * p.G);
+#pragma unroll
+      for (int c = 0; c < D / 32; ++c) {
+        uint32_t v[32];
+        if (turn > 0) {
+          tmem_ld32(o_at + c * 32, v);
+          tmem_wait_ld();
+        } else {
+#pragma unroll
+          for (int i = 0; i < 32; ++i) v[i] = 0;
+        }
+        if (live) {
+          uint4* dst = reinterpret_cast<uint4*>(p.out + at * D + c * 32);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            uint32_t x[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              x[e] = Num<T>::down(__uint_as_float(v[8 * i + 2 * e]) * inv, __uint_as_float(v[8 * i + 2 * e + 1]) * inv);
+            dst[i] = make_uint4(x[0], x[1], x[2], x[3]);
+          }
+        }
+      }
+      if (live && p.lse) p.lse[at] = l == 0.0f ? -INFINITY : (m + log2f(l)) * kLn2;
+    }
+  }
+  // every product has completed before TMEM and shared memory go
+  volatile int never = 0;                              // also when a wait gave up: the products still end
+  mbar_wait(all_done, 0, &never, p.kv.err);
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 8) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+template <class T, int D, bool FP4, bool SHARED>
+csa2_status run(const Params& p, dim3 grid, cudaStream_t stream) {
+  using L = Lay<D, SHARED>;
+  static PerDevice<int> opted;
+  opted.get(+[]() -> int {
+    cudaFuncSetAttribute(paged_window_kernel<T, D, FP4, SHARED>, cudaFuncAttributeMaxDynamicSharedMemorySize, L::BYTES);
+    return 1;
+  });
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = L::BYTES;
+  cfg.stream = stream;
+  cudaLaunchAttribute at[1] = {pdl_attribute()};
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  begin_launch(stream);
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, paged_window_kernel<T, D, FP4, SHARED>, p);
+  note_launch(LK_ATTN, 1, stream);
+  if (e != cudaSuccess) {
+    cudaGetLastError();
+    return fail(CSA2_ERR_CUDA, "csa2_paged_window_attn: launch failed: %s", cudaGetErrorString(e));
+  }
+  return check_launch("csa2_paged_window_attn");
+}
+
+}  // namespace
+
+bool paged_window_tc_applies(const PagedAttn& a) { return a.D == 64 || a.D == 128; }
+
+csa2_status launch_paged_window_tc(const PagedAttn& a, const int32_t* cu_q, int64_t T, cudaStream_t stream) {
+  Params p = {};
+  p.q = static_cast<const uint16_t*>(a.q);
+  p.q_token = a.q_token;
+  p.q_head = a.q_head;
+  p.out = static_cast<uint16_t*>(a.out);
+  p.lse = a.lse;
+  p.cu_q = cu_q;
+  p.T = T;
+  const float s = a.scale * kLog2e;
+  p.flip = s < 0.0f ? 0x80008000u : 0u;
+  p.scale2 = std::max(s < 0.0f ? -s : s, 1.1754944e-38f);
+  p.Hq = a.Hq;
+  p.G = a.G;
+  p.window = a.window;
+  p.sinks = a.sinks;
+  p.kv = a.kv;
+  // at most one tile more per sequence than all rows need
+  const int64_t tiles = (T * a.G + 2 * RT - 1) / (2 * RT) + a.kv.B;
+  if (tiles > 0x7fffffffLL) return fail(CSA2_ERR_UNSUPPORTED, "csa2_paged_window_attn: too many rows");
+  const dim3 grid(static_cast<unsigned>(tiles), static_cast<unsigned>(a.kv.heads));
+  const bool sh = a.kv.v == a.kv.k;
+#define CSA2_WIN_T(T_, D_, F_) (sh ? run<T_, D_, F_, true>(p, grid, stream) : run<T_, D_, F_, false>(p, grid, stream))
+#define CSA2_WIN(D_)                                                                       \
+  if (a.D == D_)                                                                           \
+    return a.fmt == CSA2_KV_FP4   ? CSA2_WIN_T(__nv_bfloat16, D_, true)                    \
+           : a.fmt == CSA2_KV_F16 ? CSA2_WIN_T(__half, D_, false)                          \
+                                  : CSA2_WIN_T(__nv_bfloat16, D_, false);
+  CSA2_WIN(64) CSA2_WIN(128)
+#undef CSA2_WIN
+#undef CSA2_WIN_T
+  return CSA2_ERR_UNSUPPORTED;
+}
+
+}  // namespace csa2
