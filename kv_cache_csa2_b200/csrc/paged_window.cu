@@ -257,179 +257,179 @@ __global__ void __launch_bounds__(kThreads, 1) paged_window_kernel(const Params 
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
-  // registers: 168 x 384 threads at launch = 208 x 256 (softmax) + 88 x 128 (the rest)
-  if (warp >= 8)
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
-  else
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
   constexpr uint32_t O_COL = 256;                      // S / P of tile w at 128 w, O at 256 + 128 w
 
-  if (warp >= 9) {
-    // ------------------------------------------------------------ loaders
-    // unit u = (key tile u / 4, its 32 tokens u % 4); the three warps in turn
-    const int units = 4 * wk.tiles;
-    auto row_of = [&](int u) -> int64_t {
-      if (u >= units) return -1;
-      const int j = tile_start(wk, u >> 2) + (u & 3) * 32 + lane;
-      if (j > wk.pmax || (j < wk.lo && j >= wk.ns)) return -1;
-      const int64_t r = token_row(p.kv, wk.b, j);
-      return r < 0 ? -1 : r + kvh * p.kv.head_stride;
-    };
-    auto lost_of = [&](int u, int64_t row) {           // wanted, but its page is outside the pool
-      const int j = tile_start(wk, u >> 2) + (u & 3) * 32 + lane;
-      return row < 0 && j <= wk.pmax && (j >= wk.lo || j < wk.ns);
-    };
-    constexpr int HALVES = SHARED ? 1 : 2;
-    constexpr int CH = FP4 ? D / 32 : D / 8;           // 16-byte pieces of a row
-    uint64_t* waiting = nullptr;                       // copies issued, not yet announced
-    int64_t row = row_of(warp - 9);
-    bool ok = true;
-    for (int u = warp - 9; u < units && ok; u += 3) {
-      const int tile = u >> 2, r0 = (u & 3) * 32;
-      const int64_t next = row_of(u + 3);
-      const uint32_t lost = __ballot_sync(0xffffffffu, lost_of(u, row));
-#pragma unroll
-      for (int half = 0; half < HALVES; ++half) {
-        const int ring = half ? VS : L::KST, st = tile % ring;
-        uint8_t* dst = (half ? sV : sK) + st * L::TILE;
-        const uint8_t* src = half ? p.kv.v : p.kv.k;
-        uint64_t* full = (half ? v_full : k_full) + st;
-        uint64_t* empty = (half ? v_empty : k_empty) + st;
-        const uint32_t parity = ((tile / ring) & 1) ^ 1;
-        if (!FP4) {
-          // do not hold back what has landed while the stage is still in use
-          if (waiting && !__all_sync(0xffffffffu, mbar_try_wait(empty, parity))) {
-            cp_async_wait<0>();
-            fence_proxy_async_smem();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(waiting);
-            waiting = nullptr;
-          }
-          ok = mbar_wait(empty, parity, abort_flag, p.kv.err);
-          ok = __all_sync(0xffffffffu, ok);
-          if (!ok) break;
-#pragma unroll 8
-          for (int i = 0; i < CH; ++i) {
-            const int piece = i * 32 + lane, r = piece / CH, c = piece % CH;
-            const int64_t at = __shfl_sync(0xffffffffu, row, r);
-            cp_async_16(dst + (c / 8) * L::BLK + sw128_offset(r0 + r, c % 8), src + (at < 0 ? 0 : at * 2 + c * 16),
-                        at < 0 ? 0u : 16u);
-          }
-          cp_async_commit();
-          if (half == 0 && lane == 0) bits[(tile % kBits) * 4 + (u & 3)] = ~lost;
-          if (waiting) {
-            cp_async_wait<1>();
-            fence_proxy_async_smem();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(waiting);
-          }
-          waiting = full;
-        } else {
-          const uint8_t* sc = half ? p.kv.v_scales : p.kv.k_scales;
-          uint4 w[CH];
-          uint32_t s2[CH];
-#pragma unroll
-          for (int i = 0; i < CH; ++i) {
-            const int piece = i * 32 + lane, r = piece / CH, c = piece % CH;
-            const int64_t at = __shfl_sync(0xffffffffu, row, r);
-            w[i] = make_uint4(0, 0, 0, 0);
-            s2[i] = 0;
-            if (at >= 0) {
-              w[i] = __ldg(reinterpret_cast<const uint4*>(src + at / 2) + c);
-              s2[i] = __ldg(reinterpret_cast<const uint16_t*>(sc + at / 16) + c);
-            }
-          }
-          ok = mbar_wait(empty, parity, abort_flag, p.kv.err);
-          ok = __all_sync(0xffffffffu, ok);
-          if (!ok) break;
-#pragma unroll
-          for (int i = 0; i < CH; ++i) {
-            const int piece = i * 32 + lane, r = r0 + piece / CH, c = (piece % CH) * 4;
-            const uint32_t lo = scale_pair(s2[i] & 255u), hi = scale_pair(s2[i] >> 8);
-            uint8_t* d = dst + (c / 8) * L::BLK;
-            *reinterpret_cast<uint4*>(d + sw128_offset(r, c % 8)) = dequant8(w[i].x, lo);
-            *reinterpret_cast<uint4*>(d + sw128_offset(r, c % 8 + 1)) = dequant8(w[i].y, lo);
-            *reinterpret_cast<uint4*>(d + sw128_offset(r, c % 8 + 2)) = dequant8(w[i].z, hi);
-            *reinterpret_cast<uint4*>(d + sw128_offset(r, c % 8 + 3)) = dequant8(w[i].w, hi);
-          }
-          if (half == 0 && lane == 0) bits[(tile % kBits) * 4 + (u & 3)] = ~lost;
-          fence_proxy_async_smem();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(full);
-        }
-      }
-      row = next;
-    }
-    if (!FP4) {
-      cp_async_wait<0>();
-      fence_proxy_async_smem();
-      __syncwarp();
-      if (waiting && lane == 0) mbar_arrive(waiting);
-    }
-  } else if (warp == 8) {
-    // ------------------------------------------------------------ products
-    if (lane == 0) {
-      constexpr uint32_t idesc_s = idesc_of<T>(128, KT, false), idesc_o = idesc_of<T>(128, D, true);
-      const RowTile rt[2] = {RowTile(wk, 0, p.G, p.window, p.sinks), RowTile(wk, 1, p.G, p.window, p.sinks)};
-      const uint32_t q0 = smem_u32(smem + L::Q), k0 = smem_u32(sK), v0 = smem_u32(sV);
-      uint32_t turns[2] = {0, 0};                      // weights consumed per row tile
-      bool started[2] = {false, false};
-      int k_seen = -1, v_seen = -1;                    // last tile whose arrival was waited for
+  // registers: 168 x 384 threads at launch = 208 x 256 (softmax) + 88 x 128 (the rest)
+  if (warp >= 8) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
+    if (warp > 8) {
+      // ------------------------------------------------------------ loaders
+      // unit u = (key tile u / 4, its 32 tokens u % 4); the three warps in turn
+      const int units = 4 * wk.tiles;
+      auto row_of = [&](int u) -> int64_t {
+        if (u >= units) return -1;
+        const int j = tile_start(wk, u >> 2) + (u & 3) * 32 + lane;
+        if (j > wk.pmax || (j < wk.lo && j >= wk.ns)) return -1;
+        const int64_t r = token_row(p.kv, wk.b, j);
+        return r < 0 ? -1 : r + kvh * p.kv.head_stride;
+      };
+      auto lost_of = [&](int u, int64_t row) {           // wanted, but its page is outside the pool
+        const int j = tile_start(wk, u >> 2) + (u & 3) * 32 + lane;
+        return row < 0 && j <= wk.pmax && (j >= wk.lo || j < wk.ns);
+      };
+      constexpr int HALVES = SHARED ? 1 : 2;
+      constexpr int CH = FP4 ? D / 32 : D / 8;           // 16-byte pieces of a row
+      uint64_t* waiting = nullptr;                       // copies issued, not yet announced
+      int64_t row = row_of(warp - 9);
       bool ok = true;
-      auto active = [&](int w, int j, int& c0, int& c1) {
-        rt[w].range(tile_start(wk, j), c0, c1);
-        return c0 < c1;
-      };
-      auto scores = [&](int w, int j) {
-        if (k_seen < j) {
-          ok = ok && mbar_wait(k_full + j % L::KST, (j / L::KST) & 1, abort_flag, p.kv.err);
-          k_seen = j;
-          tc_fence_after();
-        }
-        if (!ok) return;
-        const uint32_t a = q0 + w * L::TILE, bk = k0 + (j % L::KST) * L::TILE;
+      for (int u = warp - 9; u < units && ok; u += 3) {
+        const int tile = u >> 2, r0 = (u & 3) * 32;
+        const int64_t next = row_of(u + 3);
+        const uint32_t lost = __ballot_sync(0xffffffffu, lost_of(u, row));
 #pragma unroll
-        for (int kk = 0; kk < D / 16; ++kk)
-          mma_bf16(tmem + w * 128, desc_kmajor_sw128(a + (kk >> 2) * L::BLK + (kk & 3) * 32),
-                   desc_kmajor_sw128(bk + (kk >> 2) * L::BLK + (kk & 3) * 32), idesc_s, kk != 0);
-        mma_commit(s_full + w);
-      };
-      int c0, c1;
-      if (wk.tiles > 0) {
-        for (int w = 0; w < 2; ++w)
-          if (active(w, 0, c0, c1)) scores(w, 0);
-        if (!SHARED && ok) mma_commit(k_empty);
-      }
-      for (int j = 0; j < wk.tiles && ok; ++j) {
-        for (int w = 0; w < 2 && ok; ++w) {
-          if (active(w, j, c0, c1)) {
-            ok = mbar_wait(p_full + w, turns[w] & 1, abort_flag, p.kv.err);
-            ++turns[w];
-            if (ok && v_seen < j) {
-              ok = mbar_wait(v_full + j % VS, (j / VS) & 1, abort_flag, p.kv.err);
-              v_seen = j;
+        for (int half = 0; half < HALVES; ++half) {
+          const int ring = half ? VS : L::KST, st = tile % ring;
+          uint8_t* dst = (half ? sV : sK) + st * L::TILE;
+          const uint8_t* src = half ? p.kv.v : p.kv.k;
+          uint64_t* full = (half ? v_full : k_full) + st;
+          uint64_t* empty = (half ? v_empty : k_empty) + st;
+          const uint32_t parity = ((tile / ring) & 1) ^ 1;
+          if (!FP4) {
+            // do not hold back what has landed while the stage is still in use
+            if (waiting && !__all_sync(0xffffffffu, mbar_try_wait(empty, parity))) {
+              cp_async_wait<0>();
+              fence_proxy_async_smem();
+              __syncwarp();
+              if (lane == 0) mbar_arrive(waiting);
+              waiting = nullptr;
             }
+            ok = mbar_wait(empty, parity, abort_flag, p.kv.err);
+            ok = __all_sync(0xffffffffu, ok);
             if (!ok) break;
-            tc_fence_after();
-            const uint32_t bv = v0 + (j % VS) * L::TILE;
-            for (int kk = 2 * c0; kk < 2 * c1; ++kk) { // 16 keys per product
-              mma_ts(tmem + O_COL + w * 128, tmem + w * 128 + kk * 8,
-                     desc_mnmajor_sw128(bv + kk * 2048, L::BLK, 1024), idesc_o, started[w]);
-              started[w] = true;
+#pragma unroll 8
+            for (int i = 0; i < CH; ++i) {
+              const int piece = i * 32 + lane, r = piece / CH, c = piece % CH;
+              const int64_t at = __shfl_sync(0xffffffffu, row, r);
+              cp_async_16(dst + (c / 8) * L::BLK + sw128_offset(r0 + r, c % 8), src + (at < 0 ? 0 : at * 2 + c * 16),
+                          at < 0 ? 0u : 16u);
             }
-            mma_commit(pv_done + w);
+            cp_async_commit();
+            if (half == 0 && lane == 0) bits[(tile % kBits) * 4 + (u & 3)] = ~lost;
+            if (waiting) {
+              cp_async_wait<1>();
+              fence_proxy_async_smem();
+              __syncwarp();
+              if (lane == 0) mbar_arrive(waiting);
+            }
+            waiting = full;
+          } else {
+            const uint8_t* sc = half ? p.kv.v_scales : p.kv.k_scales;
+            uint4 w[CH];
+            uint32_t s2[CH];
+#pragma unroll
+            for (int i = 0; i < CH; ++i) {
+              const int piece = i * 32 + lane, r = piece / CH, c = piece % CH;
+              const int64_t at = __shfl_sync(0xffffffffu, row, r);
+              w[i] = make_uint4(0, 0, 0, 0);
+              s2[i] = 0;
+              if (at >= 0) {
+                w[i] = __ldg(reinterpret_cast<const uint4*>(src + at / 2) + c);
+                s2[i] = __ldg(reinterpret_cast<const uint16_t*>(sc + at / 16) + c);
+              }
+            }
+            ok = mbar_wait(empty, parity, abort_flag, p.kv.err);
+            ok = __all_sync(0xffffffffu, ok);
+            if (!ok) break;
+#pragma unroll
+            for (int i = 0; i < CH; ++i) {
+              const int piece = i * 32 + lane, r = r0 + piece / CH, c = (piece % CH) * 4;
+              const uint32_t lo = scale_pair(s2[i] & 255u), hi = scale_pair(s2[i] >> 8);
+              uint8_t* d = dst + (c / 8) * L::BLK;
+              *reinterpret_cast<uint4*>(d + sw128_offset(r, c % 8)) = dequant8(w[i].x, lo);
+              *reinterpret_cast<uint4*>(d + sw128_offset(r, c % 8 + 1)) = dequant8(w[i].y, lo);
+              *reinterpret_cast<uint4*>(d + sw128_offset(r, c % 8 + 2)) = dequant8(w[i].z, hi);
+              *reinterpret_cast<uint4*>(d + sw128_offset(r, c % 8 + 3)) = dequant8(w[i].w, hi);
+            }
+            if (half == 0 && lane == 0) bits[(tile % kBits) * 4 + (u & 3)] = ~lost;
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(full);
           }
-          if (w == 1) mma_commit(v_empty + j % VS);    // both tiles are past this one's values
-          if (j + 1 < wk.tiles && active(w, j + 1, c0, c1)) scores(w, j + 1);
-          if (!SHARED && w == 1 && j + 1 < wk.tiles && ok) mma_commit(k_empty + (j + 1) % L::KST);
         }
+        row = next;
       }
-      // completes once every product issued above has, also when a wait gave up
-      mma_commit(all_done);
+      if (!FP4) {
+        cp_async_wait<0>();
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (waiting && lane == 0) mbar_arrive(waiting);
+      }
+    } else {
+      // ------------------------------------------------------------ products
+      if (lane == 0) {
+        constexpr uint32_t idesc_s = idesc_of<T>(128, KT, false), idesc_o = idesc_of<T>(128, D, true);
+        const RowTile rt[2] = {RowTile(wk, 0, p.G, p.window, p.sinks), RowTile(wk, 1, p.G, p.window, p.sinks)};
+        const uint32_t q0 = smem_u32(smem + L::Q), k0 = smem_u32(sK), v0 = smem_u32(sV);
+        uint32_t turns[2] = {0, 0};                      // weights consumed per row tile
+        bool started[2] = {false, false};
+        int k_seen = -1, v_seen = -1;                    // last tile whose arrival was waited for
+        bool ok = true;
+        auto active = [&](int w, int j, int& c0, int& c1) {
+          rt[w].range(tile_start(wk, j), c0, c1);
+          return c0 < c1;
+        };
+        auto scores = [&](int w, int j) {
+          if (k_seen < j) {
+            ok = ok && mbar_wait(k_full + j % L::KST, (j / L::KST) & 1, abort_flag, p.kv.err);
+            k_seen = j;
+            tc_fence_after();
+          }
+          if (!ok) return;
+          const uint32_t a = q0 + w * L::TILE, bk = k0 + (j % L::KST) * L::TILE;
+#pragma unroll
+          for (int kk = 0; kk < D / 16; ++kk)
+            mma_bf16(tmem + w * 128, desc_kmajor_sw128(a + (kk >> 2) * L::BLK + (kk & 3) * 32),
+                     desc_kmajor_sw128(bk + (kk >> 2) * L::BLK + (kk & 3) * 32), idesc_s, kk != 0);
+          mma_commit(s_full + w);
+        };
+        int c0, c1;
+        if (wk.tiles > 0) {
+          for (int w = 0; w < 2; ++w)
+            if (active(w, 0, c0, c1)) scores(w, 0);
+          if (!SHARED && ok) mma_commit(k_empty);
+        }
+        for (int j = 0; j < wk.tiles && ok; ++j) {
+          for (int w = 0; w < 2 && ok; ++w) {
+            if (active(w, j, c0, c1)) {
+              ok = mbar_wait(p_full + w, turns[w] & 1, abort_flag, p.kv.err);
+              ++turns[w];
+              if (ok && v_seen < j) {
+                ok = mbar_wait(v_full + j % VS, (j / VS) & 1, abort_flag, p.kv.err);
+                v_seen = j;
+              }
+              if (!ok) break;
+              tc_fence_after();
+              const uint32_t bv = v0 + (j % VS) * L::TILE;
+              for (int kk = 2 * c0; kk < 2 * c1; ++kk) { // 16 keys per product
+                mma_ts(tmem + O_COL + w * 128, tmem + w * 128 + kk * 8,
+                       desc_mnmajor_sw128(bv + kk * 2048, L::BLK, 1024), idesc_o, started[w]);
+                started[w] = true;
+              }
+              mma_commit(pv_done + w);
+            }
+            if (w == 1) mma_commit(v_empty + j % VS);    // both tiles are past this one's values
+            if (j + 1 < wk.tiles && active(w, j + 1, c0, c1)) scores(w, j + 1);
+            if (!SHARED && w == 1 && j + 1 < wk.tiles && ok) mma_commit(k_empty + (j + 1) % L::KST);
+          }
+        }
+        // completes once every product issued above has, also when a wait gave up
+        mma_commit(all_done);
+      }
+      __syncwarp();
     }
-    __syncwarp();
   } else {
     // ------------------------------------------------------------ softmax and output
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
     const int w = warp >> 2, quad = warp & 3;
     const int r = quad * 32 + lane;                    // row of the tile = TMEM lane
     const uint32_t lane_off = static_cast<uint32_t>(quad * 32) << 16;
