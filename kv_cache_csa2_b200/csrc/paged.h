@@ -2,6 +2,8 @@
 // validated by the C-ABI layer (paged_api.cu).
 #pragma once
 
+#include <cuda.h>
+
 #include "common.cuh"
 #include "rope.cuh"
 
@@ -62,6 +64,11 @@ csa2_status launch_paged_decode(const PagedAttn& a, int64_t max_len, int chunk, 
 bool paged_decode_stream_applies(const PagedAttn& a);
 csa2_status launch_paged_decode_stream(const PagedAttn& a, int chunk, int chunks, float* part_o, float2* part_ml,
                                        cudaStream_t stream);
+// Tensor map of 16-bit cache rows as [page][slot][head][channel] with the 128-byte
+// swizzle: a box is 64 channels of box_rows slots of one head and page.
+csa2_status make_tensor_map_paged(CUtensorMap* map, const void* base, int dim, int heads, int64_t head_stride,
+                                  int page_size, int64_t token_stride, int64_t n_pages, int64_t page_stride,
+                                  int box_rows);
 // Prompt attention on the tensor cores, rows of 64 or 128 channels (paged_window.cu).
 bool paged_window_tc_applies(const PagedAttn& a);
 csa2_status launch_paged_window_tc(const PagedAttn& a, const int32_t* cu_q, int64_t T, cudaStream_t stream);

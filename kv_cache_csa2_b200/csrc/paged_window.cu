@@ -11,8 +11,12 @@
 //   warp 8          issues S = Q K^T (M=128, N=128, K=D) and O += P V (M=128,
 //                   N=D, K=keys), tile 0 and 1 in turn, so that one tile's
 //                   softmax runs under the other's products
-//   warps 9-11      gather the key and value rows by page into the 128-byte
-//                   swizzled layout (cp.async; FP4 rows are dequantised on the way)
+//   warps 9-11      bring the key and value rows into the 128-byte swizzled layout,
+//                   32 tokens at a time: TMA boxes of a page when all 32 are wanted
+//                   and pages hold at least 8 tokens, else cp.async row by row with
+//                   zeros for the rest (what lies past a sequence's end may be
+//                   anything, and a weight of 0 does not silence a NaN); FP4 rows are
+//                   dequantised on the way
 // The output stays in TMEM; it is rescaled only when a row's maximum has grown
 // by more than 2^8 since its last reference (its weights then exceed 1 by at
 // most that, which neither type nor the f32 sums mind).
@@ -68,8 +72,19 @@ struct Params {
   float scale2;                      // |scale| * log2(e), at least the smallest normal
   uint32_t flip;                     // 0x80008000 for a negative scale: q's signs turn
   int Hq, G, window, sinks;
+  int box;                           // rows of a TMA box (0: none)
   PagedView kv;
 };
+
+// One box of the cache's tensor map: channels c .. c + 63 of box rows from `slot` on.
+__device__ __forceinline__ void tma_load_page(void* dst, const CUtensorMap* map, uint64_t* bar, int c, int head, int slot,
+                                              int page) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%3, %4, %5, %6}], [%2];" ::"r"(smem_u32(dst)),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(c), "r"(head), "r"(slot), "r"(page)
+      : "memory");
+}
 
 __device__ __forceinline__ void mma_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc,
                                        uint32_t accumulate) {
@@ -189,7 +204,8 @@ __device__ bool locate(const Params& p, int64_t index, Work& w) {
 }
 
 template <class T, int D, bool FP4, bool SHARED>
-__global__ void __launch_bounds__(kThreads, 1) paged_window_kernel(const Params p) {
+__global__ void __launch_bounds__(kThreads, 1) paged_window_kernel(const Params p, const __grid_constant__ CUtensorMap k_map,
+                                                               const __grid_constant__ CUtensorMap v_map) {
   using L = Lay<D, SHARED>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -286,6 +302,16 @@ __global__ void __launch_bounds__(kThreads, 1) paged_window_kernel(const Params 
         const int tile = u >> 2, r0 = (u & 3) * 32;
         const int64_t next = row_of(u + 3);
         const uint32_t lost = __ballot_sync(0xffffffffu, lost_of(u, row));
+        // a whole unit: boxes of p.box rows and 64 channels, one per lane
+        const bool whole = !FP4 && p.box > 0 && __all_sync(0xffffffffu, row >= 0);
+        constexpr int BLKS = D / 64;
+        const int boxes = whole ? 32 / p.box * BLKS : 0;
+        int box_page = 0, box_slot = 0;
+        if (lane < boxes) {
+          const int j = tile_start(wk, tile) + r0 + lane / BLKS * p.box;
+          box_page = __ldg(p.kv.table + wk.b * p.kv.table_stride + (j >> p.kv.page_shift));
+          box_slot = j & ((1 << p.kv.page_shift) - 1);
+        }
 #pragma unroll
         for (int half = 0; half < HALVES; ++half) {
           const int ring = half ? VS : L::KST, st = tile % ring;
@@ -306,6 +332,17 @@ __global__ void __launch_bounds__(kThreads, 1) paged_window_kernel(const Params 
             ok = mbar_wait(empty, parity, abort_flag, p.kv.err);
             ok = __all_sync(0xffffffffu, ok);
             if (!ok) break;
+            if (whole) {
+              if (lane == 0) {
+                if (half == 0) bits[(tile % kBits) * 4 + (u & 3)] = 0xffffffffu;
+                mbar_arrive_expect_tx(full, 32 * D * 2);
+              }
+              __syncwarp();
+              if (lane < boxes)
+                tma_load_page(dst + (lane % BLKS) * L::BLK + (r0 + lane / BLKS * p.box) * 128, half ? &v_map : &k_map,
+                              full, (lane % BLKS) * 64, kvh, box_slot, box_page);
+              continue;
+            }
 #pragma unroll 8
             for (int i = 0; i < CH; ++i) {
               const int piece = i * 32 + lane, r = piece / CH, c = piece % CH;
@@ -565,7 +602,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_window_kernel(const Params 
 }
 
 template <class T, int D, bool FP4, bool SHARED>
-csa2_status run(const Params& p, dim3 grid, cudaStream_t stream) {
+csa2_status run(const Params& p, dim3 grid, const CUtensorMap& k_map, const CUtensorMap& v_map, cudaStream_t stream) {
   using L = Lay<D, SHARED>;
   static PerDevice<int> opted;
   opted.get(+[]() -> int {
@@ -581,7 +618,7 @@ csa2_status run(const Params& p, dim3 grid, cudaStream_t stream) {
   cfg.attrs = at;
   cfg.numAttrs = 1;
   begin_launch(stream);
-  const cudaError_t e = cudaLaunchKernelEx(&cfg, paged_window_kernel<T, D, FP4, SHARED>, p);
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, paged_window_kernel<T, D, FP4, SHARED>, p, k_map, v_map);
   note_launch(LK_ATTN, 1, stream);
   if (e != cudaSuccess) {
     cudaGetLastError();
@@ -616,7 +653,16 @@ csa2_status launch_paged_window_tc(const PagedAttn& a, const int32_t* cu_q, int6
   if (tiles > 0x7fffffffLL) return fail(CSA2_ERR_UNSUPPORTED, "csa2_paged_window_attn: too many rows");
   const dim3 grid(static_cast<unsigned>(tiles), static_cast<unsigned>(a.kv.heads));
   const bool sh = a.kv.v == a.kv.k;
-#define CSA2_WIN_T(T_, D_, F_) (sh ? run<T_, D_, F_, true>(p, grid, stream) : run<T_, D_, F_, false>(p, grid, stream))
+  CUtensorMap k_map = {}, v_map = {};
+  const int page = 1 << a.kv.page_shift;
+  if (a.fmt != CSA2_KV_FP4 && page >= 8 && a.kv.n_pages > 0) {
+    p.box = std::min(page, 32);
+    for (int i = 0; i < (sh ? 1 : 2); ++i)
+      CSA2_TRY(make_tensor_map_paged(i ? &v_map : &k_map, i ? a.kv.v : a.kv.k, a.D, a.kv.heads, a.kv.head_stride, page,
+                                     a.kv.token_stride, a.kv.n_pages, a.kv.page_stride, p.box));
+  }
+#define CSA2_WIN_T(T_, D_, F_) \
+  (sh ? run<T_, D_, F_, true>(p, grid, k_map, v_map, stream) : run<T_, D_, F_, false>(p, grid, k_map, v_map, stream))
 #define CSA2_WIN(D_)                                                                       \
   if (a.D == D_)                                                                           \
     return a.fmt == CSA2_KV_FP4   ? CSA2_WIN_T(__nv_bfloat16, D_, true)                    \

@@ -45,4 +45,25 @@ csa2_status make_tensor_map_bf16_2d(CUtensorMap* map, const void* base, uint64_t
   return CSA2_OK;
 }
 
+csa2_status make_tensor_map_paged(CUtensorMap* map, const void* base, int dim, int heads, int64_t head_stride,
+                                  int page_size, int64_t token_stride, int64_t n_pages, int64_t page_stride,
+                                  int box_rows) {
+  auto fn = encode_fn();
+  if (!fn) return fail(CSA2_ERR_CUDA, "cuTensorMapEncodeTiled unavailable");
+  // a dimension of one element may carry any stride; give it a valid one
+  const cuuint64_t row = static_cast<cuuint64_t>(dim) * 2;
+  const cuuint64_t dims[4] = {static_cast<cuuint64_t>(dim), static_cast<cuuint64_t>(heads),
+                              static_cast<cuuint64_t>(page_size), static_cast<cuuint64_t>(n_pages)};
+  const cuuint64_t strides[3] = {heads > 1 ? static_cast<cuuint64_t>(head_stride) * 2 : row,
+                                 page_size > 1 ? static_cast<cuuint64_t>(token_stride) * 2 : row,
+                                 n_pages > 1 ? static_cast<cuuint64_t>(page_stride) * 2 : row};
+  const cuuint32_t box[4] = {64, 1, static_cast<cuuint32_t>(box_rows), 1};
+  const cuuint32_t estr[4] = {1, 1, 1, 1};
+  const CUresult r = fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(base), dims, strides, box, estr,
+                        CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                        CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  if (r != CUDA_SUCCESS) return fail(CSA2_ERR_CUDA, "cuTensorMapEncodeTiled failed (%d)", int(r));
+  return CSA2_OK;
+}
+
 }  // namespace csa2
