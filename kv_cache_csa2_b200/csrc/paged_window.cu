@@ -104,6 +104,28 @@ __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16
       : "memory");
 }
 
+// Pairs of f32 in one instruction, each rounded to nearest.
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  float2 d;
+  asm("{.reg .b64 x, y, z, w; mov.b64 x, {%2, %3}; mov.b64 y, {%4, %5}; mov.b64 z, {%6, %7};"
+      " fma.rn.f32x2 w, x, y, z; mov.b64 {%0, %1}, w;}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+  return d;
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+  float2 d;
+  asm("{.reg .b64 x, y, w; mov.b64 x, {%2, %3}; mov.b64 y, {%4, %5}; add.rn.f32x2 w, x, y; mov.b64 {%0, %1}, w;}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return d;
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float d;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
+
 template <class T>
 __host__ __device__ constexpr uint32_t idesc_of(int M, int N, bool b_mn) {
   return std::is_same<T, __half>::value ? idesc_f16_f32(M, N, false, b_mn) : idesc_bf16_f32(M, N, false, b_mn);
@@ -478,7 +500,8 @@ __global__ void __launch_bounds__(kThreads, 1) paged_window_kernel(const Params 
     // tokens [win, pos] and [0, sink_end) are visible
     const int win = p.window > 0 ? pos - p.window + 1 : 0;
     const int sink_end = min(p.sinks, pos + 1);
-    float m = -INFINITY, l0 = 0.0f, l1 = 0.0f;
+    float m = -INFINITY;
+    float2 l = make_float2(0.0f, 0.0f);
     uint32_t turn = 0;
     bool ok = true;
     for (int j = 0; j < wk.tiles && ok; ++j) {
@@ -490,65 +513,101 @@ __global__ void __launch_bounds__(kThreads, 1) paged_window_kernel(const Params 
       ok = __all_sync(0xffffffffu, ok);
       if (!ok) break;
       tc_fence_after();
-      float s[4][32];
-#pragma unroll
-      for (int c = 0; c < 4; ++c)
-        if (c >= c0 && c < c1) tmem_ld32(s_at + c * 32, reinterpret_cast<uint32_t(&)[32]>(s[c]));
-      tmem_wait_ld();
-      float mx = -INFINITY;
-#pragma unroll
-      for (int c = 0; c < 4; ++c) {
-        if (c < c0 || c >= c1) continue;
+      // bit i: token j0 + 32 c + i visible to this row
+      auto visible = [&](int c) -> uint32_t {
         const int ja = j0 + c * 32;
         const uint32_t here = *reinterpret_cast<volatile uint32_t*>(bits + (j % kBits) * 4 + c);
-        const bool whole = ja >= win && ja + 31 <= pos && here == 0xffffffffu;
-        if (!__all_sync(0xffffffffu, whole)) {
-          // bit i: token ja + i visible
-          auto upto = [](int n) -> uint32_t { return n <= 0 ? 0u : n >= 32 ? 0xffffffffu : (1u << n) - 1u; };
-          const uint32_t vis = ((upto(pos + 1 - ja) & ~upto(win - ja)) | upto(sink_end - ja)) & here;
+        auto upto = [](int n) -> uint32_t { return n <= 0 ? 0u : n >= 32 ? 0xffffffffu : (1u << n) - 1u; };
+        return ((upto(pos + 1 - ja) & ~upto(win - ja)) | upto(sink_end - ja)) & here;
+      };
+      // Takes the tile's maximum into the reference: kept while it has not outgrown
+      // it, else the output so far is rescaled (its product must have ended).
+      auto refer = [&](float mx) -> float {
+        mx *= p.scale2;
+        const bool grow = mx > m + kLazy || (m == -INFINITY && mx > -INFINITY);
+        const bool scale_o = grow && m > -INFINITY;
+        if (__any_sync(0xffffffffu, scale_o)) {
+          const float f = scale_o ? exp2_approx(m - mx) : 1.0f;
+          l.x *= f;
+          l.y *= f;
+          ok = mbar_wait(pv_done + w, (turn - 1) & 1, abort_flag, p.kv.err);   // turn > 0: m is finite
+          ok = __all_sync(0xffffffffu, ok);
+          tc_fence_after();
+#pragma unroll 1
+          for (int c = 0; c < D / 16 && ok; ++c) {
+            uint32_t v[16];
+            tmem_ld16(o_at + c * 16, v);
+            tmem_wait_ld();
 #pragma unroll
-          for (int i = 0; i < 32; ++i) s[c][i] = (vis >> i) & 1u ? s[c][i] : -INFINITY;
+            for (int i = 0; i < 16; ++i) v[i] = __float_as_uint(__uint_as_float(v[i]) * f);
+            tmem_st16(o_at + c * 16, v);
+          }
         }
-#pragma unroll
-        for (int i = 0; i < 32; ++i) mx = fmaxf(mx, s[c][i]);
+        if (grow) m = mx;
+        return m == -INFINITY ? 0.0f : m;
+      };
+      bool plain = c0 == 0 && c1 == 4 && j0 >= win && j0 + KT - 1 <= pos;
+      {
+        const volatile uint32_t* here = bits + (j % kBits) * 4;
+        plain = plain && (here[0] & here[1] & here[2] & here[3]) == 0xffffffffu;
       }
-      mx *= p.scale2;
-      // keep the old reference while the maximum has not outgrown it
-      const bool grow = mx > m + kLazy || (m == -INFINITY && mx > -INFINITY);
-      const bool scale_o = grow && m > -INFINITY;
-      if (__any_sync(0xffffffffu, scale_o)) {
-        const float f = scale_o ? exp2_approx(m - mx) : 1.0f;
-        l0 *= f;
-        l1 *= f;
-        ok = mbar_wait(pv_done + w, (turn - 1) & 1, abort_flag, p.kv.err);   // turn > 0: m is finite
-        ok = __all_sync(0xffffffffu, ok);
-        if (!ok) break;
-        tc_fence_after();
+      if (__all_sync(0xffffffffu, plain)) {
+        // every row sees the whole tile: its 128 scores stay in registers
+        float s[KT];
 #pragma unroll
-        for (int c = 0; c < D / 32; ++c) {
+        for (int c = 0; c < 4; ++c) tmem_ld32(s_at + c * 32, *reinterpret_cast<uint32_t(*)[32]>(s + c * 32));
+        tmem_wait_ld();
+        float mx[4] = {s[0], s[1], s[2], s[3]};
+#pragma unroll
+        for (int i = 4; i < KT; i += 8)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) mx[e] = i + 4 + e < KT ? max3(mx[e], s[i + e], s[i + 4 + e]) : fmaxf(mx[e], s[i + e]);
+        const float ref = refer(fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])));
+        if (!ok) break;
+        const float2 sc = make_float2(p.scale2, p.scale2), nr = make_float2(-ref, -ref);
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          uint32_t pk[16];
+#pragma unroll
+          for (int i = 0; i < 16; ++i) {
+            const float2 x = fma2(make_float2(s[c * 32 + 2 * i], s[c * 32 + 2 * i + 1]), sc, nr);
+            const float2 e = make_float2(exp2_approx(x.x), exp2_approx(x.y));
+            l = add2(l, e);
+            pk[i] = Num<T>::down(e.x, e.y);
+          }
+          tmem_st16(s_at + c * 16, pk);
+        }
+      } else {
+        // 32 columns at a time, read twice (the weights of block c land on scores
+        // of block c / 2, which have been read)
+        float mx = -INFINITY;
+#pragma unroll 1
+        for (int c = c0; c < c1; ++c) {
           uint32_t v[32];
-          tmem_ld32(o_at + c * 32, v);
+          tmem_ld32(s_at + c * 32, v);
+          const uint32_t vis = visible(c);
           tmem_wait_ld();
 #pragma unroll
-          for (int i = 0; i < 32; ++i) v[i] = __float_as_uint(__uint_as_float(v[i]) * f);
-          tmem_st32(o_at + c * 32, v);
+          for (int i = 0; i < 32; ++i) mx = fmaxf(mx, (vis >> i) & 1u ? __uint_as_float(v[i]) : -INFINITY);
         }
-      }
-      if (grow) m = mx;
-      const float ref = m == -INFINITY ? 0.0f : m;
+        const float ref = refer(mx);
+        if (!ok) break;
+#pragma unroll 1
+        for (int c = c0; c < c1; ++c) {
+          uint32_t v[32], pk[16];
+          tmem_ld32(s_at + c * 32, v);
+          const uint32_t vis = visible(c);
+          tmem_wait_ld();
 #pragma unroll
-      for (int c = 0; c < 4; ++c) {
-        if (c < c0 || c >= c1) continue;
-        uint32_t pk[16];
-#pragma unroll
-        for (int i = 0; i < 16; ++i) {
-          const float e0 = exp2_approx(fmaf(s[c][2 * i], p.scale2, -ref));
-          const float e1 = exp2_approx(fmaf(s[c][2 * i + 1], p.scale2, -ref));
-          l0 += e0;
-          l1 += e1;
-          pk[i] = Num<T>::down(e0, e1);
+          for (int i = 0; i < 16; ++i) {
+            const float a = (vis >> (2 * i)) & 1u ? __uint_as_float(v[2 * i]) : -INFINITY;
+            const float b = (vis >> (2 * i + 1)) & 1u ? __uint_as_float(v[2 * i + 1]) : -INFINITY;
+            const float2 e = make_float2(exp2_approx(fmaf(a, p.scale2, -ref)), exp2_approx(fmaf(b, p.scale2, -ref)));
+            l = add2(l, e);
+            pk[i] = Num<T>::down(e.x, e.y);
+          }
+          tmem_st16(s_at + c * 16, pk);
         }
-        tmem_st16(s_at + c * 16, pk);
       }
       tmem_wait_st();
       tc_fence_before();
@@ -562,8 +621,8 @@ __global__ void __launch_bounds__(kThreads, 1) paged_window_kernel(const Params 
       tc_fence_after();
     }
     if (ok) {
-      const float l = l0 + l1;
-      const float inv = l > 0.0f ? 1.0f / l : (l == 0.0f ? 0.0f : l);
+      const float sum = l.x + l.y;
+      const float inv = sum > 0.0f ? 1.0f / sum : (sum == 0.0f ? 0.0f : sum);
       const int64_t at = (wk.q_row0 + tok) * p.Hq + kvh * p.G + (rr - tok * p.G);
 #pragma unroll
       for (int c = 0; c < D / 32; ++c) {
@@ -587,7 +646,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_window_kernel(const Params 
           }
         }
       }
-      if (live && p.lse) p.lse[at] = l == 0.0f ? -INFINITY : (m + log2f(l)) * kLn2;
+      if (live && p.lse) p.lse[at] = sum == 0.0f ? -INFINITY : (m + log2f(sum)) * kLn2;
     }
   }
   // every product has completed before TMEM and shared memory go
