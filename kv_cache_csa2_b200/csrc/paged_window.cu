@@ -21,9 +21,10 @@
 // by more than 2^8 since its last reference (its weights then exceed 1 by at
 // most that, which neither type nor the f32 sums mind).
 //
-// Key tiles are aligned to 128 tokens and a tile's columns that no row of the
-// tile sees are skipped in blocks of 32, both of which leave a row's sums alone:
-// its bits depend on its own tokens only.
+// Key tiles are aligned to 128 tokens, and within a tile the blocks of 32 tokens
+// that no row of the row tile sees are skipped; neither touches a row's sums, so
+// its bits depend on its own tokens only.  The weights are handed on in halves, so
+// the products with the values start while the second half is still exponentials.
 //
 // Bound: 4 D flops per (row, key) on the tensor cores against one exponential,
 // 16 of which an SM does per clock: at D = 128 both take 1024 clocks per pair of
@@ -42,6 +43,7 @@ using rope::Num;
 
 constexpr int kThreads = 384;
 constexpr int KT = 128;                                // keys per tile
+constexpr int KB = 32;                                 // keys per block
 constexpr int RT = 128;                                // rows per row tile
 constexpr int kBits = 8;                               // slots of the presence words
 constexpr float kLazy = 8.0f;                          // log2 growth of a maximum that O tolerates
@@ -56,7 +58,7 @@ struct Lay {
   static constexpr int K = Q + 2 * TILE;
   static constexpr int V = K + KST * TILE;
   static constexpr int BAR = V + VST * TILE;
-  static constexpr int NBAR = 2 * KST + 2 * VST + 2 + 2 + 2 + 1;
+  static constexpr int NBAR = 2 * KST + 2 * VST + 2 + 4 + 2 + 1 + 1;
   static constexpr int BITS = BAR + NBAR * 8;
   static constexpr int MISC = BITS + kBits * 4 * 4;
   static constexpr int BYTES = MISC + 16 + 1024;
@@ -134,16 +136,16 @@ __host__ __device__ constexpr uint32_t idesc_of(int M, int N, bool b_mn) {
 // Row tiles of a CTA: the sequence, its rows, and what they see.
 struct Work {
   int b, base, n_rows;               // sequence, position of its first new token, rows of this CTA (<= 256)
-  int64_t q_row0, r0;                // first q row of the sequence, first (token, head) row of the CTA
+  int q_row0, r0;                    // first q row of the sequence, first (token, head) row of the CTA
   int sink_tiles, first_tile, tiles; // key tiles: the sinks', then from first_tile on
   int lo, ns, pmax;                  // tokens loaded: [0, ns) and [lo, pmax]
+
+  __device__ __forceinline__ int tile_start(int j) const {
+    return (j < sink_tiles ? j : j - sink_tiles + first_tile) * KT;
+  }
 };
 
-__device__ __forceinline__ int tile_start(const Work& w, int j) {
-  return (j < w.sink_tiles ? j : j - w.sink_tiles + w.first_tile) * KT;
-}
-
-// Columns of a key tile that row tile w sees, in blocks of 32: [c0, c1).
+// What the rows of row tile w see together.
 struct RowTile {
   int lo, ns, pmax;
   __device__ __forceinline__ RowTile(const Work& k, int w, int G, int window, int sinks) {
@@ -151,26 +153,23 @@ struct RowTile {
     lo = ns = 0;
     pmax = -1;
     if (rows > 0) {
-      const int64_t r = k.r0 + w * RT;
-      const int pmin = k.base + static_cast<int>(r / G);
-      pmax = k.base + static_cast<int>((r + rows - 1) / G);
-      const Seen s(pmin, pmax, window, sinks);
+      const int r = k.r0 + w * RT;
+      pmax = k.base + (r + rows - 1) / G;
+      const Seen s(k.base + r / G, pmax, window, sinks);
       lo = s.lo;
       ns = s.ns;
     }
   }
-  __device__ __forceinline__ void range(int j0, int& c0, int& c1) const {
-    c0 = c1 = 0;
-    if (pmax < 0) return;
-    const int a = max(j0, lo), e = min(j0 + KT - 1, pmax);
-    if (a <= e) {
-      c0 = (a - j0) >> 5;
-      c1 = ((e - j0) >> 5) + 1;
+  // bit c: block c of the tile is seen by some row
+  __device__ __forceinline__ uint32_t blocks(const Work& k, int tile) const {
+    uint32_t m = 0;
+    const int t0 = k.tile_start(tile);
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+      const int t = t0 + c * KB;
+      if (t <= pmax && (t + KB > lo || t < ns)) m |= 1u << c;
     }
-    if (j0 < ns) {
-      c0 = 0;
-      c1 = max(c1, ((min(ns, j0 + KT) - 1 - j0) >> 5) + 1);
-    }
+    return m;
   }
 };
 
@@ -207,12 +206,11 @@ __device__ bool locate(const Params& p, int64_t index, Work& w) {
       c1 = __shfl_sync(0xffffffffu, c1, src);
       w.b = s0 + src;
       w.q_row0 = c0;
-      w.r0 = tile * 2 * RT;
+      w.r0 = static_cast<int>(tile * 2 * RT);
       w.n_rows = static_cast<int>(min(static_cast<int64_t>(2 * RT), static_cast<int64_t>(c1 - c0) * p.G - w.r0));
       w.base = length_of(p.kv, w.b, threadIdx.x == 0) - (c1 - c0);
-      const int pmin = w.base + static_cast<int>(w.r0 / p.G);
-      w.pmax = w.base + static_cast<int>((w.r0 + w.n_rows - 1) / p.G);
-      const Seen s(pmin, w.pmax, p.window, p.sinks);
+      w.pmax = w.base + (w.r0 + w.n_rows - 1) / p.G;
+      const Seen s(w.base + w.r0 / p.G, w.pmax, p.window, p.sinks);
       w.lo = s.lo;
       w.ns = s.ns;
       w.sink_tiles = (s.ns + KT - 1) / KT;
@@ -237,9 +235,10 @@ __global__ void __launch_bounds__(kThreads, 1) paged_window_kernel(const Params 
   uint64_t* v_full = SHARED ? k_full : k_empty + L::KST;
   uint64_t* v_empty = SHARED ? k_empty : v_full + L::VST;
   uint64_t* s_full = bar + 2 * L::KST + 2 * L::VST;    // [2]
-  uint64_t* p_full = s_full + 2;
-  uint64_t* pv_done = p_full + 2;
+  uint64_t* p_full = s_full + 2;                       // [2][2]: one per half of a tile
+  uint64_t* pv_done = p_full + 4;                      // [2]
   uint64_t* all_done = pv_done + 2;
+  uint64_t* q_full = all_done + 1;
   constexpr int VS = SHARED ? L::KST : L::VST;
   uint32_t* bits = reinterpret_cast<uint32_t*>(smem + L::BITS);       // [kBits][4]: tokens present
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + L::MISC);
@@ -255,7 +254,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_window_kernel(const Params 
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < L::KST; ++i) {
-      mbar_init(k_full + i, 4);                        // one arrival per 32 tokens
+      mbar_init(k_full + i, 4);                        // one arrival per block
       mbar_init(k_empty + i, 1);
     }
     for (int i = 0; i < L::VST; ++i) {
@@ -264,10 +263,12 @@ __global__ void __launch_bounds__(kThreads, 1) paged_window_kernel(const Params 
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(s_full + i, 1);
-      mbar_init(p_full + i, 4);
+      mbar_init(p_full + 2 * i, 4);
+      mbar_init(p_full + 2 * i + 1, 4);
       mbar_init(pv_done + i, 1);
     }
     mbar_init(all_done, 1);
+    mbar_init(q_full, 8);
     *abort_flag = 0;
     fence_mbar_init();
   }
@@ -275,45 +276,27 @@ __global__ void __launch_bounds__(kThreads, 1) paged_window_kernel(const Params 
     tmem_alloc(tmem_slot, 512);
     tmem_relinquish();
   }
-  // q rows (zero past the last) into K-major swizzled tiles
-  for (int i = threadIdx.x; i < 2 * RT * (D / 8); i += kThreads) {
-    const int r = i / (D / 8), c = i % (D / 8);
-    uint4 v = make_uint4(0, 0, 0, 0);
-    if (r < wk.n_rows) {
-      const int64_t rr = wk.r0 + r, t = rr / p.G;
-      v = __ldg(reinterpret_cast<const uint4*>(p.q + (wk.q_row0 + t) * p.q_token +
-                                               (kvh * p.G + (rr - t * p.G)) * p.q_head) + c);
-      v.x ^= p.flip;
-      v.y ^= p.flip;
-      v.z ^= p.flip;
-      v.w ^= p.flip;
-    }
-    *reinterpret_cast<uint4*>(smem + L::Q + (r / RT) * L::TILE + (c / 8) * L::BLK + sw128_offset(r % RT, c % 8)) = v;
-  }
-  fence_proxy_async_smem();
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
   constexpr uint32_t O_COL = 256;                      // S / P of tile w at 128 w, O at 256 + 128 w
-
   // registers: 168 x 384 threads at launch = 208 x 256 (softmax) + 88 x 128 (the rest)
   if (warp >= 8) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
     if (warp > 8) {
       // ------------------------------------------------------------ loaders
-      // unit u = (key tile u / 4, its 32 tokens u % 4); the three warps in turn
+      // unit u = (key tile u / 4, its block u % 4); the three warps in turn
       const int units = 4 * wk.tiles;
-      auto row_of = [&](int u) -> int64_t {
-        if (u >= units) return -1;
-        const int j = tile_start(wk, u >> 2) + (u & 3) * 32 + lane;
-        if (j > wk.pmax || (j < wk.lo && j >= wk.ns)) return -1;
-        const int64_t r = token_row(p.kv, wk.b, j);
-        return r < 0 ? -1 : r + kvh * p.kv.head_stride;
+      auto token_of = [&](int u) { return wk.tile_start(u >> 2) + (u & 3) * KB + lane; };
+      auto wanted = [&](int u) {                       // this lane's token is seen by some row
+        const int j = token_of(u);
+        return u < units && j <= wk.pmax && (j >= wk.lo || j < wk.ns);
       };
-      auto lost_of = [&](int u, int64_t row) {           // wanted, but its page is outside the pool
-        const int j = tile_start(wk, u >> 2) + (u & 3) * 32 + lane;
-        return row < 0 && j <= wk.pmax && (j >= wk.lo || j < wk.ns);
+      auto row_of = [&](int u) -> int64_t {
+        if (!wanted(u)) return -1;
+        const int64_t r = token_row(p.kv, wk.b, token_of(u));
+        return r < 0 ? -1 : r + kvh * p.kv.head_stride;
       };
       constexpr int HALVES = SHARED ? 1 : 2;
       constexpr int CH = FP4 ? D / 32 : D / 8;           // 16-byte pieces of a row
@@ -323,14 +306,16 @@ __global__ void __launch_bounds__(kThreads, 1) paged_window_kernel(const Params 
       for (int u = warp - 9; u < units && ok; u += 3) {
         const int tile = u >> 2, r0 = (u & 3) * 32;
         const int64_t next = row_of(u + 3);
-        const uint32_t lost = __ballot_sync(0xffffffffu, lost_of(u, row));
+        const uint32_t want = __ballot_sync(0xffffffffu, wanted(u));
+        const uint32_t lost = __ballot_sync(0xffffffffu, row < 0) & want;    // its page is outside the pool
+        const bool empty_block = want == 0;            // its columns are never used
         // a whole unit: boxes of p.box rows and 64 channels, one per lane
         const bool whole = !FP4 && p.box > 0 && __all_sync(0xffffffffu, row >= 0);
         constexpr int BLKS = D / 64;
         const int boxes = whole ? 32 / p.box * BLKS : 0;
         int box_page = 0, box_slot = 0;
         if (lane < boxes) {
-          const int j = tile_start(wk, tile) + r0 + lane / BLKS * p.box;
+          const int j = wk.tile_start(tile) + r0 + lane / BLKS * p.box;
           box_page = __ldg(p.kv.table + wk.b * p.kv.table_stride + (j >> p.kv.page_shift));
           box_slot = j & ((1 << p.kv.page_shift) - 1);
         }
@@ -342,15 +327,19 @@ __global__ void __launch_bounds__(kThreads, 1) paged_window_kernel(const Params 
           uint64_t* full = (half ? v_full : k_full) + st;
           uint64_t* empty = (half ? v_empty : k_empty) + st;
           const uint32_t parity = ((tile / ring) & 1) ^ 1;
-          if (!FP4) {
-            // do not hold back what has landed while the stage is still in use
-            if (waiting && !__all_sync(0xffffffffu, mbar_try_wait(empty, parity))) {
-              cp_async_wait<0>();
-              fence_proxy_async_smem();
-              __syncwarp();
-              if (lane == 0) mbar_arrive(waiting);
-              waiting = nullptr;
-            }
+          // do not hold back what has landed while the stage is still in use
+          if (waiting && !__all_sync(0xffffffffu, mbar_try_wait(empty, parity))) {
+            cp_async_wait<0>();
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(waiting);
+            waiting = nullptr;
+          }
+          if (empty_block) {
+            ok = __all_sync(0xffffffffu, mbar_wait(empty, parity, abort_flag, p.kv.err));
+            if (!ok) break;
+            if (lane == 0) mbar_arrive(full);
+          } else if (!FP4) {
             ok = mbar_wait(empty, parity, abort_flag, p.kv.err);
             ok = __all_sync(0xffffffffu, ok);
             if (!ok) break;
@@ -429,14 +418,10 @@ __global__ void __launch_bounds__(kThreads, 1) paged_window_kernel(const Params 
         constexpr uint32_t idesc_s = idesc_of<T>(128, KT, false), idesc_o = idesc_of<T>(128, D, true);
         const RowTile rt[2] = {RowTile(wk, 0, p.G, p.window, p.sinks), RowTile(wk, 1, p.G, p.window, p.sinks)};
         const uint32_t q0 = smem_u32(smem + L::Q), k0 = smem_u32(sK), v0 = smem_u32(sV);
-        uint32_t turns[2] = {0, 0};                      // weights consumed per row tile
+        uint32_t p_phase[2] = {0, 0};                  // bit h: parity of p_full[w][h]
         bool started[2] = {false, false};
-        int k_seen = -1, v_seen = -1;                    // last tile whose arrival was waited for
-        bool ok = true;
-        auto active = [&](int w, int j, int& c0, int& c1) {
-          rt[w].range(tile_start(wk, j), c0, c1);
-          return c0 < c1;
-        };
+        int k_seen = -1, v_seen = -1;                  // last tile whose arrival was waited for
+        bool ok = mbar_wait(q_full, 0, abort_flag, p.kv.err);
         auto scores = [&](int w, int j) {
           if (k_seen < j) {
             ok = ok && mbar_wait(k_full + j % L::KST, (j / L::KST) & 1, abort_flag, p.kv.err);
@@ -451,33 +436,43 @@ __global__ void __launch_bounds__(kThreads, 1) paged_window_kernel(const Params 
                      desc_kmajor_sw128(bk + (kk >> 2) * L::BLK + (kk & 3) * 32), idesc_s, kk != 0);
           mma_commit(s_full + w);
         };
-        int c0, c1;
+        uint32_t act[2] = {0, 0}, next[2] = {0, 0};
         if (wk.tiles > 0) {
-          for (int w = 0; w < 2; ++w)
-            if (active(w, 0, c0, c1)) scores(w, 0);
+          for (int w = 0; w < 2; ++w) {
+            next[w] = rt[w].blocks(wk, 0);
+            if (next[w]) scores(w, 0);
+          }
           if (!SHARED && ok) mma_commit(k_empty);
         }
         for (int j = 0; j < wk.tiles && ok; ++j) {
+          const uint32_t bv = v0 + (j % VS) * L::TILE;
           for (int w = 0; w < 2 && ok; ++w) {
-            if (active(w, j, c0, c1)) {
-              ok = mbar_wait(p_full + w, turns[w] & 1, abort_flag, p.kv.err);
-              ++turns[w];
+            act[w] = next[w];
+            next[w] = j + 1 < wk.tiles ? rt[w].blocks(wk, j + 1) : 0u;
+            for (int half = 0; half < 2 && ok; ++half) {
+              const uint32_t mine = (act[w] >> (2 * half)) & 3u;
+              if (mine == 0) continue;
+              ok = mbar_wait(p_full + 2 * w + half, (p_phase[w] >> half) & 1, abort_flag, p.kv.err);
+              p_phase[w] ^= 1u << half;
               if (ok && v_seen < j) {
                 ok = mbar_wait(v_full + j % VS, (j / VS) & 1, abort_flag, p.kv.err);
                 v_seen = j;
               }
               if (!ok) break;
               tc_fence_after();
-              const uint32_t bv = v0 + (j % VS) * L::TILE;
-              for (int kk = 2 * c0; kk < 2 * c1; ++kk) { // 16 keys per product
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {            // 16 keys per product
+                if (!((mine >> (i >> 1)) & 1u)) continue;
+                const int kk = 4 * half + i;
                 mma_ts(tmem + O_COL + w * 128, tmem + w * 128 + kk * 8,
                        desc_mnmajor_sw128(bv + kk * 2048, L::BLK, 1024), idesc_o, started[w]);
                 started[w] = true;
               }
-              mma_commit(pv_done + w);
             }
-            if (w == 1) mma_commit(v_empty + j % VS);    // both tiles are past this one's values
-            if (j + 1 < wk.tiles && active(w, j + 1, c0, c1)) scores(w, j + 1);
+            if (act[w]) mma_commit(pv_done + w);
+            if (!ok) break;
+            if (w == 1) mma_commit(v_empty + j % VS);  // both tiles are past this one's values
+            if (next[w]) scores(w, j + 1);
             if (!SHARED && w == 1 && j + 1 < wk.tiles && ok) mma_commit(k_empty + (j + 1) % L::KST);
           }
         }
@@ -493,126 +488,148 @@ __global__ void __launch_bounds__(kThreads, 1) paged_window_kernel(const Params 
     const int r = quad * 32 + lane;                    // row of the tile = TMEM lane
     const uint32_t lane_off = static_cast<uint32_t>(quad * 32) << 16;
     const uint32_t s_at = tmem + lane_off + w * 128, o_at = tmem + lane_off + O_COL + w * 128;
-    const RowTile rt(wk, w, p.G, p.window, p.sinks);
     const bool live = w * RT + r < wk.n_rows;
-    const int64_t rr = wk.r0 + w * RT + r, tok = rr / p.G;
-    const int pos = live ? wk.base + static_cast<int>(tok) : -1;
+    const int rr = wk.r0 + w * RT + r, tok = rr / p.G, head = kvh * p.G + (rr - tok * p.G);
+    {
+      // this thread's q row (zero past the last) into the K-major swizzled tile
+      const uint4* src = reinterpret_cast<const uint4*>(p.q + (static_cast<int64_t>(wk.q_row0) + tok) * p.q_token +
+                                                        head * p.q_head);
+      uint4 v[D / 8];
+#pragma unroll
+      for (int c = 0; c < D / 8; ++c) v[c] = live ? __ldg(src + c) : make_uint4(0, 0, 0, 0);
+#pragma unroll
+      for (int c = 0; c < D / 8; ++c) {
+        v[c].x ^= p.flip;
+        v[c].y ^= p.flip;
+        v[c].z ^= p.flip;
+        v[c].w ^= p.flip;
+        *reinterpret_cast<uint4*>(smem + L::Q + w * L::TILE + (c / 8) * L::BLK + sw128_offset(r, c % 8)) = v[c];
+      }
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(q_full);
+    }
+    const RowTile rt(wk, w, p.G, p.window, p.sinks);
+    const int pos = live ? wk.base + tok : -1;
     // tokens [win, pos] and [0, sink_end) are visible
     const int win = p.window > 0 ? pos - p.window + 1 : 0;
     const int sink_end = min(p.sinks, pos + 1);
     float m = -INFINITY;
     float2 l = make_float2(0.0f, 0.0f);
-    uint32_t turn = 0;
+    uint32_t turn = 0;                                 // tiles done
     bool ok = true;
     for (int j = 0; j < wk.tiles && ok; ++j) {
-      const int j0 = tile_start(wk, j);
-      int c0, c1;
-      rt.range(j0, c0, c1);
-      if (c0 >= c1) continue;
+      const uint32_t act = rt.blocks(wk, j);
+      if (act == 0) continue;
       ok = mbar_wait(s_full + w, turn & 1, abort_flag, p.kv.err);
       ok = __all_sync(0xffffffffu, ok);
       if (!ok) break;
       tc_fence_after();
-      // bit i: token j0 + 32 c + i visible to this row
-      auto visible = [&](int c) -> uint32_t {
-        const int ja = j0 + c * 32;
-        const uint32_t here = *reinterpret_cast<volatile uint32_t*>(bits + (j % kBits) * 4 + c);
-        auto upto = [](int n) -> uint32_t { return n <= 0 ? 0u : n >= 32 ? 0xffffffffu : (1u << n) - 1u; };
-        return ((upto(pos + 1 - ja) & ~upto(win - ja)) | upto(sink_end - ja)) & here;
-      };
-      // Takes the tile's maximum into the reference: kept while it has not outgrown
-      // it, else the output so far is rescaled (its product must have ended).
-      auto refer = [&](float mx) -> float {
-        mx *= p.scale2;
-        const bool grow = mx > m + kLazy || (m == -INFINITY && mx > -INFINITY);
-        const bool scale_o = grow && m > -INFINITY;
-        if (__any_sync(0xffffffffu, scale_o)) {
-          const float f = scale_o ? exp2_approx(m - mx) : 1.0f;
-          l.x *= f;
-          l.y *= f;
-          ok = mbar_wait(pv_done + w, (turn - 1) & 1, abort_flag, p.kv.err);   // turn > 0: m is finite
-          ok = __all_sync(0xffffffffu, ok);
-          tc_fence_after();
+      const int t0 = wk.tile_start(j);
+      const volatile uint32_t* here = bits + (j % kBits) * 4;
+      // the reference stays while the maximum has not outgrown it; else the output
+      // so far is rescaled (its products ended before this tile's scores did)
+      auto refer = [&](float top) -> float {
+        const bool grow = top > m + kLazy || (m == -INFINITY && top > -INFINITY);
+        if (__any_sync(0xffffffffu, grow)) {
+          const bool scale_o = grow && m > -INFINITY;
+          if (__any_sync(0xffffffffu, scale_o)) {
+            const float f = scale_o ? exp2_approx(m - top) : 1.0f;
+            l.x *= f;
+            l.y *= f;
 #pragma unroll 1
-          for (int c = 0; c < D / 16 && ok; ++c) {
-            uint32_t v[16];
-            tmem_ld16(o_at + c * 16, v);
-            tmem_wait_ld();
+            for (int i = 0; i < D / 16; ++i) {
+              uint32_t x[16];
+              tmem_ld16(o_at + i * 16, x);
+              tmem_wait_ld();
 #pragma unroll
-            for (int i = 0; i < 16; ++i) v[i] = __float_as_uint(__uint_as_float(v[i]) * f);
-            tmem_st16(o_at + c * 16, v);
+              for (int e = 0; e < 16; ++e) x[e] = __float_as_uint(__uint_as_float(x[e]) * f);
+              tmem_st16(o_at + i * 16, x);
+            }
           }
+          if (grow) m = top;
         }
-        if (grow) m = mx;
         return m == -INFINITY ? 0.0f : m;
       };
-      bool plain = c0 == 0 && c1 == 4 && j0 >= win && j0 + KT - 1 <= pos;
-      {
-        const volatile uint32_t* here = bits + (j % kBits) * 4;
-        plain = plain && (here[0] & here[1] & here[2] & here[3]) == 0xffffffffu;
-      }
+      auto hand_on = [&](int half) {                   // this half of the weights is complete
+        tmem_wait_st();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(p_full + 2 * w + half);
+      };
+      const bool plain = act == 15u && t0 >= win && t0 + KT - 1 <= pos && (here[0] & here[1] & here[2] & here[3]) == 0xffffffffu;
       if (__all_sync(0xffffffffu, plain)) {
         // every row sees the whole tile: its 128 scores stay in registers
         float s[KT];
 #pragma unroll
-        for (int c = 0; c < 4; ++c) tmem_ld32(s_at + c * 32, *reinterpret_cast<uint32_t(*)[32]>(s + c * 32));
+        for (int c = 0; c < 4; ++c) tmem_ld32(s_at + c * KB, *reinterpret_cast<uint32_t(*)[32]>(s + c * KB));
         tmem_wait_ld();
         float mx[4] = {s[0], s[1], s[2], s[3]};
 #pragma unroll
-        for (int i = 4; i < KT; i += 8)
+        for (int i = 4; i < KT - 4; i += 8)
 #pragma unroll
-          for (int e = 0; e < 4; ++e) mx[e] = i + 4 + e < KT ? max3(mx[e], s[i + e], s[i + 4 + e]) : fmaxf(mx[e], s[i + e]);
-        const float ref = refer(fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])));
-        if (!ok) break;
+          for (int e = 0; e < 4; ++e) mx[e] = max3(mx[e], s[i + e], s[i + 4 + e]);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) mx[e] = fmaxf(mx[e], s[KT - 4 + e]);
+        const float ref = refer(fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * p.scale2);
         const float2 sc = make_float2(p.scale2, p.scale2), nr = make_float2(-ref, -ref);
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
           uint32_t pk[16];
 #pragma unroll
           for (int i = 0; i < 16; ++i) {
-            const float2 x = fma2(make_float2(s[c * 32 + 2 * i], s[c * 32 + 2 * i + 1]), sc, nr);
+            const float2 x = fma2(make_float2(s[c * KB + 2 * i], s[c * KB + 2 * i + 1]), sc, nr);
             const float2 e = make_float2(exp2_approx(x.x), exp2_approx(x.y));
             l = add2(l, e);
             pk[i] = Num<T>::down(e.x, e.y);
           }
           tmem_st16(s_at + c * 16, pk);
+          if (c & 1) hand_on(c >> 1);
         }
       } else {
-        // 32 columns at a time, read twice (the weights of block c land on scores
-        // of block c / 2, which have been read)
-        float mx = -INFINITY;
+        // block by block, read twice (the weights of block c land on scores of block
+        // c / 2, which have been read)
+        auto visible = [&](int c) -> uint32_t {        // bit i: token i of the block
+          const int t = t0 + c * KB;
+          auto upto = [](int n) -> uint32_t { return n <= 0 ? 0u : n >= 32 ? 0xffffffffu : (1u << n) - 1u; };
+          return ((upto(pos + 1 - t) & ~upto(win - t)) | upto(sink_end - t)) & here[c];
+        };
+        float top = -INFINITY;
 #pragma unroll 1
-        for (int c = c0; c < c1; ++c) {
-          uint32_t v[32];
-          tmem_ld32(s_at + c * 32, v);
+        for (int c = 0; c < 4; ++c) {
+          if (!((act >> c) & 1u)) continue;
+          uint32_t v[KB];
+          tmem_ld32(s_at + c * KB, v);
           const uint32_t vis = visible(c);
           tmem_wait_ld();
+          float mx[2] = {-INFINITY, -INFINITY};
 #pragma unroll
-          for (int i = 0; i < 32; ++i) mx = fmaxf(mx, (vis >> i) & 1u ? __uint_as_float(v[i]) : -INFINITY);
+          for (int i = 0; i < KB; ++i) mx[i & 1] = fmaxf(mx[i & 1], (vis >> i) & 1u ? __uint_as_float(v[i]) : -INFINITY);
+          top = fmaxf(top, fmaxf(mx[0], mx[1]));
         }
-        const float ref = refer(mx);
-        if (!ok) break;
+        const float ref = refer(top * p.scale2);
+        const float2 sc = make_float2(p.scale2, p.scale2), nr = make_float2(-ref, -ref);
 #pragma unroll 1
-        for (int c = c0; c < c1; ++c) {
-          uint32_t v[32], pk[16];
-          tmem_ld32(s_at + c * 32, v);
-          const uint32_t vis = visible(c);
-          tmem_wait_ld();
+        for (int c = 0; c < 4; ++c) {
+          if ((act >> c) & 1u) {
+            uint32_t v[KB], pk[16];
+            tmem_ld32(s_at + c * KB, v);
+            const uint32_t vis = visible(c);
+            tmem_wait_ld();
 #pragma unroll
-          for (int i = 0; i < 16; ++i) {
-            const float a = (vis >> (2 * i)) & 1u ? __uint_as_float(v[2 * i]) : -INFINITY;
-            const float b = (vis >> (2 * i + 1)) & 1u ? __uint_as_float(v[2 * i + 1]) : -INFINITY;
-            const float2 e = make_float2(exp2_approx(fmaf(a, p.scale2, -ref)), exp2_approx(fmaf(b, p.scale2, -ref)));
-            l = add2(l, e);
-            pk[i] = Num<T>::down(e.x, e.y);
+            for (int i = 0; i < 16; ++i) {
+              const float2 x = fma2(make_float2((vis >> (2 * i)) & 1u ? __uint_as_float(v[2 * i]) : -INFINITY,
+                                                (vis >> (2 * i + 1)) & 1u ? __uint_as_float(v[2 * i + 1]) : -INFINITY),
+                                    sc, nr);
+              const float2 e = make_float2(exp2_approx(x.x), exp2_approx(x.y));
+              l = add2(l, e);
+              pk[i] = Num<T>::down(e.x, e.y);
+            }
+            tmem_st16(s_at + c * 16, pk);
           }
-          tmem_st16(s_at + c * 16, pk);
+          if ((c & 1) && ((act >> (c - 1)) & 3u)) hand_on(c >> 1);
         }
       }
-      tmem_wait_st();
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(p_full + w);
       ++turn;
     }
     if (turn > 0 && ok) {
@@ -623,7 +640,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_window_kernel(const Params 
     if (ok) {
       const float sum = l.x + l.y;
       const float inv = sum > 0.0f ? 1.0f / sum : (sum == 0.0f ? 0.0f : sum);
-      const int64_t at = (wk.q_row0 + tok) * p.Hq + kvh * p.G + (rr - tok * p.G);
+      const int64_t at = (static_cast<int64_t>(wk.q_row0) + tok) * p.Hq + head;
 #pragma unroll
       for (int c = 0; c < D / 32; ++c) {
         uint32_t v[32];
@@ -709,7 +726,7 @@ csa2_status launch_paged_window_tc(const PagedAttn& a, const int32_t* cu_q, int6
   p.kv = a.kv;
   // at most one tile more per sequence than all rows need
   const int64_t tiles = (T * a.G + 2 * RT - 1) / (2 * RT) + a.kv.B;
-  if (tiles > 0x7fffffffLL) return fail(CSA2_ERR_UNSUPPORTED, "csa2_paged_window_attn: too many rows");
+  if (T * a.G > 0x7fffff00LL || tiles > 0x7fffffffLL) return fail(CSA2_ERR_UNSUPPORTED, "csa2_paged_window_attn: too many rows");
   const dim3 grid(static_cast<unsigned>(tiles), static_cast<unsigned>(a.kv.heads));
   const bool sh = a.kv.v == a.kv.k;
   CUtensorMap k_map = {}, v_map = {};
