@@ -88,6 +88,16 @@ __device__ __forceinline__ void tma_load_page(void* dst, const CUtensorMap* map,
       : "memory");
 }
 
+// One lane of a converged warp.  The products are issued under this instruction's
+// predicate rather than a lane test: their operands live in uniform registers, and
+// only here does the compiler know that a single lane is active.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t e;
+  asm volatile("{.reg .pred p; elect.sync _|p, 0xffffffff; selp.u32 %0, 1, 0, p;}" : "=r"(e));
+  return e != 0;
+}
+// Descriptors are a base plus an offset of their low word (16-byte units of shared memory).
+__device__ __forceinline__ uint64_t desc_at(uint64_t base, uint32_t bytes) { return base + (bytes >> 4); }
 __device__ __forceinline__ void mma_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc,
                                        uint32_t accumulate) {
   asm volatile(
@@ -414,71 +424,89 @@ __global__ void __launch_bounds__(kThreads, 1) paged_window_kernel(const Params 
       }
     } else {
       // ------------------------------------------------------------ products
-      if (lane == 0) {
-        constexpr uint32_t idesc_s = idesc_of<T>(128, KT, false), idesc_o = idesc_of<T>(128, D, true);
-        const RowTile rt[2] = {RowTile(wk, 0, p.G, p.window, p.sinks), RowTile(wk, 1, p.G, p.window, p.sinks)};
-        const uint32_t q0 = smem_u32(smem + L::Q), k0 = smem_u32(sK), v0 = smem_u32(sV);
-        uint32_t p_phase[2] = {0, 0};                  // bit h: parity of p_full[w][h]
-        bool started[2] = {false, false};
-        int k_seen = -1, v_seen = -1;                  // last tile whose arrival was waited for
-        bool ok = mbar_wait(q_full, 0, abort_flag, p.kv.err);
-        auto scores = [&](int w, int j) {
-          if (k_seen < j) {
-            ok = ok && mbar_wait(k_full + j % L::KST, (j / L::KST) & 1, abort_flag, p.kv.err);
-            k_seen = j;
-            tc_fence_after();
-          }
-          if (!ok) return;
-          const uint32_t a = q0 + w * L::TILE, bk = k0 + (j % L::KST) * L::TILE;
+      constexpr uint32_t idesc_s = idesc_of<T>(128, KT, false), idesc_o = idesc_of<T>(128, D, true);
+      const RowTile rt[2] = {RowTile(wk, 0, p.G, p.window, p.sinks), RowTile(wk, 1, p.G, p.window, p.sinks)};
+      const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
+      const uint64_t q_desc = desc_kmajor_sw128(smem_u32(smem + L::Q)), k_desc = desc_kmajor_sw128(smem_u32(sK));
+      const uint64_t v_desc = desc_mnmajor_sw128(smem_u32(sV), L::BLK, 1024);
+      uint32_t p_phase = 0;                            // bit 2 w + h: parity of p_full[w][h]
+      uint32_t started = 0;                            // bit w: the output has its first product
+      int k_seen = -1, v_seen = -1;                    // last tile whose arrival was waited for
+      auto wait = [&](uint64_t* at, uint32_t parity) {
+        return __all_sync(0xffffffffu, mbar_wait(at, parity, abort_flag, p.kv.err));
+      };
+      bool ok = wait(q_full, 0);
+      auto scores = [&](int w, int j) {
+        if (k_seen < j) {
+          ok = ok && wait(k_full + j % L::KST, (j / L::KST) & 1);
+          k_seen = j;
+          tc_fence_after();
+        }
+        if (!ok) return;
+        const uint64_t a = desc_at(q_desc, w * L::TILE), bk = desc_at(k_desc, (j % L::KST) * L::TILE);
+        if (elect_one()) {
 #pragma unroll
           for (int kk = 0; kk < D / 16; ++kk)
-            mma_bf16(tmem + w * 128, desc_kmajor_sw128(a + (kk >> 2) * L::BLK + (kk & 3) * 32),
-                     desc_kmajor_sw128(bk + (kk >> 2) * L::BLK + (kk & 3) * 32), idesc_s, kk != 0);
+            mma_bf16(tm + w * 128, desc_at(a, (kk >> 2) * L::BLK + (kk & 3) * 32),
+                     desc_at(bk, (kk >> 2) * L::BLK + (kk & 3) * 32), idesc_s, kk != 0);
           mma_commit(s_full + w);
-        };
-        uint32_t act[2] = {0, 0}, next[2] = {0, 0};
-        if (wk.tiles > 0) {
-          for (int w = 0; w < 2; ++w) {
-            next[w] = rt[w].blocks(wk, 0);
-            if (next[w]) scores(w, 0);
-          }
-          if (!SHARED && ok) mma_commit(k_empty);
         }
-        for (int j = 0; j < wk.tiles && ok; ++j) {
-          const uint32_t bv = v0 + (j % VS) * L::TILE;
-          for (int w = 0; w < 2 && ok; ++w) {
-            act[w] = next[w];
-            next[w] = j + 1 < wk.tiles ? rt[w].blocks(wk, j + 1) : 0u;
-            for (int half = 0; half < 2 && ok; ++half) {
-              const uint32_t mine = (act[w] >> (2 * half)) & 3u;
-              if (mine == 0) continue;
-              ok = mbar_wait(p_full + 2 * w + half, (p_phase[w] >> half) & 1, abort_flag, p.kv.err);
-              p_phase[w] ^= 1u << half;
-              if (ok && v_seen < j) {
-                ok = mbar_wait(v_full + j % VS, (j / VS) & 1, abort_flag, p.kv.err);
-                v_seen = j;
-              }
-              if (!ok) break;
-              tc_fence_after();
+        __syncwarp();
+      };
+      uint32_t next[2] = {0, 0};
+      if (wk.tiles > 0) {
+        for (int w = 0; w < 2; ++w) {
+          next[w] = rt[w].blocks(wk, 0);
+          if (next[w]) scores(w, 0);
+        }
+        if (!SHARED && ok && elect_one()) mma_commit(k_empty);
+        __syncwarp();
+      }
+      for (int j = 0; j < wk.tiles && ok; ++j) {
+        const uint64_t bv = desc_at(v_desc, (j % VS) * L::TILE);
 #pragma unroll
-              for (int i = 0; i < 4; ++i) {            // 16 keys per product
-                if (!((mine >> (i >> 1)) & 1u)) continue;
-                const int kk = 4 * half + i;
-                mma_ts(tmem + O_COL + w * 128, tmem + w * 128 + kk * 8,
-                       desc_mnmajor_sw128(bv + kk * 2048, L::BLK, 1024), idesc_o, started[w]);
-                started[w] = true;
+        for (int w = 0; w < 2; ++w) {
+          if (!ok) break;
+          const uint32_t act = next[w];
+          next[w] = j + 1 < wk.tiles ? rt[w].blocks(wk, j + 1) : 0u;
+#pragma unroll
+          for (int half = 0; half < 2; ++half) {
+            const uint32_t mine = (act >> (2 * half)) & 3u;
+            if (mine == 0 || !ok) continue;
+            ok = wait(p_full + 2 * w + half, (p_phase >> (2 * w + half)) & 1);
+            p_phase ^= 1u << (2 * w + half);
+            if (ok && v_seen < j) {
+              ok = wait(v_full + j % VS, (j / VS) & 1);
+              v_seen = j;
+            }
+            if (!ok) continue;
+            tc_fence_after();
+            if (elect_one()) {
+#pragma unroll
+              for (int c = 0; c < 2; ++c) {            // 16 keys per product, a block at a time
+                if (!((mine >> c) & 1u)) continue;
+                const int kk = 4 * half + 2 * c;
+                const uint32_t more = ((started >> w) & 1u) | (c & mine);   // the output has its first product
+                mma_ts(tm + O_COL + w * 128, tm + w * 128 + kk * 8, desc_at(bv, kk * 2048), idesc_o, more);
+                mma_ts(tm + O_COL + w * 128, tm + w * 128 + kk * 8 + 8, desc_at(bv, kk * 2048 + 2048), idesc_o, 1u);
               }
             }
-            if (act[w]) mma_commit(pv_done + w);
-            if (!ok) break;
-            if (w == 1) mma_commit(v_empty + j % VS);  // both tiles are past this one's values
-            if (next[w]) scores(w, j + 1);
-            if (!SHARED && w == 1 && j + 1 < wk.tiles && ok) mma_commit(k_empty + (j + 1) % L::KST);
+            __syncwarp();
+            started |= 1u << w;
           }
+          if (!ok) break;
+          if (elect_one()) {
+            if (act) mma_commit(pv_done + w);
+            if (w == 1) mma_commit(v_empty + j % VS);  // both tiles are past this one's values
+          }
+          __syncwarp();
+          if (next[w]) scores(w, j + 1);
+          if (!SHARED && w == 1 && j + 1 < wk.tiles && ok && elect_one()) mma_commit(k_empty + (j + 1) % L::KST);
+          __syncwarp();
         }
-        // completes once every product issued above has, also when a wait gave up
-        mma_commit(all_done);
       }
+      // completes once every product issued above has, also when a wait gave up
+      if (elect_one()) mma_commit(all_done);
       __syncwarp();
     }
   } else {
