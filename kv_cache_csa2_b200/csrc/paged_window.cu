@@ -8,10 +8,10 @@
 //                   scores from TMEM, writes the weights back there as 16-bit
 //                   pairs (the next product's left operand), and at the end
 //                   divides and stores the output
-//   warp 8          issues S = Q K^T (M=128, N=128, K=D) and O += P V (M=128,
-//                   N=D, K=keys), tile 0 and 1 in turn, so that one tile's
-//                   softmax runs under the other's products
-//   warps 9-11      bring the key and value rows into the 128-byte swizzled layout,
+//   warps 8, 9      issue row tile 0's / 1's S = Q K^T (M=128, N=128, K=D) and
+//                   O += P V (M=128, N=D, K=keys); one tile's softmax runs under the
+//                   other's products (one warp for both spent its time issuing)
+//   warps 10, 11    bring the key and value rows into the 128-byte swizzled layout,
 //                   32 tokens at a time: TMA boxes of a page when all 32 are wanted
 //                   and pages hold at least 8 tokens, else cp.async row by row with
 //                   zeros for the rest (what lies past a sequence's end may be
@@ -58,7 +58,7 @@ struct Lay {
   static constexpr int K = Q + 2 * TILE;
   static constexpr int V = K + KST * TILE;
   static constexpr int BAR = V + VST * TILE;
-  static constexpr int NBAR = 2 * KST + 2 * VST + 2 + 4 + 2 + 1 + 1;
+  static constexpr int NBAR = 2 * KST + 2 * VST + 2 + 4 + 2 + 1;
   static constexpr int BITS = BAR + NBAR * 8;
   static constexpr int MISC = BITS + kBits * 4 * 4;
   static constexpr int BYTES = MISC + 16 + 1024;
@@ -246,9 +246,8 @@ __global__ void __launch_bounds__(kThreads, 1) paged_window_kernel(const Params 
   uint64_t* v_empty = SHARED ? k_empty : v_full + L::VST;
   uint64_t* s_full = bar + 2 * L::KST + 2 * L::VST;    // [2]
   uint64_t* p_full = s_full + 2;                       // [2][2]: one per half of a tile
-  uint64_t* pv_done = p_full + 4;                      // [2]
-  uint64_t* all_done = pv_done + 2;
-  uint64_t* q_full = all_done + 1;
+  uint64_t* all_done = p_full + 4;                     // [2]: every product of the row tile has ended
+  uint64_t* q_full = all_done + 2;
   constexpr int VS = SHARED ? L::KST : L::VST;
   uint32_t* bits = reinterpret_cast<uint32_t*>(smem + L::BITS);       // [kBits][4]: tokens present
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + L::MISC);
@@ -265,19 +264,18 @@ __global__ void __launch_bounds__(kThreads, 1) paged_window_kernel(const Params 
   if (threadIdx.x == 0) {
     for (int i = 0; i < L::KST; ++i) {
       mbar_init(k_full + i, 4);                        // one arrival per block
-      mbar_init(k_empty + i, 1);
+      mbar_init(k_empty + i, 2);                       // one per row tile
     }
     for (int i = 0; i < L::VST; ++i) {
       mbar_init(v_full + i, 4);
-      mbar_init(v_empty + i, 1);
+      mbar_init(v_empty + i, 2);
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(s_full + i, 1);
       mbar_init(p_full + 2 * i, 4);
       mbar_init(p_full + 2 * i + 1, 4);
-      mbar_init(pv_done + i, 1);
+      mbar_init(all_done + i, 1);
     }
-    mbar_init(all_done, 1);
     mbar_init(q_full, 8);
     *abort_flag = 0;
     fence_mbar_init();
@@ -294,9 +292,9 @@ __global__ void __launch_bounds__(kThreads, 1) paged_window_kernel(const Params 
   // registers: 168 x 384 threads at launch = 208 x 256 (softmax) + 88 x 128 (the rest)
   if (warp >= 8) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
-    if (warp > 8) {
+    if (warp > 9) {
       // ------------------------------------------------------------ loaders
-      // unit u = (key tile u / 4, its block u % 4); the three warps in turn
+      // unit u = (key tile u / 4, its block u % 4); the two warps in turn
       const int units = 4 * wk.tiles;
       auto token_of = [&](int u) { return wk.tile_start(u >> 2) + (u & 3) * KB + lane; };
       auto wanted = [&](int u) {                       // this lane's token is seen by some row
@@ -311,11 +309,11 @@ __global__ void __launch_bounds__(kThreads, 1) paged_window_kernel(const Params 
       constexpr int HALVES = SHARED ? 1 : 2;
       constexpr int CH = FP4 ? D / 32 : D / 8;           // 16-byte pieces of a row
       uint64_t* waiting = nullptr;                       // copies issued, not yet announced
-      int64_t row = row_of(warp - 9);
+      int64_t row = row_of(warp - 10);
       bool ok = true;
-      for (int u = warp - 9; u < units && ok; u += 3) {
+      for (int u = warp - 10; u < units && ok; u += 2) {
         const int tile = u >> 2, r0 = (u & 3) * 32;
-        const int64_t next = row_of(u + 3);
+        const int64_t next = row_of(u + 2);
         const uint32_t want = __ballot_sync(0xffffffffu, wanted(u));
         const uint32_t lost = __ballot_sync(0xffffffffu, row < 0) & want;    // its page is outside the pool
         const bool empty_block = want == 0;            // its columns are never used
@@ -424,89 +422,78 @@ __global__ void __launch_bounds__(kThreads, 1) paged_window_kernel(const Params 
       }
     } else {
       // ------------------------------------------------------------ products
+      const int w = warp - 8;
       constexpr uint32_t idesc_s = idesc_of<T>(128, KT, false), idesc_o = idesc_of<T>(128, D, true);
-      const RowTile rt[2] = {RowTile(wk, 0, p.G, p.window, p.sinks), RowTile(wk, 1, p.G, p.window, p.sinks)};
-      const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
-      const uint64_t q_desc = desc_kmajor_sw128(smem_u32(smem + L::Q)), k_desc = desc_kmajor_sw128(smem_u32(sK));
+      const RowTile rt(wk, w, p.G, p.window, p.sinks);
+      const uint32_t s_at = __shfl_sync(0xffffffffu, tmem, 0) + w * 128, o_at = s_at + O_COL;
+      const uint64_t q_desc = desc_kmajor_sw128(smem_u32(smem + L::Q + w * L::TILE)), k_desc = desc_kmajor_sw128(smem_u32(sK));
       const uint64_t v_desc = desc_mnmajor_sw128(smem_u32(sV), L::BLK, 1024);
-      uint32_t p_phase = 0;                            // bit 2 w + h: parity of p_full[w][h]
-      uint32_t started = 0;                            // bit w: the output has its first product
-      int k_seen = -1, v_seen = -1;                    // last tile whose arrival was waited for
+      uint32_t p_phase = 0;                            // bit h: parity of p_full[w][h]
+      uint32_t started = 0;                            // the output has its first product
       auto wait = [&](uint64_t* at, uint32_t parity) {
         return __all_sync(0xffffffffu, mbar_wait(at, parity, abort_flag, p.kv.err));
       };
-      bool ok = wait(q_full, 0);
-      auto scores = [&](int w, int j) {
-        if (k_seen < j) {
-          ok = ok && wait(k_full + j % L::KST, (j / L::KST) & 1);
-          k_seen = j;
-          tc_fence_after();
-        }
-        if (!ok) return;
-        const uint64_t a = desc_at(q_desc, w * L::TILE), bk = desc_at(k_desc, (j % L::KST) * L::TILE);
-        if (elect_one()) {
+      auto scores = [&](int j) {                       // called by one lane
+        const uint64_t bk = desc_at(k_desc, (j % L::KST) * L::TILE);
 #pragma unroll
-          for (int kk = 0; kk < D / 16; ++kk)
-            mma_bf16(tm + w * 128, desc_at(a, (kk >> 2) * L::BLK + (kk & 3) * 32),
-                     desc_at(bk, (kk >> 2) * L::BLK + (kk & 3) * 32), idesc_s, kk != 0);
-          mma_commit(s_full + w);
-        }
-        __syncwarp();
+        for (int kk = 0; kk < D / 16; ++kk)
+          mma_bf16(s_at, desc_at(q_desc, (kk >> 2) * L::BLK + (kk & 3) * 32),
+                   desc_at(bk, (kk >> 2) * L::BLK + (kk & 3) * 32), idesc_s, kk != 0);
+        mma_commit(s_full + w);
       };
-      uint32_t next[2] = {0, 0};
-      if (wk.tiles > 0) {
-        for (int w = 0; w < 2; ++w) {
-          next[w] = rt[w].blocks(wk, 0);
-          if (next[w]) scores(w, 0);
+      uint32_t next = wk.tiles > 0 ? rt.blocks(wk, 0) : 0u;
+      bool ok = wait(q_full, 0);
+      if (wk.tiles > 0 && ok) {
+        ok = wait(k_full, 0);
+        tc_fence_after();
+        if (ok && elect_one()) {
+          if (next) scores(0);
+          if (!SHARED) mma_commit(k_empty);
         }
-        if (!SHARED && ok && elect_one()) mma_commit(k_empty);
         __syncwarp();
       }
       for (int j = 0; j < wk.tiles && ok; ++j) {
         const uint64_t bv = desc_at(v_desc, (j % VS) * L::TILE);
+        const uint32_t act = next;
+        const bool more = j + 1 < wk.tiles;
+        next = more ? rt.blocks(wk, j + 1) : 0u;
+        ok = wait(v_full + j % VS, (j / VS) & 1);
+        auto values = [&](int half) {                  // called by one lane: 16 keys per product
+          const uint32_t mine = (act >> (2 * half)) & 3u;
 #pragma unroll
-        for (int w = 0; w < 2; ++w) {
-          if (!ok) break;
-          const uint32_t act = next[w];
-          next[w] = j + 1 < wk.tiles ? rt[w].blocks(wk, j + 1) : 0u;
-#pragma unroll
-          for (int half = 0; half < 2; ++half) {
-            const uint32_t mine = (act >> (2 * half)) & 3u;
-            if (mine == 0 || !ok) continue;
-            ok = wait(p_full + 2 * w + half, (p_phase >> (2 * w + half)) & 1);
-            p_phase ^= 1u << (2 * w + half);
-            if (ok && v_seen < j) {
-              ok = wait(v_full + j % VS, (j / VS) & 1);
-              v_seen = j;
-            }
-            if (!ok) continue;
-            tc_fence_after();
-            if (elect_one()) {
-#pragma unroll
-              for (int c = 0; c < 2; ++c) {            // 16 keys per product, a block at a time
-                if (!((mine >> c) & 1u)) continue;
-                const int kk = 4 * half + 2 * c;
-                const uint32_t more = ((started >> w) & 1u) | (c & mine);   // the output has its first product
-                mma_ts(tm + O_COL + w * 128, tm + w * 128 + kk * 8, desc_at(bv, kk * 2048), idesc_o, more);
-                mma_ts(tm + O_COL + w * 128, tm + w * 128 + kk * 8 + 8, desc_at(bv, kk * 2048 + 2048), idesc_o, 1u);
-              }
-            }
-            __syncwarp();
-            started |= 1u << w;
+          for (int c = 0; c < 2; ++c) {
+            if (!((mine >> c) & 1u)) continue;
+            const int kk = 4 * half + 2 * c;
+            mma_ts(o_at, s_at + kk * 8, desc_at(bv, kk * 2048), idesc_o, started | (c & mine));
+            mma_ts(o_at, s_at + kk * 8 + 8, desc_at(bv, kk * 2048 + 2048), idesc_o, 1u);
           }
-          if (!ok) break;
-          if (elect_one()) {
-            if (act) mma_commit(pv_done + w);
-            if (w == 1) mma_commit(v_empty + j % VS);  // both tiles are past this one's values
-          }
+        };
+        if (ok && (act & 3u)) {
+          ok = wait(p_full + 2 * w, p_phase & 1);
+          p_phase ^= 1u;
+          tc_fence_after();
+          if (ok && elect_one()) values(0);
           __syncwarp();
-          if (next[w]) scores(w, j + 1);
-          if (!SHARED && w == 1 && j + 1 < wk.tiles && ok && elect_one()) mma_commit(k_empty + (j + 1) % L::KST);
-          __syncwarp();
+          started = 1u;
         }
+        if (ok && more) ok = wait(k_full + (j + 1) % L::KST, ((j + 1) / L::KST) & 1);
+        if (ok && (act & 12u)) {
+          ok = wait(p_full + 2 * w + 1, p_phase >> 1);
+          p_phase ^= 2u;
+        }
+        if (!ok) break;
+        tc_fence_after();
+        if (elect_one()) {
+          if (act & 12u) values(1);
+          mma_commit(v_empty + j % VS);                // this row tile is past the tile's values
+          if (next) scores(j + 1);
+          if (!SHARED && more) mma_commit(k_empty + (j + 1) % L::KST);
+        }
+        __syncwarp();
+        if (act & 12u) started = 1u;
       }
       // completes once every product issued above has, also when a wait gave up
-      if (elect_one()) mma_commit(all_done);
+      if (elect_one()) mma_commit(all_done + w);
       __syncwarp();
     }
   } else {
@@ -661,7 +648,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_window_kernel(const Params 
       ++turn;
     }
     if (turn > 0 && ok) {
-      ok = mbar_wait(pv_done + w, (turn - 1) & 1, abort_flag, p.kv.err);
+      ok = mbar_wait(all_done + w, 0, abort_flag, p.kv.err);
       ok = __all_sync(0xffffffffu, ok);
       tc_fence_after();
     }
@@ -697,6 +684,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_window_kernel(const Params 
   // every product has completed before TMEM and shared memory go
   volatile int never = 0;                              // also when a wait gave up: the products still end
   mbar_wait(all_done, 0, &never, p.kv.err);
+  mbar_wait(all_done + 1, 0, &never, p.kv.err);
   tc_fence_before();
   __syncthreads();
   if (warp == 8) {
