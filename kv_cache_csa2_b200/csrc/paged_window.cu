@@ -8,9 +8,8 @@
 //                   scores from TMEM, writes the weights back there as 16-bit
 //                   pairs (the next product's left operand), and at the end
 //                   divides and stores the output
-//   warps 8, 9      issue row tile 0's / 1's S = Q K^T (M=128, N=128, K=D) and
-//                   O += P V (M=128, N=D, K=keys); one tile's softmax runs under the
-//                   other's products (one warp for both spent its time issuing)
+//   warps 8, 9      issue row tile 0's / 1's S = Q K^T (M=128, N=64, K=D) and
+//                   O += P V (M=128, N=D, K=64), half a key tile at a time
 //   warps 10, 11    bring the key and value rows into the 128-byte swizzled layout,
 //                   32 tokens at a time: TMA boxes of a page when all 32 are wanted
 //                   and pages hold at least 8 tokens, else cp.async row by row with
@@ -21,10 +20,13 @@
 // by more than 2^8 since its last reference (its weights then exceed 1 by at
 // most that, which neither type nor the f32 sums mind).
 //
-// Key tiles are aligned to 128 tokens, and within a tile the blocks of 32 tokens
-// that no row of the row tile sees are skipped; neither touches a row's sums, so
-// its bits depend on its own tokens only.  The weights are handed on in halves, so
-// the products with the values start while the second half is still exponentials.
+// A row tile's scores have two buffers of 64 columns, one per half of a key tile:
+// the tensor cores fill one while the softmax works on the other, whose weights
+// take the place of its scores.  (With one buffer of 128 columns the softmax stood
+// still for both products of every tile: 3950 clocks per key tile, of which 2200
+// were softmax.)  Tiles are aligned to 128 tokens, and within a half the blocks of
+// 32 tokens that no row of the row tile sees are skipped; neither touches a row's
+// sums, so its bits depend on its own tokens only.
 //
 // Bound: 4 D flops per (row, key) on the tensor cores against one exponential,
 // 16 of which an SM does per clock: at D = 128 both take 1024 clocks per pair of
@@ -43,6 +45,7 @@ using rope::Num;
 
 constexpr int kThreads = 384;
 constexpr int KT = 128;                                // keys per tile
+constexpr int HT = 64;                                 // keys per half of a tile: one buffer of scores
 constexpr int KB = 32;                                 // keys per block
 constexpr int RT = 128;                                // rows per row tile
 constexpr int kBits = 8;                               // slots of the presence words
@@ -58,7 +61,7 @@ struct Lay {
   static constexpr int K = Q + 2 * TILE;
   static constexpr int V = K + KST * TILE;
   static constexpr int BAR = V + VST * TILE;
-  static constexpr int NBAR = 2 * KST + 2 * VST + 2 + 4 + 2 + 1;
+  static constexpr int NBAR = 2 * KST + 2 * VST + 4 + 4 + 4 + 2 + 1;
   static constexpr int BITS = BAR + NBAR * 8;
   static constexpr int MISC = BITS + kBits * 4 * 4;
   static constexpr int BYTES = MISC + 16 + 1024;
@@ -244,9 +247,10 @@ __global__ void __launch_bounds__(kThreads, 1) paged_window_kernel(const Params 
   uint64_t* k_empty = k_full + L::KST;
   uint64_t* v_full = SHARED ? k_full : k_empty + L::KST;
   uint64_t* v_empty = SHARED ? k_empty : v_full + L::VST;
-  uint64_t* s_full = bar + 2 * L::KST + 2 * L::VST;    // [2]
-  uint64_t* p_full = s_full + 2;                       // [2][2]: one per half of a tile
-  uint64_t* all_done = p_full + 4;                     // [2]: every product of the row tile has ended
+  uint64_t* s_full = bar + 2 * L::KST + 2 * L::VST;    // [2][2]: row tile, half
+  uint64_t* p_full = s_full + 4;                       // [2][2]
+  uint64_t* pv_done = p_full + 4;                      // [2][2]
+  uint64_t* all_done = pv_done + 4;                    // [2]: every product of the row tile has ended
   uint64_t* q_full = all_done + 2;
   constexpr int VS = SHARED ? L::KST : L::VST;
   uint32_t* bits = reinterpret_cast<uint32_t*>(smem + L::BITS);       // [kBits][4]: tokens present
@@ -271,9 +275,11 @@ __global__ void __launch_bounds__(kThreads, 1) paged_window_kernel(const Params 
       mbar_init(v_empty + i, 2);
     }
     for (int i = 0; i < 2; ++i) {
-      mbar_init(s_full + i, 1);
-      mbar_init(p_full + 2 * i, 4);
-      mbar_init(p_full + 2 * i + 1, 4);
+      for (int h = 0; h < 2; ++h) {
+        mbar_init(s_full + 2 * i + h, 1);
+        mbar_init(p_full + 2 * i + h, 4);
+        mbar_init(pv_done + 2 * i + h, 1);
+      }
       mbar_init(all_done + i, 1);
     }
     mbar_init(q_full, 8);
@@ -423,7 +429,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_window_kernel(const Params 
     } else {
       // ------------------------------------------------------------ products
       const int w = warp - 8;
-      constexpr uint32_t idesc_s = idesc_of<T>(128, KT, false), idesc_o = idesc_of<T>(128, D, true);
+      constexpr uint32_t idesc_s = idesc_of<T>(128, HT, false), idesc_o = idesc_of<T>(128, D, true);
       const RowTile rt(wk, w, p.G, p.window, p.sinks);
       const uint32_t s_at = __shfl_sync(0xffffffffu, tmem, 0) + w * 128, o_at = s_at + O_COL;
       const uint64_t q_desc = desc_kmajor_sw128(smem_u32(smem + L::Q + w * L::TILE)), k_desc = desc_kmajor_sw128(smem_u32(sK));
@@ -433,13 +439,13 @@ __global__ void __launch_bounds__(kThreads, 1) paged_window_kernel(const Params 
       auto wait = [&](uint64_t* at, uint32_t parity) {
         return __all_sync(0xffffffffu, mbar_wait(at, parity, abort_flag, p.kv.err));
       };
-      auto scores = [&](int j) {                       // called by one lane
-        const uint64_t bk = desc_at(k_desc, (j % L::KST) * L::TILE);
+      auto scores = [&](int j, int h) {                // called by one lane
+        const uint64_t bk = desc_at(k_desc, (j % L::KST) * L::TILE + h * HT * 128);
 #pragma unroll
         for (int kk = 0; kk < D / 16; ++kk)
-          mma_bf16(s_at, desc_at(q_desc, (kk >> 2) * L::BLK + (kk & 3) * 32),
+          mma_bf16(s_at + h * HT, desc_at(q_desc, (kk >> 2) * L::BLK + (kk & 3) * 32),
                    desc_at(bk, (kk >> 2) * L::BLK + (kk & 3) * 32), idesc_s, kk != 0);
-        mma_commit(s_full + w);
+        mma_commit(s_full + 2 * w + h);
       };
       uint32_t next = wk.tiles > 0 ? rt.blocks(wk, 0) : 0u;
       bool ok = wait(q_full, 0);
@@ -447,7 +453,8 @@ __global__ void __launch_bounds__(kThreads, 1) paged_window_kernel(const Params 
         ok = wait(k_full, 0);
         tc_fence_after();
         if (ok && elect_one()) {
-          if (next) scores(0);
+          if (next & 3u) scores(0, 0);
+          if (next & 12u) scores(0, 1);
           if (!SHARED) mma_commit(k_empty);
         }
         __syncwarp();
@@ -458,39 +465,32 @@ __global__ void __launch_bounds__(kThreads, 1) paged_window_kernel(const Params 
         const bool more = j + 1 < wk.tiles;
         next = more ? rt.blocks(wk, j + 1) : 0u;
         ok = wait(v_full + j % VS, (j / VS) & 1);
-        auto values = [&](int half) {                  // called by one lane: 16 keys per product
-          const uint32_t mine = (act >> (2 * half)) & 3u;
-#pragma unroll
-          for (int c = 0; c < 2; ++c) {
-            if (!((mine >> c) & 1u)) continue;
-            const int kk = 4 * half + 2 * c;
-            mma_ts(o_at, s_at + kk * 8, desc_at(bv, kk * 2048), idesc_o, started | (c & mine));
-            mma_ts(o_at, s_at + kk * 8 + 8, desc_at(bv, kk * 2048 + 2048), idesc_o, 1u);
-          }
-        };
-        if (ok && (act & 3u)) {
-          ok = wait(p_full + 2 * w, p_phase & 1);
-          p_phase ^= 1u;
-          tc_fence_after();
-          if (ok && elect_one()) values(0);
-          __syncwarp();
-          started = 1u;
-        }
         if (ok && more) ok = wait(k_full + (j + 1) % L::KST, ((j + 1) / L::KST) & 1);
-        if (ok && (act & 12u)) {
-          ok = wait(p_full + 2 * w + 1, p_phase >> 1);
-          p_phase ^= 2u;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const uint32_t mine = (act >> (2 * h)) & 3u;
+          if (ok && mine) {
+            ok = wait(p_full + 2 * w + h, (p_phase >> h) & 1);
+            p_phase ^= 1u << h;
+          }
+          if (!ok) break;
+          tc_fence_after();
+          if (elect_one()) {
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {              // 16 keys per product, a block at a time
+              if (!((mine >> c) & 1u)) continue;
+              const int kk = 4 * h + 2 * c;
+              mma_ts(o_at, s_at + h * HT + c * 16, desc_at(bv, kk * 2048), idesc_o, started | (c & mine));
+              mma_ts(o_at, s_at + h * HT + c * 16 + 8, desc_at(bv, kk * 2048 + 2048), idesc_o, 1u);
+            }
+            if (mine) mma_commit(pv_done + 2 * w + h);
+            if (h == 1) mma_commit(v_empty + j % VS);  // this row tile is past the tile's values
+            if ((next >> (2 * h)) & 3u) scores(j + 1, h);
+            if (!SHARED && h == 1 && more) mma_commit(k_empty + (j + 1) % L::KST);
+          }
+          __syncwarp();
+          if (mine) started = 1u;
         }
-        if (!ok) break;
-        tc_fence_after();
-        if (elect_one()) {
-          if (act & 12u) values(1);
-          mma_commit(v_empty + j % VS);                // this row tile is past the tile's values
-          if (next) scores(j + 1);
-          if (!SHARED && more) mma_commit(k_empty + (j + 1) % L::KST);
-        }
-        __syncwarp();
-        if (act & 12u) started = 1u;
       }
       // completes once every product issued above has, also when a wait gave up
       if (elect_one()) mma_commit(all_done + w);
@@ -531,27 +531,23 @@ __global__ void __launch_bounds__(kThreads, 1) paged_window_kernel(const Params 
     const int sink_end = min(p.sinks, pos + 1);
     float m = -INFINITY;
     float2 l = make_float2(0.0f, 0.0f);
-    uint32_t turn = 0;                                 // tiles done
-    bool ok = true;
-    for (int j = 0; j < wk.tiles && ok; ++j) {
-      const uint32_t act = rt.blocks(wk, j);
-      if (act == 0) continue;
-      ok = mbar_wait(s_full + w, turn & 1, abort_flag, p.kv.err);
-      ok = __all_sync(0xffffffffu, ok);
-      if (!ok) break;
-      tc_fence_after();
-      const int t0 = wk.tile_start(j);
-      const volatile uint32_t* here = bits + (j % kBits) * 4;
-      // the reference stays while the maximum has not outgrown it; else the output
-      // so far is rescaled (its products ended before this tile's scores did)
-      auto refer = [&](float top) -> float {
-        const bool grow = top > m + kLazy || (m == -INFINITY && top > -INFINITY);
-        if (__any_sync(0xffffffffu, grow)) {
-          const bool scale_o = grow && m > -INFINITY;
-          if (__any_sync(0xffffffffu, scale_o)) {
-            const float f = scale_o ? exp2_approx(m - top) : 1.0f;
-            l.x *= f;
-            l.y *= f;
+    uint32_t phase = 0, pv_phase = 0;                  // bit h: parity of s_full[w][h], of pv_done[w][h]
+    int last = 0;                                      // half handed on last
+    bool any = false, ok = true;
+    // The reference stays while the maximum has not outgrown it; else the output so
+    // far is rescaled, once the products of the half handed on last have ended.
+    auto refer = [&](float top) -> float {
+      const bool grow = top > m + kLazy || (m == -INFINITY && top > -INFINITY);
+      if (__any_sync(0xffffffffu, grow)) {
+        const bool scale_o = grow && m > -INFINITY;
+        if (__any_sync(0xffffffffu, scale_o)) {
+          const float f = scale_o ? exp2_approx(m - top) : 1.0f;
+          l.x *= f;
+          l.y *= f;
+          ok = __all_sync(0xffffffffu, mbar_wait(pv_done + 2 * w + last, ((pv_phase >> last) & 1) ^ 1, abort_flag,
+                                                  p.kv.err));
+          if (ok) {
+            tc_fence_after();
 #pragma unroll 1
             for (int i = 0; i < D / 16; ++i) {
               uint32_t x[16];
@@ -562,73 +558,84 @@ __global__ void __launch_bounds__(kThreads, 1) paged_window_kernel(const Params 
               tmem_st16(o_at + i * 16, x);
             }
           }
-          if (grow) m = top;
         }
-        return m == -INFINITY ? 0.0f : m;
-      };
-      auto hand_on = [&](int half) {                   // this half of the weights is complete
-        tmem_wait_st();
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(p_full + 2 * w + half);
-      };
-      const bool plain = act == 15u && t0 >= win && t0 + KT - 1 <= pos && (here[0] & here[1] & here[2] & here[3]) == 0xffffffffu;
-      if (__all_sync(0xffffffffu, plain)) {
-        // every row sees the whole tile: its 128 scores stay in registers
-        float s[KT];
-#pragma unroll
-        for (int c = 0; c < 4; ++c) tmem_ld32(s_at + c * KB, *reinterpret_cast<uint32_t(*)[32]>(s + c * KB));
-        tmem_wait_ld();
-        float mx[4] = {s[0], s[1], s[2], s[3]};
-#pragma unroll
-        for (int i = 4; i < KT - 4; i += 8)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) mx[e] = max3(mx[e], s[i + e], s[i + 4 + e]);
-#pragma unroll
-        for (int e = 0; e < 4; ++e) mx[e] = fmaxf(mx[e], s[KT - 4 + e]);
-        const float ref = refer(fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * p.scale2);
-        const float2 sc = make_float2(p.scale2, p.scale2), nr = make_float2(-ref, -ref);
-#pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          uint32_t pk[16];
-#pragma unroll
-          for (int i = 0; i < 16; ++i) {
-            const float2 x = fma2(make_float2(s[c * KB + 2 * i], s[c * KB + 2 * i + 1]), sc, nr);
-            const float2 e = make_float2(exp2_approx(x.x), exp2_approx(x.y));
-            l = add2(l, e);
-            pk[i] = Num<T>::down(e.x, e.y);
-          }
-          tmem_st16(s_at + c * 16, pk);
-          if (c & 1) hand_on(c >> 1);
-        }
-      } else {
-        // block by block, read twice (the weights of block c land on scores of block
-        // c / 2, which have been read)
-        auto visible = [&](int c) -> uint32_t {        // bit i: token i of the block
-          const int t = t0 + c * KB;
-          auto upto = [](int n) -> uint32_t { return n <= 0 ? 0u : n >= 32 ? 0xffffffffu : (1u << n) - 1u; };
-          return ((upto(pos + 1 - t) & ~upto(win - t)) | upto(sink_end - t)) & here[c];
-        };
-        float top = -INFINITY;
+        if (grow) m = top;
+      }
+      return m == -INFINITY ? 0.0f : m;
+    };
+    for (int j = 0; j < wk.tiles && ok; ++j) {
+      const uint32_t act = rt.blocks(wk, j);
+      const int t0 = wk.tile_start(j);
+      const volatile uint32_t* here = bits + (j % kBits) * 4;
 #pragma unroll 1
-        for (int c = 0; c < 4; ++c) {
-          if (!((act >> c) & 1u)) continue;
-          uint32_t v[KB];
-          tmem_ld32(s_at + c * KB, v);
-          const uint32_t vis = visible(c);
+      for (int h = 0; h < 2; ++h) {
+        const uint32_t mine = (act >> (2 * h)) & 3u;
+        if (mine == 0) continue;
+        const int th = t0 + h * HT;
+        const uint32_t sh = s_at + h * HT;
+        ok = mbar_wait(s_full + 2 * w + h, (phase >> h) & 1, abort_flag, p.kv.err);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+        phase ^= 1u << h;
+        any = true;
+        tc_fence_after();
+        const bool plain = mine == 3u && th >= win && th + HT - 1 <= pos && (here[2 * h] & here[2 * h + 1]) == 0xffffffffu;
+        if (__all_sync(0xffffffffu, plain)) {
+          // every row sees all 64: the scores stay in registers
+          float s[HT];
+          tmem_ld32(sh, *reinterpret_cast<uint32_t(*)[32]>(s));
+          tmem_ld32(sh + KB, *reinterpret_cast<uint32_t(*)[32]>(s + KB));
           tmem_wait_ld();
-          float mx[2] = {-INFINITY, -INFINITY};
+          float mx[4] = {s[0], s[1], s[2], s[3]};
 #pragma unroll
-          for (int i = 0; i < KB; ++i) mx[i & 1] = fmaxf(mx[i & 1], (vis >> i) & 1u ? __uint_as_float(v[i]) : -INFINITY);
-          top = fmaxf(top, fmaxf(mx[0], mx[1]));
-        }
-        const float ref = refer(top * p.scale2);
-        const float2 sc = make_float2(p.scale2, p.scale2), nr = make_float2(-ref, -ref);
+          for (int i = 4; i < HT - 4; i += 8)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) mx[e] = max3(mx[e], s[i + e], s[i + 4 + e]);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) mx[e] = fmaxf(mx[e], s[HT - 4 + e]);
+          const float ref = refer(fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * p.scale2);
+          const float2 sc = make_float2(p.scale2, p.scale2), nr = make_float2(-ref, -ref);
+#pragma unroll
+          for (int c = 0; c < 2; ++c) {
+            uint32_t pk[16];
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+              const float2 x = fma2(make_float2(s[c * KB + 2 * i], s[c * KB + 2 * i + 1]), sc, nr);
+              const float2 e = make_float2(exp2_approx(x.x), exp2_approx(x.y));
+              l = add2(l, e);
+              pk[i] = Num<T>::down(e.x, e.y);
+            }
+            tmem_st16(sh + c * 16, pk);
+          }
+        } else {
+          // block by block, read twice (the weights of block 1 land on block 0's
+          // scores, which have been read)
+          auto visible = [&](int c) -> uint32_t {      // bit i: token i of the block
+            const int t = th + c * KB;
+            auto upto = [](int n) -> uint32_t { return n <= 0 ? 0u : n >= 32 ? 0xffffffffu : (1u << n) - 1u; };
+            return ((upto(pos + 1 - t) & ~upto(win - t)) | upto(sink_end - t)) & here[2 * h + c];
+          };
+          float top = -INFINITY;
 #pragma unroll 1
-        for (int c = 0; c < 4; ++c) {
-          if ((act >> c) & 1u) {
+          for (int c = 0; c < 2; ++c) {
+            if (!((mine >> c) & 1u)) continue;
+            uint32_t v[KB];
+            tmem_ld32(sh + c * KB, v);
+            const uint32_t vis = visible(c);
+            tmem_wait_ld();
+            float mx[2] = {-INFINITY, -INFINITY};
+#pragma unroll
+            for (int i = 0; i < KB; ++i)
+              mx[i & 1] = fmaxf(mx[i & 1], (vis >> i) & 1u ? __uint_as_float(v[i]) : -INFINITY);
+            top = fmaxf(top, fmaxf(mx[0], mx[1]));
+          }
+          const float ref = refer(top * p.scale2);
+          const float2 sc = make_float2(p.scale2, p.scale2), nr = make_float2(-ref, -ref);
+#pragma unroll 1
+          for (int c = 0; c < 2; ++c) {
+            if (!((mine >> c) & 1u)) continue;
             uint32_t v[KB], pk[16];
-            tmem_ld32(s_at + c * KB, v);
+            tmem_ld32(sh + c * KB, v);
             const uint32_t vis = visible(c);
             tmem_wait_ld();
 #pragma unroll
@@ -640,14 +647,19 @@ __global__ void __launch_bounds__(kThreads, 1) paged_window_kernel(const Params 
               l = add2(l, e);
               pk[i] = Num<T>::down(e.x, e.y);
             }
-            tmem_st16(s_at + c * 16, pk);
+            tmem_st16(sh + c * 16, pk);
           }
-          if ((c & 1) && ((act >> (c - 1)) & 3u)) hand_on(c >> 1);
         }
+        if (!ok) break;
+        tmem_wait_st();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(p_full + 2 * w + h);
+        pv_phase ^= 1u << h;
+        last = h;
       }
-      ++turn;
     }
-    if (turn > 0 && ok) {
+    if (any && ok) {
       ok = mbar_wait(all_done + w, 0, abort_flag, p.kv.err);
       ok = __all_sync(0xffffffffu, ok);
       tc_fence_after();
@@ -659,7 +671,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_window_kernel(const Params 
 #pragma unroll
       for (int c = 0; c < D / 32; ++c) {
         uint32_t v[32];
-        if (turn > 0) {
+        if (any) {
           tmem_ld32(o_at + c * 32, v);
           tmem_wait_ld();
         } else {
