@@ -10,12 +10,13 @@
 //                   divides and stores the output
 //   warps 8, 9      issue row tile 0's / 1's S = Q K^T (M=128, N=64, K=D) and
 //                   O += P V (M=128, N=D, K=64), half a key tile at a time
-//   warps 10, 11    bring the key and value rows into the 128-byte swizzled layout,
-//                   32 tokens at a time: TMA boxes of a page when all 32 are wanted
-//                   and pages hold at least 8 tokens, else cp.async row by row with
-//                   zeros for the rest (what lies past a sequence's end may be
-//                   anything, and a weight of 0 does not silence a NaN); FP4 rows are
-//                   dequantised on the way
+//   warps 10-15     bring the key (even warps) and value rows into the 128-byte
+//                   swizzled layout.  16-bit rows in pages of at least 8 tokens: one
+//                   warp each, a TMA box per lane.  Boxes of values that hold unwanted
+//                   tokens are copied row by row with zeros in their place (what lies
+//                   past a sequence's end may be anything, and a weight of 0 does not
+//                   silence a NaN).  Smaller pages go row by row by cp.async, FP4 rows
+//                   are dequantised on the way, by three warps each.
 // The output stays in TMEM; it is rescaled only when a row's maximum has grown
 // by more than 2^8 since its last reference (its weights then exceed 1 by at
 // most that, which neither type nor the f32 sums mind).
@@ -43,7 +44,7 @@ using namespace paged;
 using namespace sm100;
 using rope::Num;
 
-constexpr int kThreads = 384;
+constexpr int kThreads = 512;
 constexpr int KT = 128;                                // keys per tile
 constexpr int HT = 64;                                 // keys per half of a tile: one buffer of scores
 constexpr int KB = 32;                                 // keys per block
@@ -267,11 +268,11 @@ __global__ void __launch_bounds__(kThreads, 1) paged_window_kernel(const Params 
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < L::KST; ++i) {
-      mbar_init(k_full + i, 4);                        // one arrival per block
+      mbar_init(k_full + i, p.box ? 1 : 4);            // TMA: per tile; else per block
       mbar_init(k_empty + i, 2);                       // one per row tile
     }
     for (int i = 0; i < L::VST; ++i) {
-      mbar_init(v_full + i, 4);
+      mbar_init(v_full + i, p.box ? 1 : 4);
       mbar_init(v_empty + i, 2);
     }
     for (int i = 0; i < 2; ++i) {
@@ -295,95 +296,139 @@ __global__ void __launch_bounds__(kThreads, 1) paged_window_kernel(const Params 
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
   constexpr uint32_t O_COL = 256;                      // S / P of tile w at 128 w, O at 256 + 128 w
-  // registers: 168 x 384 threads at launch = 208 x 256 (softmax) + 88 x 128 (the rest)
+  // registers: 128 x 512 threads at launch = 168 x 256 (softmax) + 88 x 256 (the rest)
   if (warp >= 8) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
     if (warp > 9) {
       // ------------------------------------------------------------ loaders
-      // unit u = (key tile u / 4, its block u % 4); the two warps in turn
-      const int units = 4 * wk.tiles;
-      auto token_of = [&](int u) { return wk.tile_start(u >> 2) + (u & 3) * KB + lane; };
-      auto wanted = [&](int u) {                       // this lane's token is seen by some row
-        const int j = token_of(u);
-        return u < units && j <= wk.pmax && (j >= wk.lo || j < wk.ns);
+      const int half = (warp - 10) & 1, group = (warp - 10) >> 1;       // keys or values; which of three
+      const int ring = half ? VS : L::KST;
+      const uint8_t* src = half ? p.kv.v : p.kv.k;
+      uint8_t* const dst0 = half ? sV : sK;
+      uint64_t *const fulls = half ? v_full : k_full, *const empties = half ? v_empty : k_empty;
+      auto wait = [&](uint64_t* at, uint32_t parity) {
+        return __all_sync(0xffffffffu, mbar_wait(at, parity, abort_flag, p.kv.err));
       };
-      auto row_of = [&](int u) -> int64_t {
-        if (!wanted(u)) return -1;
-        const int64_t r = token_row(p.kv, wk.b, token_of(u));
+      auto wanted = [&](int j) { return j <= wk.pmax && (j >= wk.lo || j < wk.ns); };   // seen by some row
+      // channel offset of a wanted token, -1 when its page is outside the pool
+      auto row_of = [&](int j) -> int64_t {
+        const int64_t r = token_row(p.kv, wk.b, j);
         return r < 0 ? -1 : r + kvh * p.kv.head_stride;
       };
-      constexpr int HALVES = SHARED ? 1 : 2;
-      constexpr int CH = FP4 ? D / 32 : D / 8;           // 16-byte pieces of a row
-      uint64_t* waiting = nullptr;                       // copies issued, not yet announced
-      int64_t row = row_of(warp - 10);
       bool ok = true;
-      for (int u = warp - 10; u < units && ok; u += 2) {
-        const int tile = u >> 2, r0 = (u & 3) * 32;
-        const int64_t next = row_of(u + 2);
-        const uint32_t want = __ballot_sync(0xffffffffu, wanted(u));
-        const uint32_t lost = __ballot_sync(0xffffffffu, row < 0) & want;    // its page is outside the pool
-        const bool empty_block = want == 0;            // its columns are never used
-        // a whole unit: boxes of p.box rows and 64 channels, one per lane
-        const bool whole = !FP4 && p.box > 0 && __all_sync(0xffffffffu, row >= 0);
+      if (SHARED && half == 1) {
+        // the keys are the values
+      } else if (p.box > 0) {
+        // lane i: channels 64 (i % BLKS) of the box of rows (i / BLKS) * p.box of each tile
         constexpr int BLKS = D / 64;
-        const int boxes = whole ? 32 / p.box * BLKS : 0;
-        int box_page = 0, box_slot = 0;
-        if (lane < boxes) {
-          const int j = wk.tile_start(tile) + r0 + lane / BLKS * p.box;
-          box_page = __ldg(p.kv.table + wk.b * p.kv.table_stride + (j >> p.kv.page_shift));
-          box_slot = j & ((1 << p.kv.page_shift) - 1);
-        }
-#pragma unroll
-        for (int half = 0; half < HALVES; ++half) {
-          const int ring = half ? VS : L::KST, st = tile % ring;
-          uint8_t* dst = (half ? sV : sK) + st * L::TILE;
-          const uint8_t* src = half ? p.kv.v : p.kv.k;
-          uint64_t* full = (half ? v_full : k_full) + st;
-          uint64_t* empty = (half ? v_empty : k_empty) + st;
-          const uint32_t parity = ((tile / ring) & 1) ^ 1;
-          // do not hold back what has landed while the stage is still in use
-          if (waiting && !__all_sync(0xffffffffu, mbar_try_wait(empty, parity))) {
+        const int br = lane / BLKS * p.box;
+        const bool mine = group == 0 && br < KT;
+        auto some = [&](int a, int n) { return a <= wk.pmax && (a + n > wk.lo || a < wk.ns); };
+        auto page_of = [&](int tile) -> int {
+          if (!mine || tile >= wk.tiles || !some(wk.tile_start(tile) + br, p.box)) return -1;
+          const int pg = __ldg(p.kv.table + wk.b * p.kv.table_stride + ((wk.tile_start(tile) + br) >> p.kv.page_shift));
+          if (pg >= 0 && pg < p.kv.n_pages) return pg;
+          raise_dev_error(p.kv.err, DEVERR_BOUNDS);
+          return -1;
+        };
+        int page = page_of(0);
+        for (int tile = 0; tile < (group == 0 ? wk.tiles : 0) && ok; ++tile) {
+          const int next = page_of(tile + 1);
+          const int st = tile % ring, t0 = wk.tile_start(tile), a = t0 + br;
+          uint8_t* dst = dst0 + st * L::TILE;
+          const bool any = mine && some(a, p.box);
+          const bool all = any && ((a >= wk.lo && a + p.box - 1 <= wk.pmax) || a + p.box <= wk.ns);
+          const bool lost = any && page < 0;
+          // values: what a block of 32 that is seen holds besides whole boxes goes row by row
+          const bool clean = half == 1 || SHARED;
+          const bool box = any && !lost && (all || !clean);
+          const uint32_t boxes = __ballot_sync(0xffffffffu, box);
+          uint32_t rows = __ballot_sync(0xffffffffu, clean && mine && !box && lane % BLKS == 0 && some(a & ~(KB - 1), KB));
+          const bool some_lost = __any_sync(0xffffffffu, lost);
+          ok = wait(empties + st, ((tile / ring) & 1) ^ 1);
+          if (!ok) break;
+          if (half == 0) {
+            // tokens present, 32 to a word
+#pragma unroll 1
+            for (int c = 0; c < 4; ++c) {
+              uint32_t here = 0xffffffffu;
+              if (some_lost) {
+                const int j = t0 + c * KB + lane;
+                here = ~__ballot_sync(0xffffffffu, wanted(j) && row_of(j) < 0);
+              }
+              if (lane == 0) bits[(tile % kBits) * 4 + c] = here;
+            }
+          }
+          if (rows) {
+            for (; rows; rows &= rows - 1) {
+              const int r0 = (__ffs(rows) - 1) / BLKS * p.box;
+              for (int i = lane; i < p.box * (D / 8); i += 32) {
+                const int r = r0 + i / (D / 8), c = i % (D / 8);
+                const int64_t at = wanted(t0 + r) ? row_of(t0 + r) : -1;
+                cp_async_16(dst + (c / 8) * L::BLK + sw128_offset(r, c % 8), src + (at < 0 ? 0 : at * 2 + c * 16),
+                            at < 0 ? 0u : 16u);
+              }
+            }
+            cp_async_commit();
             cp_async_wait<0>();
             fence_proxy_async_smem();
             __syncwarp();
-            if (lane == 0) mbar_arrive(waiting);
-            waiting = nullptr;
           }
-          if (empty_block) {
-            ok = __all_sync(0xffffffffu, mbar_wait(empty, parity, abort_flag, p.kv.err));
+          if (lane == 0) mbar_arrive_expect_tx(fulls + st, __popc(boxes) * p.box * 128);
+          __syncwarp();
+          if (box)
+            tma_load_page(dst + (lane % BLKS) * L::BLK + br * 128, half ? &v_map : &k_map, fulls + st, (lane % BLKS) * 64,
+                          kvh, a & ((1 << p.kv.page_shift) - 1), page);
+          __syncwarp();
+          page = next;
+        }
+      } else {
+        // block u % 4 of tile u / 4, three warps in turn
+        constexpr int CH = FP4 ? D / 32 : D / 8;       // 16-byte pieces of a row
+        const int units = 4 * wk.tiles;
+        auto lane_row = [&](int u) -> int64_t {
+          if (u >= units) return -1;
+          const int j = wk.tile_start(u >> 2) + (u & 3) * KB + lane;
+          return wanted(j) ? row_of(j) : -1;
+        };
+        uint64_t* waiting = nullptr;                   // copies issued, not yet announced
+        auto announce = [&](int keep) {                // the copies before the last `keep` groups have landed
+          if (keep)
+            cp_async_wait<1>();
+          else
+            cp_async_wait<0>();
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(waiting);
+          waiting = nullptr;
+        };
+        int64_t row = lane_row(group);
+        for (int u = group; u < units && ok; u += 3) {
+          const int tile = u >> 2, r0 = (u & 3) * KB, st = tile % ring;
+          const int64_t next = lane_row(u + 3);
+          const bool want = wanted(wk.tile_start(tile) + r0 + lane);
+          const uint32_t lost = __ballot_sync(0xffffffffu, want && row < 0);
+          const bool none = !__any_sync(0xffffffffu, want);              // its columns are never used
+          uint8_t* dst = dst0 + st * L::TILE;
+          const uint32_t parity = ((tile / ring) & 1) ^ 1;
+          if (!FP4) {
+            // do not hold back what has landed while the stage is still in use
+            if (waiting && !__all_sync(0xffffffffu, mbar_try_wait(empties + st, parity))) announce(0);
+            ok = wait(empties + st, parity);
             if (!ok) break;
-            if (lane == 0) mbar_arrive(full);
-          } else if (!FP4) {
-            ok = mbar_wait(empty, parity, abort_flag, p.kv.err);
-            ok = __all_sync(0xffffffffu, ok);
-            if (!ok) break;
-            if (whole) {
-              if (lane == 0) {
-                if (half == 0) bits[(tile % kBits) * 4 + (u & 3)] = 0xffffffffu;
-                mbar_arrive_expect_tx(full, 32 * D * 2);
-              }
-              __syncwarp();
-              if (lane < boxes)
-                tma_load_page(dst + (lane % BLKS) * L::BLK + (r0 + lane / BLKS * p.box) * 128, half ? &v_map : &k_map,
-                              full, (lane % BLKS) * 64, kvh, box_slot, box_page);
-              continue;
-            }
+            if (!none) {
 #pragma unroll 8
-            for (int i = 0; i < CH; ++i) {
-              const int piece = i * 32 + lane, r = piece / CH, c = piece % CH;
-              const int64_t at = __shfl_sync(0xffffffffu, row, r);
-              cp_async_16(dst + (c / 8) * L::BLK + sw128_offset(r0 + r, c % 8), src + (at < 0 ? 0 : at * 2 + c * 16),
-                          at < 0 ? 0u : 16u);
+              for (int i = 0; i < CH; ++i) {
+                const int piece = i * 32 + lane, r = piece / CH, c = piece % CH;
+                const int64_t at = __shfl_sync(0xffffffffu, row, r);
+                cp_async_16(dst + (c / 8) * L::BLK + sw128_offset(r0 + r, c % 8), src + (at < 0 ? 0 : at * 2 + c * 16),
+                            at < 0 ? 0u : 16u);
+              }
             }
             cp_async_commit();
             if (half == 0 && lane == 0) bits[(tile % kBits) * 4 + (u & 3)] = ~lost;
-            if (waiting) {
-              cp_async_wait<1>();
-              fence_proxy_async_smem();
-              __syncwarp();
-              if (lane == 0) mbar_arrive(waiting);
-            }
-            waiting = full;
+            if (waiting) announce(1);
+            waiting = fulls + st;
           } else {
             const uint8_t* sc = half ? p.kv.v_scales : p.kv.k_scales;
             uint4 w[CH];
@@ -399,8 +444,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_window_kernel(const Params 
                 s2[i] = __ldg(reinterpret_cast<const uint16_t*>(sc + at / 16) + c);
               }
             }
-            ok = mbar_wait(empty, parity, abort_flag, p.kv.err);
-            ok = __all_sync(0xffffffffu, ok);
+            ok = wait(empties + st, parity);
             if (!ok) break;
 #pragma unroll
             for (int i = 0; i < CH; ++i) {
@@ -415,16 +459,11 @@ __global__ void __launch_bounds__(kThreads, 1) paged_window_kernel(const Params 
             if (half == 0 && lane == 0) bits[(tile % kBits) * 4 + (u & 3)] = ~lost;
             fence_proxy_async_smem();
             __syncwarp();
-            if (lane == 0) mbar_arrive(full);
+            if (lane == 0) mbar_arrive(fulls + st);
           }
+          row = next;
         }
-        row = next;
-      }
-      if (!FP4) {
-        cp_async_wait<0>();
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (waiting && lane == 0) mbar_arrive(waiting);
+        if (waiting) announce(0);
       }
     } else {
       // ------------------------------------------------------------ products
@@ -465,7 +504,6 @@ __global__ void __launch_bounds__(kThreads, 1) paged_window_kernel(const Params 
         const bool more = j + 1 < wk.tiles;
         next = more ? rt.blocks(wk, j + 1) : 0u;
         ok = wait(v_full + j % VS, (j / VS) & 1);
-        if (ok && more) ok = wait(k_full + (j + 1) % L::KST, ((j + 1) / L::KST) & 1);
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
           const uint32_t mine = (act >> (2 * h)) & 3u;
@@ -485,6 +523,14 @@ __global__ void __launch_bounds__(kThreads, 1) paged_window_kernel(const Params 
             }
             if (mine) mma_commit(pv_done + 2 * w + h);
             if (h == 1) mma_commit(v_empty + j % VS);  // this row tile is past the tile's values
+          }
+          __syncwarp();
+          if (h == 0 && more) {
+            ok = wait(k_full + (j + 1) % L::KST, ((j + 1) / L::KST) & 1);
+            if (!ok) break;
+            tc_fence_after();
+          }
+          if (elect_one()) {
             if ((next >> (2 * h)) & 3u) scores(j + 1, h);
             if (!SHARED && h == 1 && more) mma_commit(k_empty + (j + 1) % L::KST);
           }
@@ -498,7 +544,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_window_kernel(const Params 
     }
   } else {
     // ------------------------------------------------------------ softmax and output
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 168;");
     const int w = warp >> 2, quad = warp & 3;
     const int r = quad * 32 + lane;                    // row of the tile = TMEM lane
     const uint32_t lane_off = static_cast<uint32_t>(quad * 32) << 16;
@@ -506,19 +552,23 @@ __global__ void __launch_bounds__(kThreads, 1) paged_window_kernel(const Params 
     const bool live = w * RT + r < wk.n_rows;
     const int rr = wk.r0 + w * RT + r, tok = rr / p.G, head = kvh * p.G + (rr - tok * p.G);
     {
-      // this thread's q row (zero past the last) into the K-major swizzled tile
-      const uint4* src = reinterpret_cast<const uint4*>(p.q + (static_cast<int64_t>(wk.q_row0) + tok) * p.q_token +
-                                                        head * p.q_head);
-      uint4 v[D / 8];
+      // the warp's 32 q rows (zero past the last) into the K-major swizzled tile
+      const int64_t mine = live ? (static_cast<int64_t>(wk.q_row0) + tok) * p.q_token + head * p.q_head : -1;
+      constexpr int CH = D / 8;
+      uint4 v[CH];
 #pragma unroll
-      for (int c = 0; c < D / 8; ++c) v[c] = live ? __ldg(src + c) : make_uint4(0, 0, 0, 0);
+      for (int i = 0; i < CH; ++i) {
+        const int64_t at = __shfl_sync(0xffffffffu, mine, (i * 32 + lane) / CH);
+        v[i] = at >= 0 ? __ldg(reinterpret_cast<const uint4*>(p.q + at) + lane % CH) : make_uint4(0, 0, 0, 0);
+      }
 #pragma unroll
-      for (int c = 0; c < D / 8; ++c) {
-        v[c].x ^= p.flip;
-        v[c].y ^= p.flip;
-        v[c].z ^= p.flip;
-        v[c].w ^= p.flip;
-        *reinterpret_cast<uint4*>(smem + L::Q + w * L::TILE + (c / 8) * L::BLK + sw128_offset(r, c % 8)) = v[c];
+      for (int i = 0; i < CH; ++i) {
+        const int row = quad * 32 + (i * 32 + lane) / CH, c = lane % CH;
+        v[i].x ^= p.flip;
+        v[i].y ^= p.flip;
+        v[i].z ^= p.flip;
+        v[i].w ^= p.flip;
+        *reinterpret_cast<uint4*>(smem + L::Q + w * L::TILE + (c / 8) * L::BLK + sw128_offset(row, c % 8)) = v[i];
       }
       fence_proxy_async_smem();
       __syncwarp();

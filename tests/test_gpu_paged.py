@@ -302,6 +302,24 @@ def test_window_bits_do_not_depend_on_batch_or_cut(kind, D, G, window):
     assert torch.equal(o, out[-77:]) and torch.equal(l, lse[-77:])
 
 
+@pytest.mark.parametrize("D,page,shared", [(64, 8, False), (128, 16, False), (128, 32, True), (128, 2, False)])
+def test_window_ignores_what_ran_before(D, page, shared):
+    """A launch over NaN values leaves them in shared memory; the next one, whose window starts
+    inside a block of tokens and whose pages end inside it, must not see them."""
+    cache, host = P.make_cache("bf16", [300], page, 1, D, shared=shared, seed=87)
+    q = P.rng_normal(88, 40, 8, D)
+    cu = torch.tensor([0, 40], dtype=torch.int32, device="cuda")
+    bad = K.PagedKv(torch.full_like(cache.k, float("nan")), cache.table, cache.lens,
+                    v=None if shared else torch.full_like(cache.k, float("nan")))
+    wide = P.rng_normal(89, 40 * 32, 8, D)                           # every SM
+    many = K.PagedKv(bad.k, cache.table.expand(32, -1).contiguous(), cache.lens.expand(32).contiguous(), v=bad.v)
+    for window, sinks in ((53, 0), (70, 3), (0, 0), (17, 9)):
+        K.csa2_paged_window_attn(wide, torch.arange(33, dtype=torch.int32, device="cuda") * 40, many, 0.1)
+        out, lse = K.csa2_paged_window_attn(q, cu, cache, 0.1, window=window, sinks=sinks)
+        want = O.causal_attn(P.f64(q), np.arange(260, 300), *host[0], 0.1, window, sinks)
+        P.check_attn(out, lse, want, P.f64(q), host[0][0], 0.1, torch.bfloat16, 300)
+
+
 def test_window_bad_cu_q():
     cache, _ = P.make_cache("bf16", [50, 50, 50], 16, 1, 64, seed=85)
     q = P.rng_normal(86, 40, 2, 64)
