@@ -69,6 +69,10 @@ csa2_status launch_paged_decode_stream(const PagedAttn& a, int chunk, int chunks
 csa2_status make_tensor_map_paged(CUtensorMap* map, const void* base, int dim, int heads, int64_t head_stride,
                                   int page_size, int64_t token_stride, int64_t n_pages, int64_t page_stride,
                                   int box_rows);
+// Tensor map of rows of heads as [token][head][channel]: a box is 64 channels of
+// box_heads heads of box_tokens tokens.
+csa2_status make_tensor_map_heads(CUtensorMap* map, const void* base, int dim, int heads, int64_t head_stride,
+                                  int64_t tokens, int64_t token_stride, int box_heads, int box_tokens);
 // Prompt attention on the tensor cores, rows of 64 or 128 channels (paged_window.cu).
 bool paged_window_tc_applies(const PagedAttn& a);
 csa2_status launch_paged_window_tc(const PagedAttn& a, const int32_t* cu_q, int64_t T, cudaStream_t stream);

@@ -116,5 +116,28 @@ __device__ __forceinline__ bool sees(int p, int j, int window, int sinks) {
   return j <= p && (window <= 0 || p - j < window || j < sinks);
 }
 
+// sm100::mbar_wait for a converged warp, with a short first look and the clock
+// read only every 64 looks.  All lanes look: electing one to do it cost 190
+// clocks more per wait in the prompt kernel (330 us against 274).
+__device__ __forceinline__ bool wait_slow(uint64_t* bar, uint32_t parity, volatile int* abort, int* err) {
+  const uint64_t t0 = sm100::globaltimer_ns();
+  while (true) {
+#pragma unroll 1
+    for (int i = 0; i < 64; ++i)
+      if (sm100::mbar_try_wait(bar, parity)) return true;
+    if (*abort) return false;
+    if (sm100::globaltimer_ns() - t0 > 2000000000ull) {
+      raise_dev_error(err, DEVERR_TIMEOUT);
+      *abort = 1;
+      return false;
+    }
+  }
+}
+__device__ __forceinline__ bool wait_phase(uint64_t* bar, uint32_t parity, volatile int* abort, int* err) {
+  bool ok = true;
+  if (!sm100::mbar_try_wait(bar, parity)) ok = wait_slow(bar, parity, abort, err);
+  return __all_sync(0xffffffffu, ok);
+}
+
 }  // namespace paged
 }  // namespace csa2

@@ -12,11 +12,11 @@
 //                   O += P V (M=128, N=D, K=64), half a key tile at a time
 //   warps 10-15     bring the key (even warps) and value rows into the 128-byte
 //                   swizzled layout.  16-bit rows in pages of at least 8 tokens: one
-//                   warp each, a TMA box per lane.  Boxes of values that hold unwanted
-//                   tokens are copied row by row with zeros in their place (what lies
-//                   past a sequence's end may be anything, and a weight of 0 does not
-//                   silence a NaN).  Smaller pages go row by row by cp.async, FP4 rows
-//                   are dequantised on the way, by three warps each.
+//                   warp each, a TMA box per lane; value rows of unwanted tokens are
+//                   zeroed before the tile is announced (what lies past a sequence's
+//                   end may be anything, and a weight of 0 does not silence a NaN).
+//                   Smaller pages go row by row by cp.async, FP4 rows are dequantised
+//                   on the way, by three warps each.
 // The output stays in TMEM; it is rescaled only when a row's maximum has grown
 // by more than 2^8 since its last reference (its weights then exceed 1 by at
 // most that, which neither type nor the f32 sums mind).
@@ -62,7 +62,7 @@ struct Lay {
   static constexpr int K = Q + 2 * TILE;
   static constexpr int V = K + KST * TILE;
   static constexpr int BAR = V + VST * TILE;
-  static constexpr int NBAR = 2 * KST + 2 * VST + 4 + 4 + 4 + 2 + 1;
+  static constexpr int NBAR = 2 * KST + 2 * VST + 4 + 4 + 4 + 2 + 1 + 1;
   static constexpr int BITS = BAR + NBAR * 8;
   static constexpr int MISC = BITS + kBits * 4 * 4;
   static constexpr int BYTES = MISC + 16 + 1024;
@@ -79,6 +79,7 @@ struct Params {
   uint32_t flip;                     // 0x80008000 for a negative scale: q's signs turn
   int Hq, G, window, sinks;
   int box;                           // rows of a TMA box (0: none)
+  int q_tokens;                      // tokens of a row tile's TMA box of q (0: rows are loaded one by one)
   PagedView kv;
 };
 
@@ -102,6 +103,14 @@ __device__ __forceinline__ bool elect_one() {
 }
 // Descriptors are a base plus an offset of their low word (16-byte units of shared memory).
 __device__ __forceinline__ uint64_t desc_at(uint64_t base, uint32_t bytes) { return base + (bytes >> 4); }
+// A row tile's q rows: channels c .. c + 63 of the G heads of some tokens.
+__device__ __forceinline__ void tma_load_q(void* dst, const CUtensorMap* map, uint64_t* bar, int c, int head, int token) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(smem_u32(dst)),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(c), "r"(head), "r"(token)
+      : "memory");
+}
 __device__ __forceinline__ void mma_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc,
                                        uint32_t accumulate) {
   asm volatile(
@@ -239,7 +248,8 @@ __device__ bool locate(const Params& p, int64_t index, Work& w) {
 
 template <class T, int D, bool FP4, bool SHARED>
 __global__ void __launch_bounds__(kThreads, 1) paged_window_kernel(const Params p, const __grid_constant__ CUtensorMap k_map,
-                                                               const __grid_constant__ CUtensorMap v_map) {
+                                                               const __grid_constant__ CUtensorMap v_map,
+                                                               const __grid_constant__ CUtensorMap q_map) {
   using L = Lay<D, SHARED>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -253,6 +263,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_window_kernel(const Params 
   uint64_t* pv_done = p_full + 4;                      // [2][2]
   uint64_t* all_done = pv_done + 4;                    // [2]: every product of the row tile has ended
   uint64_t* q_full = all_done + 2;
+  uint64_t* fix_bar = q_full + 1;                      // boxes that need rows zeroed
   constexpr int VS = SHARED ? L::KST : L::VST;
   uint32_t* bits = reinterpret_cast<uint32_t*>(smem + L::BITS);       // [kBits][4]: tokens present
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + L::MISC);
@@ -283,7 +294,8 @@ __global__ void __launch_bounds__(kThreads, 1) paged_window_kernel(const Params 
       }
       mbar_init(all_done + i, 1);
     }
-    mbar_init(q_full, 8);
+    mbar_init(q_full, p.q_tokens ? 1 : 8);
+    mbar_init(fix_bar, 1);
     *abort_flag = 0;
     fence_mbar_init();
   }
@@ -296,9 +308,13 @@ __global__ void __launch_bounds__(kThreads, 1) paged_window_kernel(const Params 
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
   constexpr uint32_t O_COL = 256;                      // S / P of tile w at 128 w, O at 256 + 128 w
-  // registers: 128 x 512 threads at launch = 168 x 256 (softmax) + 88 x 256 (the rest)
+  // registers: 128 x 512 threads at launch = 176 x 256 (softmax) + 80 x 256 (the
+  // rest); the warps that dequantise FP4 rows need more
   if (warp >= 8) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
+    if (FP4)
+      asm volatile("setmaxnreg.dec.sync.aligned.u32 112;");
+    else
+      asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
     if (warp > 9) {
       // ------------------------------------------------------------ loaders
       const int half = (warp - 10) & 1, group = (warp - 10) >> 1;       // keys or values; which of three
@@ -307,7 +323,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_window_kernel(const Params 
       uint8_t* const dst0 = half ? sV : sK;
       uint64_t *const fulls = half ? v_full : k_full, *const empties = half ? v_empty : k_empty;
       auto wait = [&](uint64_t* at, uint32_t parity) {
-        return __all_sync(0xffffffffu, mbar_wait(at, parity, abort_flag, p.kv.err));
+        return wait_phase(at, parity, abort_flag, p.kv.err);
       };
       auto wanted = [&](int j) { return j <= wk.pmax && (j >= wk.lo || j < wk.ns); };   // seen by some row
       // channel offset of a wanted token, -1 when its page is outside the pool
@@ -332,6 +348,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_window_kernel(const Params 
           return -1;
         };
         int page = page_of(0);
+        uint32_t fixes = 0;                            // tiles with rows to zero so far
         for (int tile = 0; tile < (group == 0 ? wk.tiles : 0) && ok; ++tile) {
           const int next = page_of(tile + 1);
           const int st = tile % ring, t0 = wk.tile_start(tile), a = t0 + br;
@@ -339,47 +356,49 @@ __global__ void __launch_bounds__(kThreads, 1) paged_window_kernel(const Params 
           const bool any = mine && some(a, p.box);
           const bool all = any && ((a >= wk.lo && a + p.box - 1 <= wk.pmax) || a + p.box <= wk.ns);
           const bool lost = any && page < 0;
-          // values: what a block of 32 that is seen holds besides whole boxes goes row by row
+          const bool box = any && !lost;
+          // values: rows to zero, by boxes (what a block of 32 that is seen holds besides wanted rows)
           const bool clean = half == 1 || SHARED;
-          const bool box = any && !lost && (all || !clean);
           const uint32_t boxes = __ballot_sync(0xffffffffu, box);
-          uint32_t rows = __ballot_sync(0xffffffffu, clean && mine && !box && lane % BLKS == 0 && some(a & ~(KB - 1), KB));
+          uint32_t rows = __ballot_sync(0xffffffffu, clean && mine && !(box && all) && lane % BLKS == 0 &&
+                                                         some(a & ~(KB - 1), KB));
           const bool some_lost = __any_sync(0xffffffffu, lost);
           ok = wait(empties + st, ((tile / ring) & 1) ^ 1);
           if (!ok) break;
-          if (half == 0) {
+          if (half == 0 && lane < 4) {
             // tokens present, 32 to a word
-#pragma unroll 1
-            for (int c = 0; c < 4; ++c) {
-              uint32_t here = 0xffffffffu;
-              if (some_lost) {
-                const int j = t0 + c * KB + lane;
-                here = ~__ballot_sync(0xffffffffu, wanted(j) && row_of(j) < 0);
+            uint32_t here = 0xffffffffu;
+            if (some_lost)
+              for (int i = 0; i < KB; ++i) {
+                const int j = t0 + lane * KB + i;
+                if (wanted(j) && row_of(j) < 0) here &= ~(1u << i);
               }
-              if (lane == 0) bits[(tile % kBits) * 4 + c] = here;
-            }
+            bits[(tile % kBits) * 4 + lane] = here;
           }
-          if (rows) {
-            for (; rows; rows &= rows - 1) {
-              const int r0 = (__ffs(rows) - 1) / BLKS * p.box;
-              for (int i = lane; i < p.box * (D / 8); i += 32) {
-                const int r = r0 + i / (D / 8), c = i % (D / 8);
-                const int64_t at = wanted(t0 + r) ? row_of(t0 + r) : -1;
-                cp_async_16(dst + (c / 8) * L::BLK + sw128_offset(r, c % 8), src + (at < 0 ? 0 : at * 2 + c * 16),
-                            at < 0 ? 0u : 16u);
-              }
-            }
-            cp_async_commit();
-            cp_async_wait<0>();
-            fence_proxy_async_smem();
-            __syncwarp();
-          }
-          if (lane == 0) mbar_arrive_expect_tx(fulls + st, __popc(boxes) * p.box * 128);
+          __syncwarp();
+          uint64_t* const bar_at = rows ? fix_bar : fulls + st;
+          if (lane == 0) mbar_arrive_expect_tx(bar_at, __popc(boxes) * p.box * 128);
           __syncwarp();
           if (box)
-            tma_load_page(dst + (lane % BLKS) * L::BLK + br * 128, half ? &v_map : &k_map, fulls + st, (lane % BLKS) * 64,
-                          kvh, a & ((1 << p.kv.page_shift) - 1), page);
+            tma_load_page(dst + (lane % BLKS) * L::BLK + br * 128, half ? &v_map : &k_map, bar_at, (lane % BLKS) * 64, kvh,
+                          a & ((1 << p.kv.page_shift) - 1), page);
           __syncwarp();
+          if (rows) {
+            ok = wait(fix_bar, fixes & 1);
+            ++fixes;
+            if (!ok) break;
+            for (; rows; rows &= rows - 1) {
+              const int src_lane = __ffs(rows) - 1, r0 = src_lane / BLKS * p.box;
+              const bool loaded = (boxes >> src_lane) & 1u;
+              for (int r = r0; r < r0 + p.box; ++r)
+                if (!loaded || !wanted(t0 + r))
+                  if (lane < D / 8)
+                    *reinterpret_cast<uint4*>(dst + (lane / 8) * L::BLK + sw128_offset(r, lane % 8)) = make_uint4(0, 0, 0, 0);
+            }
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(fulls + st);
+          }
           page = next;
         }
       } else {
@@ -476,7 +495,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_window_kernel(const Params 
       uint32_t p_phase = 0;                            // bit h: parity of p_full[w][h]
       uint32_t started = 0;                            // the output has its first product
       auto wait = [&](uint64_t* at, uint32_t parity) {
-        return __all_sync(0xffffffffu, mbar_wait(at, parity, abort_flag, p.kv.err));
+        return wait_phase(at, parity, abort_flag, p.kv.err);
       };
       auto scores = [&](int j, int h) {                // called by one lane
         const uint64_t bk = desc_at(k_desc, (j % L::KST) * L::TILE + h * HT * 128);
@@ -544,21 +563,31 @@ __global__ void __launch_bounds__(kThreads, 1) paged_window_kernel(const Params 
     }
   } else {
     // ------------------------------------------------------------ softmax and output
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 168;");
+    if (FP4)
+      asm volatile("setmaxnreg.inc.sync.aligned.u32 144;");
+    else
+      asm volatile("setmaxnreg.inc.sync.aligned.u32 176;");
     const int w = warp >> 2, quad = warp & 3;
     const int r = quad * 32 + lane;                    // row of the tile = TMEM lane
     const uint32_t lane_off = static_cast<uint32_t>(quad * 32) << 16;
     const uint32_t s_at = tmem + lane_off + w * 128, o_at = tmem + lane_off + O_COL + w * 128;
     const bool live = w * RT + r < wk.n_rows;
     const int rr = wk.r0 + w * RT + r, tok = rr / p.G, head = kvh * p.G + (rr - tok * p.G);
-    {
+    const int64_t q_at = live ? (static_cast<int64_t>(wk.q_row0) + tok) * p.q_token + head * p.q_head : -1;
+    constexpr int CH = D / 8;                          // 16-byte pieces of a row
+    if (p.q_tokens) {
+      // boxes of whole tokens; rows past the last hold other queries, which nobody reads
+      if (threadIdx.x == 0) mbar_arrive_expect_tx(q_full, (wk.n_rows > RT ? 2 : 1) * L::TILE);
+      if (threadIdx.x == 0)
+        for (int i = 0; i < (wk.n_rows > RT ? 2 : 1) * (D / 64); ++i)
+          tma_load_q(smem + L::Q + i * L::BLK, &q_map, q_full, i % (D / 64) * 64, kvh * p.G,
+                     wk.q_row0 + wk.r0 / p.G + i / (D / 64) * p.q_tokens);
+    } else {
       // the warp's 32 q rows (zero past the last) into the K-major swizzled tile
-      const int64_t mine = live ? (static_cast<int64_t>(wk.q_row0) + tok) * p.q_token + head * p.q_head : -1;
-      constexpr int CH = D / 8;
       uint4 v[CH];
 #pragma unroll
       for (int i = 0; i < CH; ++i) {
-        const int64_t at = __shfl_sync(0xffffffffu, mine, (i * 32 + lane) / CH);
+        const int64_t at = __shfl_sync(0xffffffffu, q_at, (i * 32 + lane) / CH);
         v[i] = at >= 0 ? __ldg(reinterpret_cast<const uint4*>(p.q + at) + lane % CH) : make_uint4(0, 0, 0, 0);
       }
 #pragma unroll
@@ -594,8 +623,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_window_kernel(const Params 
           const float f = scale_o ? exp2_approx(m - top) : 1.0f;
           l.x *= f;
           l.y *= f;
-          ok = __all_sync(0xffffffffu, mbar_wait(pv_done + 2 * w + last, ((pv_phase >> last) & 1) ^ 1, abort_flag,
-                                                  p.kv.err));
+          ok = wait_phase(pv_done + 2 * w + last, ((pv_phase >> last) & 1) ^ 1, abort_flag, p.kv.err);
           if (ok) {
             tc_fence_after();
 #pragma unroll 1
@@ -623,8 +651,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_window_kernel(const Params 
         if (mine == 0) continue;
         const int th = t0 + h * HT;
         const uint32_t sh = s_at + h * HT;
-        ok = mbar_wait(s_full + 2 * w + h, (phase >> h) & 1, abort_flag, p.kv.err);
-        ok = __all_sync(0xffffffffu, ok);
+        ok = wait_phase(s_full + 2 * w + h, (phase >> h) & 1, abort_flag, p.kv.err);
         if (!ok) break;
         phase ^= 1u << h;
         any = true;
@@ -710,14 +737,16 @@ __global__ void __launch_bounds__(kThreads, 1) paged_window_kernel(const Params 
       }
     }
     if (any && ok) {
-      ok = mbar_wait(all_done + w, 0, abort_flag, p.kv.err);
-      ok = __all_sync(0xffffffffu, ok);
+      ok = wait_phase(all_done + w, 0, abort_flag, p.kv.err);
       tc_fence_after();
     }
     if (ok) {
       const float sum = l.x + l.y;
       const float inv = sum > 0.0f ? 1.0f / sum : (sum == 0.0f ? 0.0f : sum);
       const int64_t at = (static_cast<int64_t>(wk.q_row0) + tok) * p.Hq + head;
+      // through the row tile's q rows, which no product reads any more, so that a
+      // warp stores whole rows
+      uint8_t* const stage = smem + L::Q + w * L::TILE;
 #pragma unroll
       for (int c = 0; c < D / 32; ++c) {
         uint32_t v[32];
@@ -728,25 +757,32 @@ __global__ void __launch_bounds__(kThreads, 1) paged_window_kernel(const Params 
 #pragma unroll
           for (int i = 0; i < 32; ++i) v[i] = 0;
         }
-        if (live) {
-          uint4* dst = reinterpret_cast<uint4*>(p.out + at * D + c * 32);
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            uint32_t x[4];
+        for (int i = 0; i < 4; ++i) {
+          uint32_t x[4];
 #pragma unroll
-            for (int e = 0; e < 4; ++e)
-              x[e] = Num<T>::down(__uint_as_float(v[8 * i + 2 * e]) * inv, __uint_as_float(v[8 * i + 2 * e + 1]) * inv);
-            dst[i] = make_uint4(x[0], x[1], x[2], x[3]);
-          }
+          for (int e = 0; e < 4; ++e)
+            x[e] = Num<T>::down(__uint_as_float(v[8 * i + 2 * e]) * inv, __uint_as_float(v[8 * i + 2 * e + 1]) * inv);
+          *reinterpret_cast<uint4*>(stage + (c / 2) * L::BLK + sw128_offset(r, (c % 2) * 4 + i)) =
+              make_uint4(x[0], x[1], x[2], x[3]);
         }
+      }
+      __syncwarp();
+      const int64_t out_at = live ? at * D : -1;
+#pragma unroll 4
+      for (int i = 0; i < CH; ++i) {
+        const int row = quad * 32 + (i * 32 + lane) / CH, c = lane % CH;
+        const int64_t to = __shfl_sync(0xffffffffu, out_at, (i * 32 + lane) / CH);
+        const uint4 x = *reinterpret_cast<const uint4*>(stage + (c / 8) * L::BLK + sw128_offset(row, c % 8));
+        if (to >= 0) reinterpret_cast<uint4*>(p.out + to)[c] = x;
       }
       if (live && p.lse) p.lse[at] = sum == 0.0f ? -INFINITY : (m + log2f(sum)) * kLn2;
     }
   }
   // every product has completed before TMEM and shared memory go
   volatile int never = 0;                              // also when a wait gave up: the products still end
-  mbar_wait(all_done, 0, &never, p.kv.err);
-  mbar_wait(all_done + 1, 0, &never, p.kv.err);
+  wait_phase(all_done, 0, &never, p.kv.err);
+  wait_phase(all_done + 1, 0, &never, p.kv.err);
   tc_fence_before();
   __syncthreads();
   if (warp == 8) {
@@ -756,7 +792,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_window_kernel(const Params 
 }
 
 template <class T, int D, bool FP4, bool SHARED>
-csa2_status run(const Params& p, dim3 grid, const CUtensorMap& k_map, const CUtensorMap& v_map, cudaStream_t stream) {
+csa2_status run(const Params& p, dim3 grid, const CUtensorMap (&maps)[3], cudaStream_t stream) {
   using L = Lay<D, SHARED>;
   static PerDevice<int> opted;
   opted.get(+[]() -> int {
@@ -772,7 +808,7 @@ csa2_status run(const Params& p, dim3 grid, const CUtensorMap& k_map, const CUte
   cfg.attrs = at;
   cfg.numAttrs = 1;
   begin_launch(stream);
-  const cudaError_t e = cudaLaunchKernelEx(&cfg, paged_window_kernel<T, D, FP4, SHARED>, p, k_map, v_map);
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, paged_window_kernel<T, D, FP4, SHARED>, p, maps[0], maps[1], maps[2]);
   note_launch(LK_ATTN, 1, stream);
   if (e != cudaSuccess) {
     cudaGetLastError();
@@ -807,16 +843,20 @@ csa2_status launch_paged_window_tc(const PagedAttn& a, const int32_t* cu_q, int6
   if (T * a.G > 0x7fffff00LL || tiles > 0x7fffffffLL) return fail(CSA2_ERR_UNSUPPORTED, "csa2_paged_window_attn: too many rows");
   const dim3 grid(static_cast<unsigned>(tiles), static_cast<unsigned>(a.kv.heads));
   const bool sh = a.kv.v == a.kv.k;
-  CUtensorMap k_map = {}, v_map = {};
+  CUtensorMap maps[3] = {};                            // keys, values, q
   const int page = 1 << a.kv.page_shift;
   if (a.fmt != CSA2_KV_FP4 && page >= 8 && a.kv.n_pages > 0) {
     p.box = std::min(page, 32);
     for (int i = 0; i < (sh ? 1 : 2); ++i)
-      CSA2_TRY(make_tensor_map_paged(i ? &v_map : &k_map, i ? a.kv.v : a.kv.k, a.D, a.kv.heads, a.kv.head_stride, page,
+      CSA2_TRY(make_tensor_map_paged(&maps[i], i ? a.kv.v : a.kv.k, a.D, a.kv.heads, a.kv.head_stride, page,
                                      a.kv.token_stride, a.kv.n_pages, a.kv.page_stride, p.box));
   }
-#define CSA2_WIN_T(T_, D_, F_) \
-  (sh ? run<T_, D_, F_, true>(p, grid, k_map, v_map, stream) : run<T_, D_, F_, false>(p, grid, k_map, v_map, stream))
+  // q by TMA when a row tile is whole tokens and no signs turn
+  if (RT % a.G == 0 && p.flip == 0) {
+    p.q_tokens = RT / a.G;
+    CSA2_TRY(make_tensor_map_heads(&maps[2], a.q, a.D, a.Hq, a.q_head, T, a.q_token, a.G, p.q_tokens));
+  }
+#define CSA2_WIN_T(T_, D_, F_) (sh ? run<T_, D_, F_, true>(p, grid, maps, stream) : run<T_, D_, F_, false>(p, grid, maps, stream))
 #define CSA2_WIN(D_)                                                                       \
   if (a.D == D_)                                                                           \
     return a.fmt == CSA2_KV_FP4   ? CSA2_WIN_T(__nv_bfloat16, D_, true)                    \

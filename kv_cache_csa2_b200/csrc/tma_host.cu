@@ -66,4 +66,22 @@ csa2_status make_tensor_map_paged(CUtensorMap* map, const void* base, int dim, i
   return CSA2_OK;
 }
 
+csa2_status make_tensor_map_heads(CUtensorMap* map, const void* base, int dim, int heads, int64_t head_stride,
+                                  int64_t tokens, int64_t token_stride, int box_heads, int box_tokens) {
+  auto fn = encode_fn();
+  if (!fn) return fail(CSA2_ERR_CUDA, "cuTensorMapEncodeTiled unavailable");
+  const cuuint64_t row = static_cast<cuuint64_t>(dim) * 2;
+  const cuuint64_t dims[3] = {static_cast<cuuint64_t>(dim), static_cast<cuuint64_t>(heads),
+                              static_cast<cuuint64_t>(tokens)};
+  const cuuint64_t strides[2] = {heads > 1 ? static_cast<cuuint64_t>(head_stride) * 2 : row,
+                                 tokens > 1 ? static_cast<cuuint64_t>(token_stride) * 2 : row};
+  const cuuint32_t box[3] = {64, static_cast<cuuint32_t>(box_heads), static_cast<cuuint32_t>(box_tokens)};
+  const cuuint32_t estr[3] = {1, 1, 1};
+  const CUresult r = fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box, estr,
+                        CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                        CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  if (r != CUDA_SUCCESS) return fail(CSA2_ERR_CUDA, "cuTensorMapEncodeTiled failed (%d)", int(r));
+  return CSA2_OK;
+}
+
 }  // namespace csa2
