@@ -409,7 +409,8 @@ csa2_status csa2_paged_append(csa2_dtype dtype, const csa2_heads* k, const csa2_
  * statistics and sums in f32, the weights rounded to the 16-bit type for the
  * product with the values, out rounded once.  FP4 rows are dequantised exactly.
  * The visible tokens are cut into chunks that run side by side and are joined
- * in order.  chunk > 0 (a multiple of 64) fixes their length: a query's bits
+ * in order.  chunk > 0 (a multiple of 64; rows of 512 channels take the next
+ * multiple of 128) fixes their length: a query's bits
  * then depend on its own sequence only (lens[b] <= max_len); chunk = 0 lets the library choose it
  * from B, heads and max_len.
  *   q    rows of the cache's 16-bit type (bf16 for FP4), heads a multiple of

@@ -76,6 +76,12 @@ csa2_status make_tensor_map_heads(CUtensorMap* map, const void* base, int dim, i
 // Prompt attention on the tensor cores, rows of 64 or 128 channels (paged_window.cu).
 bool paged_window_tc_applies(const PagedAttn& a);
 csa2_status launch_paged_window_tc(const PagedAttn& a, const int32_t* cu_q, int64_t T, cudaStream_t stream);
+// The decode launch on the tensor cores (paged_wide.cu): chunks of aligned tiles of
+// 128 tokens; the caller joins them.
+bool paged_wide_applies(const PagedAttn& a);
+int paged_wide_heads(const PagedAttn& a);            // query heads per CTA
+csa2_status launch_paged_wide(const PagedAttn& a, int chunk, int chunks, float* part_o, float2* part_ml,
+                              cudaStream_t stream);
 csa2_status launch_paged_window(const PagedAttn& a, const int32_t* cu_q, int64_t T, cudaStream_t stream);
 
 }  // namespace csa2

@@ -33,6 +33,7 @@ struct Params {
   float2* part_ml;                   // [B * Hq][chunks]
   float scale2;                      // scale * log2(e)
   int Hq, G, row_tiles, window, sinks, chunk, chunks;
+  int aligned;                       // chunks of aligned tiles (paged_wide.cu)
   PagedView kv;
 };
 
@@ -335,9 +336,15 @@ __global__ void __launch_bounds__(128) paged_combine_kernel(const Params p) {
   const int b = static_cast<int>(at / p.Hq);
   pdl_wait();
   const int len = length_of(p.kv, b, false);
-  const Seen seen(len - 1, len - 1, p.window, p.sinks);
-  if (seen.total <= p.chunk) return;                   // written by the only chunk
-  const int n = min(p.chunks, (seen.total - 1) / p.chunk + 1);
+  int total, per = p.chunk;                            // tokens (or aligned tiles) in all, per chunk
+  if (p.aligned) {
+    total = AlignedTiles(len - 1, p.window, p.sinks).tiles;
+    per /= 128;
+  } else {
+    total = Seen(len - 1, len - 1, p.window, p.sinks).total;
+  }
+  if (total <= per) return;                            // written by the only chunk
+  const int n = min(p.chunks, (total - 1) / per + 1);
   const float2* ml = p.part_ml + at * p.chunks;
   float mx = -INFINITY;
   for (int i = threadIdx.x; i < n; i += 128) mx = fmaxf(mx, ml[i].x);
@@ -472,16 +479,41 @@ int64_t seen_bound(const PagedAttn& a, int64_t max_len) {
 struct Split {
   int chunk, chunks;
 };
-// The chunk length of a decode launch: as long as leaves about four CTAs per SM.
+// The chunk length of a decode launch.
+//  - wide rows on the tensor cores: one CTA per SM, so the number of chunks that
+//    wastes least, counting a chunk's start and partial output as 4 tiles
+//  - else about four CTAs per SM
 Split split_of(const PagedAttn& a, int64_t max_len, int chunk) {
   const int64_t seen = std::max<int64_t>(1, seen_bound(a, max_len));
+  Split s;
+  if (paged_wide_applies(a)) {
+    const int nh = paged_wide_heads(a);
+    const int64_t units = std::max<int64_t>(1, static_cast<int64_t>(a.kv.B) * a.kv.heads * ((a.G + nh - 1) / nh));
+    const int64_t tiles = (seen + 127) / 128 + (a.window > 0 ? 2 : 0);
+    int64_t per = std::min<int64_t>((static_cast<int64_t>(chunk) + 127) / 128, tiles);
+    if (chunk == 0) {
+      int64_t best = 0;
+      const int sms = sm_count();
+      for (int64_t n = 1; n <= std::min<int64_t>(tiles, 4 * sms); ++n) {
+        const int64_t len = (tiles + n - 1) / n;
+        const int64_t cost = (units * ((tiles + len - 1) / len) + sms - 1) / sms * (len + 4);
+        if (best == 0 || cost < best) {
+          best = cost;
+          per = len;
+        }
+        if (n * units > 16 * sms) break;
+      }
+    }
+    s.chunk = static_cast<int>(per * 128);
+    s.chunks = static_cast<int>((tiles + per - 1) / per);
+    return s;
+  }
   const int64_t units = static_cast<int64_t>(a.kv.B) * a.kv.heads * ((a.G + 15) / 16);
   int64_t c = chunk;
   if (c == 0) {
     const int64_t want = std::max<int64_t>(1, 4LL * sm_count() / std::max<int64_t>(1, units));
     c = std::max<int64_t>(256, ((seen + want - 1) / want + 63) / 64 * 64);
   }
-  Split s;
   s.chunk = static_cast<int>(std::min<int64_t>(c, 0x7fffffc0));
   s.chunks = static_cast<int>((seen + s.chunk - 1) / s.chunk);
   return s;
@@ -506,7 +538,10 @@ csa2_status launch_paged_decode(const PagedAttn& a, int64_t max_len, int chunk, 
     p.part_o = static_cast<float*>(ws);
     p.part_ml = reinterpret_cast<float2*>(p.part_o + static_cast<size_t>(a.kv.B) * a.Hq * s.chunks * a.D);
   }
-  if (paged_decode_stream_applies(a)) {
+  if (paged_wide_applies(a)) {
+    p.aligned = 1;
+    CSA2_TRY(launch_paged_wide(a, s.chunk, s.chunks, p.part_o, p.part_ml, stream));
+  } else if (paged_decode_stream_applies(a)) {
     CSA2_TRY(launch_paged_decode_stream(a, s.chunk, s.chunks, p.part_o, p.part_ml, stream));
   } else {
     const dim3 grid(static_cast<unsigned>(s.chunks), static_cast<unsigned>(a.kv.heads * p.row_tiles),

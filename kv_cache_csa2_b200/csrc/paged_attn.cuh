@@ -7,6 +7,8 @@
 #include <cuda_fp16.h>
 #include <cuda_fp8.h>
 
+#include <type_traits>
+
 #include "common.cuh"
 #include "paged.h"
 #include "rope.cuh"
@@ -110,10 +112,58 @@ struct Seen {
   }
   __device__ __forceinline__ int token(int slot) const { return slot < ns ? slot : slot - ns + lo; }
 };
+// The same for one row, in tiles of 128 tokens aligned to 128: the sinks', then
+// those from the window's start on.
+struct AlignedTiles {
+  int lo, ns, pmax, sink_tiles, first_tile, tiles;
+  __device__ __forceinline__ AlignedTiles(int p, int window, int sinks) : pmax(p) {
+    const Seen s(p, p, window, sinks);
+    lo = s.lo;
+    ns = s.ns;
+    sink_tiles = (ns + 127) / 128;
+    first_tile = max(lo / 128, sink_tiles);
+    tiles = s.total == 0 ? 0 : sink_tiles + max(0, p / 128 + 1 - first_tile);
+  }
+  __device__ __forceinline__ int start(int i) const { return (i < sink_tiles ? i : i - sink_tiles + first_tile) * 128; }
+};
 // window = 0: no window.  p - j < window as an unsigned difference is safe for
 // every p >= j >= 0.
 __device__ __forceinline__ bool sees(int p, int j, int window, int sinks) {
   return j <= p && (window <= 0 || p - j < window || j < sinks);
+}
+
+// One lane of a converged warp.  The products are issued under this instruction's
+// predicate rather than a lane test: their operands live in uniform registers, and
+// only here does the compiler know that a single lane is active.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t e;
+  asm volatile("{.reg .pred p; elect.sync _|p, 0xffffffff; selp.u32 %0, 1, 0, p;}" : "=r"(e));
+  return e != 0;
+}
+// Descriptors are a base plus an offset of their low word (16-byte units of shared memory).
+__device__ __forceinline__ uint64_t desc_at(uint64_t base, uint32_t bytes) { return base + (bytes >> 4); }
+// One box of the cache's tensor map: channels c .. c + 63 of box rows from `slot` on.
+__device__ __forceinline__ void tma_load_page(void* dst, const CUtensorMap* map, uint64_t* bar, int c, int head, int slot,
+                                              int page) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%3, %4, %5, %6}], [%2];" ::"r"(sm100::smem_u32(dst)),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(sm100::smem_u32(bar)), "r"(c), "r"(head), "r"(slot), "r"(page)
+      : "memory");
+}
+
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
+      "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]),
+      "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+      : "memory");
+}
+
+template <class T>
+__host__ __device__ constexpr uint32_t idesc_of(int M, int N, bool a_mn, bool b_mn) {
+  return std::is_same<T, __half>::value ? sm100::idesc_f16_f32(M, N, a_mn, b_mn) : sm100::idesc_bf16_f32(M, N, a_mn, b_mn);
 }
 
 // sm100::mbar_wait for a converged warp, with a short first look and the clock

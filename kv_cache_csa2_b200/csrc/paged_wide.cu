@@ -1,0 +1,523 @@
+// Attention of one new token per sequence over a paged cache with many query heads
+// per cache head (a shared 512-wide row under 64 heads: 128 flops per byte), on the
+// 5th-generation tensor cores.
+//
+// A CTA takes up to NH query heads of one cache head and a run of key tiles of 128
+// tokens.  Keys stand on the M side, heads on the N side, so that a cached row is
+// read from shared memory as it lies, as key and as value:
+//   S^T[key, head] = K q^T        (M = 128 keys, N = NH, K = D)
+//   O^T[channel, head] += V^T P   (M = 128 channels, N = NH, K = 128 keys)
+//   warps 0-3  softmax, one thread per key: P = 2^(s - ref) for every head, row sums
+//              kept per thread and added up at the end
+//   warp 4     issues the products
+//   warp 5     fills a ring of 8 blocks of 64 channels x 128 keys (16 KiB, TMA boxes
+//              by page); a block of a shared row serves the score and then the value
+//              product and is refilled as soon as its channels are through
+// A head's reference is its maximum over the first tile and moves (with a rescaled
+// output in TMEM) only when some score has outgrown it by 2^8, so the steady state
+// takes no maximum across keys: one barrier with an OR per tile asks whether any has.
+//
+// HBM-bound: a 128 KiB tile of 512 channels arrives in 5600 clocks at an SM's share
+// of the memory rate; its products take about 3100 (both operands from shared
+// memory), the softmax about 1000.
+#include <algorithm>
+#include <type_traits>
+
+#include "attn_common.cuh"
+#include "launchers.h"
+#include "paged_attn.cuh"
+
+namespace csa2 {
+namespace {
+using namespace paged;
+using namespace sm100;
+using rope::Num;
+
+constexpr int kThreads = 192;
+constexpr int KT = 128;                                // keys per tile
+constexpr int SLOTS = 8;
+constexpr int BLK = KT * 128;                          // 64 channels of 128 keys
+constexpr int kBits = 8;
+constexpr float kLazy = 8.0f;
+
+template <int D, int NH>
+struct Lay {
+  static constexpr int DB = D / 64;                    // blocks per tile of keys (or values)
+  static constexpr int QB = NH * 128;                  // 64 channels of q
+  static constexpr int RING = 0;
+  static constexpr int Q = RING + SLOTS * BLK;
+  static constexpr int P = Q + DB * QB;                // [128 keys][64 heads]
+  static constexpr int REF = P + BLK;                  // ref[NH], factor[NH]
+  static constexpr int RED = REF + 2 * NH * 4;         // [4][NH]
+  static constexpr int BAR = RED + 4 * NH * 4;
+  static constexpr int NBAR = 2 * SLOTS + 4;
+  static constexpr int BITS = BAR + NBAR * 8;
+  static constexpr int MISC = BITS + kBits * 4 * 4;
+  static constexpr int BYTES = MISC + 16 + 1024;
+  static_assert(P % 1024 == 0 && Q % 1024 == 0, "swizzled tiles");
+};
+
+struct Params {
+  const uint16_t* q;
+  int64_t q_token, q_head;
+  uint16_t* out;
+  float* lse;
+  float* part_o;                     // [B * Hq][chunks][D]
+  float2* part_ml;
+  float scale2;                      // |scale| * log2(e), at least the smallest normal
+  uint32_t flip;                     // 0x80008000 for a negative scale
+  int Hq, G, row_tiles, window, sinks, chunk, chunks;
+  int box;                           // rows of a TMA box
+  PagedView kv;
+};
+
+// the softmax warps: do any of the 128 threads have `pred`
+__device__ __forceinline__ bool any_of_128(bool pred) {
+  uint32_t r;
+  asm volatile(
+      "{.reg .pred p, q; setp.ne.b32 p, %1, 0; barrier.cta.red.or.pred q, 1, 128, p; selp.u32 %0, 1, 0, q;}"
+      : "=r"(r)
+      : "r"(static_cast<uint32_t>(pred))
+      : "memory");
+  return r != 0;
+}
+__device__ __forceinline__ void bar_128() { asm volatile("barrier.cta.sync 1, 128;" ::: "memory"); }
+
+template <class T, int D, int NH, bool SHARED>
+__global__ void __launch_bounds__(kThreads, 1) paged_wide_kernel(const Params p, const __grid_constant__ CUtensorMap k_map,
+                                                               const __grid_constant__ CUtensorMap v_map) {
+  using L = Lay<D, NH>;
+  constexpr int DB = L::DB;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint64_t* bar = reinterpret_cast<uint64_t*>(smem + L::BAR);
+  uint64_t *const full = bar, *const empty = bar + SLOTS;
+  uint64_t *const s_full = bar + 2 * SLOTS, *const p_full = s_full + 1, *const all_done = s_full + 2, *const fix_bar = s_full + 3;
+  uint32_t* bits = reinterpret_cast<uint32_t*>(smem + L::BITS);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + L::MISC);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + L::MISC + 4);
+  float* ref = reinterpret_cast<float*>(smem + L::REF);
+  float* factor = ref + NH;
+  float* red = reinterpret_cast<float*>(smem + L::RED);
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int b = blockIdx.z, chunk = blockIdx.x;
+  const int kvh = blockIdx.y / p.row_tiles, h0 = NH * (blockIdx.y % p.row_tiles);
+  const int rows = min(NH, p.G - h0);
+  pdl_wait();
+  const int len = length_of(p.kv, b, threadIdx.x == 0);
+  const AlignedTiles at(len - 1, p.window, p.sinks);
+  const int per = p.chunk / KT;
+  const int first = chunk * per;
+  if (chunk > 0 && first >= at.tiles) return;
+  const int tiles = (chunk + 1 < p.chunks ? min(at.tiles, first + per) : at.tiles) - first;
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < SLOTS; ++i) {
+      mbar_init(full + i, 1);
+      mbar_init(empty + i, 1);
+    }
+    mbar_init(s_full, 1);
+    mbar_init(p_full, 4);
+    mbar_init(all_done, 1);
+    mbar_init(fix_bar, 1);
+    *abort_flag = 0;
+    fence_mbar_init();
+  }
+  if (warp == 4) {
+    tmem_alloc(tmem_slot, 512);
+    tmem_relinquish();
+  }
+  if (warp < 5) {
+    // q rows (zero past the last) into K-major swizzled blocks
+#pragma unroll 8
+    for (int i = threadIdx.x; i < NH * (D / 8); i += 160) {
+      const int r = i / (D / 8), c = i % (D / 8);
+      uint4 v = make_uint4(0, 0, 0, 0);
+      if (r < rows) {
+        v = __ldg(reinterpret_cast<const uint4*>(p.q + b * p.q_token + (kvh * p.G + h0 + r) * p.q_head) + c);
+        v.x ^= p.flip;
+        v.y ^= p.flip;
+        v.z ^= p.flip;
+        v.w ^= p.flip;
+      }
+      *reinterpret_cast<uint4*>(smem + L::Q + (c / 8) * L::QB + sw128_offset(r, c % 8)) = v;
+    }
+    fence_proxy_async_smem();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  constexpr uint32_t O_COL = 128;                      // S at column 0, O block db at 128 + 64 db
+  auto wait = [&](uint64_t* x, uint32_t parity) { return wait_phase(x, parity, abort_flag, p.kv.err); };
+
+  if (warp == 5) {
+    // ------------------------------------------------------------ loader
+    // lane i: rows i * p.box .. of a tile
+    const int br = lane * p.box;
+    const bool mine = br < KT;
+    auto some = [&](int a, int n) { return a <= at.pmax && (a + n > at.lo || a < at.ns); };
+    auto wanted = [&](int j) { return j <= at.pmax && (j >= at.lo || j < at.ns); };
+    auto page_of = [&](int tile) -> int {
+      if (!mine || tile >= tiles || !some(at.start(first + tile) + br, p.box)) return -1;
+      const int pg = __ldg(p.kv.table + b * p.kv.table_stride + ((at.start(first + tile) + br) >> p.kv.page_shift));
+      if (pg >= 0 && pg < p.kv.n_pages) return pg;
+      raise_dev_error(p.kv.err, DEVERR_BOUNDS);
+      return -1;
+    };
+    int page = page_of(0);
+    uint32_t u = 0, issued = 0, fixes = 0;             // blocks of tiles behind, blocks asked for
+    bool ok = true;
+    for (int tile = 0; tile < tiles && ok; ++tile) {
+      const int next = page_of(tile + 1);
+      const int t0 = at.start(first + tile), a = t0 + br;
+      const bool any = mine && some(a, p.box);
+      const bool all = any && ((a >= at.lo && a + p.box - 1 <= at.pmax) || a + p.box <= at.ns);
+      const bool box = any && page >= 0;
+      const uint32_t boxes = __ballot_sync(0xffffffffu, box);
+      const uint32_t zero = __ballot_sync(0xffffffffu, mine && !(box && all));   // boxes with rows to zero
+      const bool some_lost = __any_sync(0xffffffffu, any && page < 0);
+      const int slot_in_page = a & ((1 << p.kv.page_shift) - 1);
+#pragma unroll
+      for (int half = 0; half < (SHARED ? 1 : 2); ++half) {
+        const bool fix = zero != 0 && (half == 1 || SHARED);
+        if (fix) {
+          // the whole tile at once, its unwanted rows zeroed before it is announced
+          for (int i = 0; i < DB && ok; ++i) ok = wait(empty + (u + i) % SLOTS, (((u + i) / SLOTS) & 1) ^ 1);
+          if (!ok) break;
+        }
+        if (half == 0) {
+          // tokens present, 32 to a word
+          if (!fix) ok = wait(empty + u % SLOTS, ((u / SLOTS) & 1) ^ 1);
+          if (!ok) break;
+          if (lane < 4) {
+            uint32_t here = 0xffffffffu;
+            if (some_lost)
+              for (int i = 0; i < 32; ++i) {
+                const int j = t0 + lane * 32 + i;
+                if (wanted(j) && token_row(p.kv, b, j) < 0) here &= ~(1u << i);
+              }
+            bits[(tile % kBits) * 4 + lane] = here;
+          }
+          __syncwarp();
+        }
+        if (fix && lane == 0) mbar_arrive_expect_tx(fix_bar, __popc(boxes) * p.box * 128 * DB);
+        for (int i = 0; i < DB && ok; ++i) {
+          const uint32_t st = (u + i) % SLOTS;
+          uint8_t* dst = smem + L::RING + st * BLK;
+          if (!fix) {
+            ok = wait(empty + st, (((u + i) / SLOTS) & 1) ^ 1);
+            if (!ok) break;
+            if (lane == 0) mbar_arrive_expect_tx(full + st, __popc(boxes) * p.box * 128);
+            issued = u + i + 1;
+          }
+          __syncwarp();
+          if (box)
+            tma_load_page(dst + br * 128, half ? &v_map : &k_map, fix ? fix_bar : full + st, i * 64, kvh, slot_in_page, page);
+          __syncwarp();
+        }
+        if (!ok) break;
+        if (fix) {
+          ok = wait(fix_bar, fixes & 1);
+          ++fixes;
+          if (!ok) break;
+          for (uint32_t z = zero; z; z &= z - 1) {
+            const int src = __ffs(z) - 1;
+            const bool loaded = (boxes >> src) & 1u;
+            for (int r = src * p.box; r < (src + 1) * p.box; ++r) {
+              if (loaded && wanted(t0 + r)) continue;
+              for (int c = lane; c < DB * 8; c += 32)
+                *reinterpret_cast<uint4*>(smem + L::RING + (u + c / 8) % SLOTS * BLK + sw128_offset(r, c % 8)) =
+                    make_uint4(0, 0, 0, 0);
+            }
+          }
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0)
+            for (int i = 0; i < DB; ++i) mbar_arrive(full + (u + i) % SLOTS);
+          __syncwarp();
+          issued = u + DB;
+        }
+        u += DB;
+      }
+      page = next;
+    }
+    if (!ok) {
+      // copies in flight land before the block's shared memory goes
+      volatile int never = 0;
+      for (uint32_t i = issued > SLOTS ? issued - SLOTS : 0; i < issued; ++i)
+        wait_phase(full + i % SLOTS, (i / SLOTS) & 1, &never, p.kv.err);
+    }
+  } else if (warp == 4) {
+    // ------------------------------------------------------------ products
+    constexpr uint32_t idesc_s = idesc_of<T>(128, NH, false, false), idesc_o = idesc_of<T>(128, NH, true, true);
+    const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
+    const uint64_t q_desc = desc_kmajor_sw128(smem_u32(smem + L::Q)), k_desc = desc_kmajor_sw128(smem_u32(smem + L::RING));
+    const uint64_t v_desc = desc_mnmajor_sw128(smem_u32(smem + L::RING), BLK, 1024);
+    const uint64_t p_desc = desc_mnmajor_sw128(smem_u32(smem + L::P), BLK, 1024);
+    uint32_t u = 0;                                    // blocks taken
+    bool ok = true;
+    for (int tile = 0; tile < tiles && ok; ++tile) {
+      for (int i = 0; i < DB && ok; ++i) {
+        const uint32_t st = (u + i) % SLOTS;
+        ok = wait(full + st, ((u + i) / SLOTS) & 1);
+        tc_fence_after();
+        if (ok && elect_one()) {
+          const uint64_t a = desc_at(k_desc, st * BLK), q = desc_at(q_desc, i * L::QB);
+#pragma unroll
+          for (int kk = 0; kk < 4; ++kk)
+            mma_bf16(tm, desc_at(a, kk * 32), desc_at(q, kk * 32), idesc_s, (i | kk) != 0);
+          if (!SHARED) mma_commit(empty + st);
+          if (i == DB - 1) mma_commit(s_full);
+        }
+        __syncwarp();
+      }
+      if (!SHARED) u += DB;
+      ok = ok && wait(p_full, tile & 1);
+      for (int db = 0; db < D / 128 && ok; ++db) {
+        const uint32_t st = (u + 2 * db) % SLOTS;
+        if (!SHARED) ok = wait(full + st, ((u + 2 * db) / SLOTS) & 1) && wait(full + st + 1, ((u + 2 * db) / SLOTS) & 1);
+        tc_fence_after();
+        if (ok && elect_one()) {
+          const uint64_t a = desc_at(v_desc, st * BLK);
+#pragma unroll
+          for (int kk = 0; kk < KT / 16; ++kk)
+            mma_bf16(tm + O_COL + db * 64, desc_at(a, kk * 2048), desc_at(p_desc, kk * 2048), idesc_o,
+                     tile > 0 || kk > 0);
+          mma_commit(empty + st);
+          mma_commit(empty + st + 1);
+        }
+        __syncwarp();
+      }
+      u += DB;
+    }
+    if (elect_one()) mma_commit(all_done);
+    __syncwarp();
+  } else {
+    // ------------------------------------------------------------ softmax and output
+    const int key = warp * 32 + lane;                  // TMEM lane
+    const uint32_t lane_off = static_cast<uint32_t>(warp * 32) << 16;
+    const uint32_t s_at = tmem + lane_off, o_at = tmem + lane_off + O_COL;
+    float l[NH];
+#pragma unroll
+    for (int h = 0; h < NH; ++h) l[h] = 0.0f;
+    bool ok = true;
+    for (int tile = 0; tile < tiles && ok; ++tile) {
+      ok = wait(s_full, tile & 1);
+      tc_fence_after();
+      float x[NH];
+      if (ok) {
+        if constexpr (NH == 64) {
+          tmem_ld32(s_at, *reinterpret_cast<uint32_t(*)[32]>(x));
+          tmem_ld32(s_at + 32, *reinterpret_cast<uint32_t(*)[32]>(x + 32));
+        } else {
+          tmem_ld16(s_at, *reinterpret_cast<uint32_t(*)[16]>(x));
+        }
+        tmem_wait_ld();
+      }
+      const int j = at.start(first + tile) + key;
+      const uint32_t here = *reinterpret_cast<volatile uint32_t*>(bits + (tile % kBits) * 4 + warp);
+      const bool seen = ok && j <= at.pmax && (j >= at.lo || j < at.ns) && ((here >> lane) & 1u);
+#pragma unroll
+      for (int h = 0; h < NH; ++h) x[h] = seen ? x[h] * p.scale2 : -INFINITY;
+      bool grow = tile == 0 || !ok;
+      if (tile > 0) {
+#pragma unroll
+        for (int h = 0; h < NH; h += 4) {
+          const float4 r = *reinterpret_cast<const float4*>(ref + h);
+          grow |= x[h] > r.x + kLazy || x[h + 1] > r.y + kLazy || x[h + 2] > r.z + kLazy || x[h + 3] > r.w + kLazy;
+        }
+      }
+      if (any_of_128(grow)) {
+        if (any_of_128(!ok)) {                         // all leave together
+          ok = false;
+          break;
+        }
+        // every head's maximum over the tile; those that outgrew theirs move to it
+#pragma unroll
+        for (int h = 0; h < NH; ++h) {
+          const float m = attn::warp_max_f32(x[h]);
+          if (lane == 0) red[warp * NH + h] = m;
+        }
+        bar_128();
+        if (key < NH) {
+          const float m = fmaxf(fmaxf(red[key], red[NH + key]), fmaxf(red[2 * NH + key], red[3 * NH + key]));
+          const float old = tile == 0 ? -INFINITY : ref[key];
+          const bool move = m > old + kLazy || (old == -INFINITY && m > -INFINITY);
+          // nothing seen so far: the output is zero and any factor serves
+          factor[key] = move && old > -INFINITY ? exp2_approx(old - m) : 1.0f;
+          ref[key] = move ? m : old;
+        }
+        bar_128();
+        if (tile > 0) {
+#pragma unroll
+          for (int h = 0; h < NH; ++h) l[h] *= factor[h];
+          // the value products of the tile before ended before this tile's scores did
+#pragma unroll 1
+          for (int i = 0; i < D / 128 * (NH / 16); ++i) {
+            const uint32_t to = o_at + i / (NH / 16) * 64 + i % (NH / 16) * 16;
+            uint32_t v[16];
+            tmem_ld16(to, v);
+            tmem_wait_ld();
+#pragma unroll
+            for (int e = 0; e < 16; ++e)
+              v[e] = __float_as_uint(__uint_as_float(v[e]) * factor[i % (NH / 16) * 16 + e]);
+            tmem_st16(to, v);
+          }
+          tmem_wait_st();
+        }
+      }
+      uint8_t* prow = smem + L::P;
+#pragma unroll
+      for (int h = 0; h < NH; h += 8) {
+        const float4 r0 = *reinterpret_cast<const float4*>(ref + h), r1 = *reinterpret_cast<const float4*>(ref + h + 4);
+        const float r[8] = {r0.x, r0.y, r0.z, r0.w, r1.x, r1.y, r1.z, r1.w};
+        float e[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          e[i] = exp2_approx(x[h + i] - (r[i] == -INFINITY ? 0.0f : r[i]));
+          l[h + i] += e[i];
+        }
+        *reinterpret_cast<uint4*>(prow + sw128_offset(key, h / 8)) =
+            make_uint4(Num<T>::down(e[0], e[1]), Num<T>::down(e[2], e[3]), Num<T>::down(e[4], e[5]), Num<T>::down(e[6], e[7]));
+      }
+      fence_proxy_async_smem();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(p_full);
+    }
+    ok = wait(all_done, 0) && ok;
+    tc_fence_after();
+    // row sums over the keys, through the ring (every product has ended)
+    float* const sums = reinterpret_cast<float*>(smem + L::RING);      // [128][NH + 1]
+#pragma unroll
+    for (int h = 0; h < NH; ++h) sums[key * (NH + 1) + h] = l[h];
+    bar_128();
+    if (key < NH) {
+      float s0 = 0.0f, s1 = 0.0f, s2 = 0.0f, s3 = 0.0f;
+#pragma unroll 8
+      for (int i = 0; i < 128; i += 4) {
+        s0 += sums[i * (NH + 1) + key];
+        s1 += sums[(i + 1) * (NH + 1) + key];
+        s2 += sums[(i + 2) * (NH + 1) + key];
+        s3 += sums[(i + 3) * (NH + 1) + key];
+      }
+      factor[key] = tiles > 0 ? (s0 + s1) + (s2 + s3) : 0.0f;          // l
+    }
+    bar_128();
+    const int64_t row0 = static_cast<int64_t>(b) * p.Hq + kvh * p.G + h0;
+    const bool partial = p.chunks > 1 && at.tiles > per;
+#pragma unroll 1
+    for (int i = 0; i < D / 128 * (NH / 16) && ok; ++i) {
+      const int db = i / (NH / 16), hb = i % (NH / 16) * 16;
+      uint32_t v[16];
+      if (tiles > 0) {
+        tmem_ld16(o_at + db * 64 + hb, v);
+        tmem_wait_ld();
+      }
+#pragma unroll
+      for (int e = 0; e < 16; ++e) {
+        if (hb + e >= rows) break;
+        const float o = tiles > 0 ? __uint_as_float(v[e]) : 0.0f;
+        const int64_t row = row0 + hb + e;
+        if (partial) {
+          p.part_o[(row * p.chunks + chunk) * D + db * 128 + key] = o;
+        } else {
+          const float s = factor[hb + e];
+          const float inv = s > 0.0f ? 1.0f / s : (s == 0.0f ? 0.0f : s);
+          p.out[row * D + db * 128 + key] = static_cast<uint16_t>(Num<T>::down(o * inv, 0.0f) & 0xffffu);
+        }
+      }
+    }
+    if (key < rows && ok) {
+      const float s = factor[key], m = tiles > 0 ? ref[key] : -INFINITY;
+      if (partial)
+        p.part_ml[(row0 + key) * p.chunks + chunk] = make_float2(s > 0.0f || s != s ? m : -INFINITY, s);
+      else if (p.lse)
+        p.lse[row0 + key] = s == 0.0f ? -INFINITY : (m + log2f(s)) * kLn2;
+    }
+  }
+  volatile int never = 0;                              // also when a wait gave up: the products still end
+  wait_phase(all_done, 0, &never, p.kv.err);
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 4) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+template <class T, int D, int NH, bool SHARED>
+csa2_status run(const Params& p, dim3 grid, const CUtensorMap (&maps)[2], cudaStream_t stream) {
+  using L = Lay<D, NH>;
+  static PerDevice<int> opted;
+  opted.get(+[]() -> int {
+    cudaFuncSetAttribute(paged_wide_kernel<T, D, NH, SHARED>, cudaFuncAttributeMaxDynamicSharedMemorySize, L::BYTES);
+    return 1;
+  });
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = L::BYTES;
+  cfg.stream = stream;
+  cudaLaunchAttribute at[1] = {pdl_attribute()};
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  begin_launch(stream);
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, paged_wide_kernel<T, D, NH, SHARED>, p, maps[0], maps[1]);
+  note_launch(LK_ATTN, 1, stream);
+  if (e != cudaSuccess) {
+    cudaGetLastError();
+    return fail(CSA2_ERR_CUDA, "csa2_paged_decode_attn: launch failed: %s", cudaGetErrorString(e));
+  }
+  return check_launch("csa2_paged_decode_attn");
+}
+
+}  // namespace
+
+int paged_wide_heads(const PagedAttn& a) { return a.G <= 16 ? 16 : 64; }
+
+bool paged_wide_applies(const PagedAttn& a) {
+  return a.fmt != CSA2_KV_FP4 && a.kv.page_shift >= 3 && a.kv.n_pages > 0 && a.D == 512;
+}
+
+csa2_status launch_paged_wide(const PagedAttn& a, int chunk, int chunks, float* part_o, float2* part_ml,
+                              cudaStream_t stream) {
+  Params p = {};
+  p.q = static_cast<const uint16_t*>(a.q);
+  p.q_token = a.q_token;
+  p.q_head = a.q_head;
+  p.out = static_cast<uint16_t*>(a.out);
+  p.lse = a.lse;
+  p.part_o = part_o;
+  p.part_ml = part_ml;
+  const float s = a.scale * kLog2e;
+  p.flip = s < 0.0f ? 0x80008000u : 0u;
+  p.scale2 = std::max(s < 0.0f ? -s : s, 1.1754944e-38f);
+  p.Hq = a.Hq;
+  p.G = a.G;
+  const int nh = paged_wide_heads(a);
+  p.row_tiles = (a.G + nh - 1) / nh;
+  p.window = a.window;
+  p.sinks = a.sinks;
+  p.chunk = chunk;
+  p.chunks = chunks;
+  p.kv = a.kv;
+  const bool sh = a.kv.v == a.kv.k;
+  const int page = 1 << a.kv.page_shift;
+  p.box = std::min(page, KT);
+  CUtensorMap maps[2] = {};
+  for (int i = 0; i < (sh ? 1 : 2); ++i)
+    CSA2_TRY(make_tensor_map_paged(&maps[i], i ? a.kv.v : a.kv.k, a.D, a.kv.heads, a.kv.head_stride, page,
+                                   a.kv.token_stride, a.kv.n_pages, a.kv.page_stride, p.box));
+  const dim3 grid(static_cast<unsigned>(chunks), static_cast<unsigned>(a.kv.heads * p.row_tiles),
+                  static_cast<unsigned>(a.kv.B));
+#define CSA2_WIDE_N(T_, N_) (sh ? run<T_, 512, N_, true>(p, grid, maps, stream) : run<T_, 512, N_, false>(p, grid, maps, stream))
+#define CSA2_WIDE(T_) (nh == 16 ? CSA2_WIDE_N(T_, 16) : CSA2_WIDE_N(T_, 64))
+  return a.fmt == CSA2_KV_F16 ? CSA2_WIDE(__half) : CSA2_WIDE(__nv_bfloat16);
+#undef CSA2_WIDE
+#undef CSA2_WIDE_N
+}
+
+}  // namespace csa2

@@ -83,26 +83,6 @@ struct Params {
   PagedView kv;
 };
 
-// One box of the cache's tensor map: channels c .. c + 63 of box rows from `slot` on.
-__device__ __forceinline__ void tma_load_page(void* dst, const CUtensorMap* map, uint64_t* bar, int c, int head, int slot,
-                                              int page) {
-  asm volatile(
-      "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes"
-      " [%0], [%1, {%3, %4, %5, %6}], [%2];" ::"r"(smem_u32(dst)),
-      "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(c), "r"(head), "r"(slot), "r"(page)
-      : "memory");
-}
-
-// One lane of a converged warp.  The products are issued under this instruction's
-// predicate rather than a lane test: their operands live in uniform registers, and
-// only here does the compiler know that a single lane is active.
-__device__ __forceinline__ bool elect_one() {
-  uint32_t e;
-  asm volatile("{.reg .pred p; elect.sync _|p, 0xffffffff; selp.u32 %0, 1, 0, p;}" : "=r"(e));
-  return e != 0;
-}
-// Descriptors are a base plus an offset of their low word (16-byte units of shared memory).
-__device__ __forceinline__ uint64_t desc_at(uint64_t base, uint32_t bytes) { return base + (bytes >> 4); }
 // A row tile's q rows: channels c .. c + 63 of the G heads of some tokens.
 __device__ __forceinline__ void tma_load_q(void* dst, const CUtensorMap* map, uint64_t* bar, int c, int head, int token) {
   asm volatile(
@@ -120,15 +100,6 @@ __device__ __forceinline__ void mma_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_
       "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
       : "memory");
 }
-__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16]) {
-  asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
-      "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(taddr),
-      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]),
-      "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
-      : "memory");
-}
-
 // Pairs of f32 in one instruction, each rounded to nearest.
 __device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
   float2 d;
@@ -149,11 +120,6 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
   float d;
   asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
   return d;
-}
-
-template <class T>
-__host__ __device__ constexpr uint32_t idesc_of(int M, int N, bool b_mn) {
-  return std::is_same<T, __half>::value ? idesc_f16_f32(M, N, false, b_mn) : idesc_bf16_f32(M, N, false, b_mn);
 }
 
 // Row tiles of a CTA: the sequence, its rows, and what they see.
@@ -487,7 +453,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_window_kernel(const Params 
     } else {
       // ------------------------------------------------------------ products
       const int w = warp - 8;
-      constexpr uint32_t idesc_s = idesc_of<T>(128, HT, false), idesc_o = idesc_of<T>(128, D, true);
+      constexpr uint32_t idesc_s = idesc_of<T>(128, HT, false, false), idesc_o = idesc_of<T>(128, D, false, true);
       const RowTile rt(wk, w, p.G, p.window, p.sinks);
       const uint32_t s_at = __shfl_sync(0xffffffffu, tmem, 0) + w * 128, o_at = s_at + O_COL;
       const uint64_t q_desc = desc_kmajor_sw128(smem_u32(smem + L::Q + w * L::TILE)), k_desc = desc_kmajor_sw128(smem_u32(sK));
