@@ -7,19 +7,21 @@
 // read from shared memory as it lies, as key and as value:
 //   S^T[key, head] = K q^T        (M = 128 keys, N = NH, K = D)
 //   O^T[channel, head] += V^T P   (M = 128 channels, N = NH, K = 128 keys)
-//   warps 0-3  softmax, one thread per key: P = 2^(s - ref) for every head, row sums
-//              kept per thread and added up at the end
-//   warp 4     issues the products
-//   warp 5     fills a ring of 8 blocks of 64 channels x 128 keys (16 KiB, TMA boxes
-//              by page); a block of a shared row serves the score and then the value
-//              product and is refilled as soon as its channels are through
+//   warps 0-3, 4-7  softmax, one thread per key and half of the heads (all of them,
+//                   warps 0-3 alone, for up to 16): P = 2^(s - ref), row sums kept
+//                   per thread and added up at the end
+//   one warp        issues the products
+//   three warps     fill a ring of 8 blocks of 64 channels x 128 keys (16 KiB, TMA
+//                   boxes by page); a block of a shared row serves the score and then
+//                   the value product and is refilled as soon as its channels are
+//                   through.  (One warp took 450 clocks a block to issue.)
 // A head's reference is its maximum over the first tile and moves (with a rescaled
 // output in TMEM) only when some score has outgrown it by 2^8, so the steady state
 // takes no maximum across keys: one barrier with an OR per tile asks whether any has.
 //
 // HBM-bound: a 128 KiB tile of 512 channels arrives in 5600 clocks at an SM's share
 // of the memory rate; its products take about 3100 (both operands from shared
-// memory), the softmax about 1000.
+// memory), and the softmax stands between them.
 #include <algorithm>
 #include <type_traits>
 
@@ -33,7 +35,7 @@ using namespace paged;
 using namespace sm100;
 using rope::Num;
 
-constexpr int kThreads = 192;
+constexpr int kLoaders = 3;
 constexpr int KT = 128;                                // keys per tile
 constexpr int SLOTS = 8;
 constexpr int BLK = KT * 128;                          // 64 channels of 128 keys
@@ -42,15 +44,18 @@ constexpr float kLazy = 8.0f;
 
 template <int D, int NH>
 struct Lay {
+  static constexpr int SW = NH == 64 ? 8 : 4;          // softmax warps
+  static constexpr int HW = NH * 4 / SW;               // heads per softmax thread
+  static constexpr int THREADS = (SW + 1 + kLoaders) * 32;
   static constexpr int DB = D / 64;                    // blocks per tile of keys (or values)
   static constexpr int QB = NH * 128;                  // 64 channels of q
   static constexpr int RING = 0;
   static constexpr int Q = RING + SLOTS * BLK;
   static constexpr int P = Q + DB * QB;                // [128 keys][64 heads]
-  static constexpr int REF = P + BLK;                  // ref[NH], factor[NH]
+  static constexpr int REF = P + BLK;                  // -reference[NH], shift[NH]
   static constexpr int RED = REF + 2 * NH * 4;         // [4][NH]
   static constexpr int BAR = RED + 4 * NH * 4;
-  static constexpr int NBAR = 2 * SLOTS + 4;
+  static constexpr int NBAR = 2 * SLOTS + 3 + kLoaders;
   static constexpr int BITS = BAR + NBAR * 8;
   static constexpr int MISC = BITS + kBits * 4 * 4;
   static constexpr int BYTES = MISC + 16 + 1024;
@@ -71,33 +76,37 @@ struct Params {
   PagedView kv;
 };
 
-// the softmax warps: do any of the 128 threads have `pred`
-__device__ __forceinline__ bool any_of_128(bool pred) {
+// the softmax warps: do any of their N threads have `pred`
+template <int N>
+__device__ __forceinline__ bool any_of(bool pred) {
   uint32_t r;
   asm volatile(
-      "{.reg .pred p, q; setp.ne.b32 p, %1, 0; barrier.cta.red.or.pred q, 1, 128, p; selp.u32 %0, 1, 0, q;}"
+      "{.reg .pred p, q; setp.ne.b32 p, %1, 0; barrier.cta.red.or.pred q, 1, %2, p; selp.u32 %0, 1, 0, q;}"
       : "=r"(r)
-      : "r"(static_cast<uint32_t>(pred))
+      : "r"(static_cast<uint32_t>(pred)), "n"(N)
       : "memory");
   return r != 0;
 }
-__device__ __forceinline__ void bar_128() { asm volatile("barrier.cta.sync 1, 128;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void bar_of() {
+  asm volatile("barrier.cta.sync 1, %0;" ::"n"(N) : "memory");
+}
 
 template <class T, int D, int NH, bool SHARED>
-__global__ void __launch_bounds__(kThreads, 1) paged_wide_kernel(const Params p, const __grid_constant__ CUtensorMap k_map,
-                                                               const __grid_constant__ CUtensorMap v_map) {
+__global__ void __launch_bounds__(Lay<D, NH>::THREADS, 1)
+    paged_wide_kernel(const Params p, const __grid_constant__ CUtensorMap k_map, const __grid_constant__ CUtensorMap v_map) {
   using L = Lay<D, NH>;
-  constexpr int DB = L::DB;
+  constexpr int DB = L::DB, SW = L::SW, HW = L::HW;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint64_t* bar = reinterpret_cast<uint64_t*>(smem + L::BAR);
   uint64_t *const full = bar, *const empty = bar + SLOTS;
-  uint64_t *const s_full = bar + 2 * SLOTS, *const p_full = s_full + 1, *const all_done = s_full + 2, *const fix_bar = s_full + 3;
+  uint64_t *const s_full = bar + 2 * SLOTS, *const p_full = s_full + 1, *const all_done = s_full + 2, *const fix_bars = s_full + 3;
   uint32_t* bits = reinterpret_cast<uint32_t*>(smem + L::BITS);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + L::MISC);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + L::MISC + 4);
   float* ref = reinterpret_cast<float*>(smem + L::REF);
-  float* factor = ref + NH;
+  float* shift = ref + NH;
   float* red = reinterpret_cast<float*>(smem + L::RED);
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -118,20 +127,20 @@ __global__ void __launch_bounds__(kThreads, 1) paged_wide_kernel(const Params p,
       mbar_init(empty + i, 1);
     }
     mbar_init(s_full, 1);
-    mbar_init(p_full, 4);
+    mbar_init(p_full, SW);
     mbar_init(all_done, 1);
-    mbar_init(fix_bar, 1);
+    for (int i = 0; i < kLoaders; ++i) mbar_init(fix_bars + i, 1);
     *abort_flag = 0;
     fence_mbar_init();
   }
-  if (warp == 4) {
+  if (warp == SW) {
     tmem_alloc(tmem_slot, 512);
     tmem_relinquish();
   }
-  if (warp < 5) {
+  if (warp < SW) {
     // q rows (zero past the last) into K-major swizzled blocks
 #pragma unroll 8
-    for (int i = threadIdx.x; i < NH * (D / 8); i += 160) {
+    for (int i = threadIdx.x; i < NH * (D / 8); i += SW * 32) {
       const int r = i / (D / 8), c = i % (D / 8);
       uint4 v = make_uint4(0, 0, 0, 0);
       if (r < rows) {
@@ -152,9 +161,11 @@ __global__ void __launch_bounds__(kThreads, 1) paged_wide_kernel(const Params p,
   constexpr uint32_t O_COL = 128;                      // S at column 0, O block db at 128 + 64 db
   auto wait = [&](uint64_t* x, uint32_t parity) { return wait_phase(x, parity, abort_flag, p.kv.err); };
 
-  if (warp == 5) {
+  if (warp > SW) {
     // ------------------------------------------------------------ loader
-    // lane i: rows i * p.box .. of a tile
+    // loader lw takes the blocks lw, lw + 3, .. of a tile; lane i: rows i * p.box ..
+    const int lw = warp - SW - 1;
+    uint64_t* const fix_bar = fix_bars + lw;
     const int br = lane * p.box;
     const bool mine = br < KT;
     auto some = [&](int a, int n) { return a <= at.pmax && (a + n > at.lo || a < at.ns); };
@@ -181,64 +192,58 @@ __global__ void __launch_bounds__(kThreads, 1) paged_wide_kernel(const Params p,
       const int slot_in_page = a & ((1 << p.kv.page_shift) - 1);
 #pragma unroll
       for (int half = 0; half < (SHARED ? 1 : 2); ++half) {
+        // values whose unwanted rows are zeroed before their blocks are announced
         const bool fix = zero != 0 && (half == 1 || SHARED);
-        if (fix) {
-          // the whole tile at once, its unwanted rows zeroed before it is announced
-          for (int i = 0; i < DB && ok; ++i) ok = wait(empty + (u + i) % SLOTS, (((u + i) / SLOTS) & 1) ^ 1);
-          if (!ok) break;
-        }
-        if (half == 0) {
-          // tokens present, 32 to a word
-          if (!fix) ok = wait(empty + u % SLOTS, ((u / SLOTS) & 1) ^ 1);
-          if (!ok) break;
-          if (lane < 4) {
-            uint32_t here = 0xffffffffu;
-            if (some_lost)
-              for (int i = 0; i < 32; ++i) {
-                const int j = t0 + lane * 32 + i;
-                if (wanted(j) && token_row(p.kv, b, j) < 0) here &= ~(1u << i);
-              }
-            bits[(tile % kBits) * 4 + lane] = here;
-          }
-          __syncwarp();
-        }
-        if (fix && lane == 0) mbar_arrive_expect_tx(fix_bar, __popc(boxes) * p.box * 128 * DB);
-        for (int i = 0; i < DB && ok; ++i) {
+        for (int i = lw; i < DB && ok; i += kLoaders) {
           const uint32_t st = (u + i) % SLOTS;
-          uint8_t* dst = smem + L::RING + st * BLK;
-          if (!fix) {
-            ok = wait(empty + st, (((u + i) / SLOTS) & 1) ^ 1);
-            if (!ok) break;
-            if (lane == 0) mbar_arrive_expect_tx(full + st, __popc(boxes) * p.box * 128);
-            issued = u + i + 1;
+          ok = wait(empty + st, (((u + i) / SLOTS) & 1) ^ 1);
+          if (!ok) break;
+          if (half == 0 && i == 0) {
+            // tokens present, 32 to a word
+            if (lane < 4) {
+              uint32_t here = 0xffffffffu;
+              if (some_lost)
+                for (int e = 0; e < 32; ++e) {
+                  const int j = t0 + lane * 32 + e;
+                  if (wanted(j) && token_row(p.kv, b, j) < 0) here &= ~(1u << e);
+                }
+              bits[(tile % kBits) * 4 + lane] = here;
+            }
+            __syncwarp();
           }
+          uint64_t* const to = fix ? fix_bar : full + st;
+          uint8_t* const dst = smem + L::RING + st * BLK;
+          if (lane == 0) mbar_arrive_expect_tx(to, __popc(boxes) * p.box * 128);
           __syncwarp();
-          if (box)
-            tma_load_page(dst + br * 128, half ? &v_map : &k_map, fix ? fix_bar : full + st, i * 64, kvh, slot_in_page, page);
-          __syncwarp();
-        }
-        if (!ok) break;
-        if (fix) {
+          for (uint32_t m = boxes; m; m &= m - 1) {
+            const int bx = __ffs(m) - 1;
+            const int pg = __shfl_sync(0xffffffffu, page, bx), sl = __shfl_sync(0xffffffffu, slot_in_page, bx);
+            if (elect_one()) tma_load_page(dst + bx * p.box * 128, half ? &v_map : &k_map, to, i * 64, kvh, sl, pg);
+            __syncwarp();
+          }
+          if (!fix) {
+            issued = u + i + 1;
+            continue;
+          }
           ok = wait(fix_bar, fixes & 1);
           ++fixes;
           if (!ok) break;
           for (uint32_t z = zero; z; z &= z - 1) {
             const int src = __ffs(z) - 1;
             const bool loaded = (boxes >> src) & 1u;
-            for (int r = src * p.box; r < (src + 1) * p.box; ++r) {
-              if (loaded && wanted(t0 + r)) continue;
-              for (int c = lane; c < DB * 8; c += 32)
-                *reinterpret_cast<uint4*>(smem + L::RING + (u + c / 8) % SLOTS * BLK + sw128_offset(r, c % 8)) =
-                    make_uint4(0, 0, 0, 0);
+#pragma unroll 4
+            for (int x = lane; x < p.box * 8; x += 32) {
+              const int r = src * p.box + x / 8;
+              if (!loaded || !wanted(t0 + r))
+                *reinterpret_cast<uint4*>(dst + sw128_offset(r, x % 8)) = make_uint4(0, 0, 0, 0);
             }
           }
           fence_proxy_async_smem();
           __syncwarp();
-          if (lane == 0)
-            for (int i = 0; i < DB; ++i) mbar_arrive(full + (u + i) % SLOTS);
-          __syncwarp();
-          issued = u + DB;
+          if (lane == 0) mbar_arrive(full + st);
+          issued = u + i + 1;
         }
+        if (!ok) break;
         u += DB;
       }
       page = next;
@@ -247,9 +252,9 @@ __global__ void __launch_bounds__(kThreads, 1) paged_wide_kernel(const Params p,
       // copies in flight land before the block's shared memory goes
       volatile int never = 0;
       for (uint32_t i = issued > SLOTS ? issued - SLOTS : 0; i < issued; ++i)
-        wait_phase(full + i % SLOTS, (i / SLOTS) & 1, &never, p.kv.err);
+        if (i % DB % kLoaders == static_cast<uint32_t>(lw)) wait_phase(full + i % SLOTS, (i / SLOTS) & 1, &never, p.kv.err);
     }
-  } else if (warp == 4) {
+  } else if (warp == SW) {
     // ------------------------------------------------------------ products
     constexpr uint32_t idesc_s = idesc_of<T>(128, NH, false, false), idesc_o = idesc_of<T>(128, NH, true, true);
     const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
@@ -296,91 +301,105 @@ __global__ void __launch_bounds__(kThreads, 1) paged_wide_kernel(const Params p,
     __syncwarp();
   } else {
     // ------------------------------------------------------------ softmax and output
-    const int key = warp * 32 + lane;                  // TMEM lane
-    const uint32_t lane_off = static_cast<uint32_t>(warp * 32) << 16;
-    const uint32_t s_at = tmem + lane_off, o_at = tmem + lane_off + O_COL;
-    float l[NH];
+    const int key = (warp & 3) * 32 + lane;            // TMEM lane
+    const int hb = warp / 4 * HW;                      // first of this thread's heads
+    constexpr int N = SW * 32;
+    const uint32_t lane_off = static_cast<uint32_t>((warp & 3) * 32) << 16;
+    const uint32_t s_at = tmem + lane_off + hb, o_at = tmem + lane_off + O_COL + hb;
+    float2 l[HW / 2];
 #pragma unroll
-    for (int h = 0; h < NH; ++h) l[h] = 0.0f;
-    bool ok = true;
+    for (int h = 0; h < HW / 2; ++h) l[h] = make_float2(0.0f, 0.0f);
+    if (threadIdx.x < NH) ref[threadIdx.x] = 0.0f;     // -reference: none so far
+    bar_of<N>();
+    const float4* const mine = reinterpret_cast<const float4*>(ref + hb);
+    bool ok = true, started = false;                   // started: some key was seen
     for (int tile = 0; tile < tiles && ok; ++tile) {
       ok = wait(s_full, tile & 1);
       tc_fence_after();
-      float x[NH];
+      float x[HW];
       if (ok) {
-        if constexpr (NH == 64) {
+        if constexpr (HW == 32) {
           tmem_ld32(s_at, *reinterpret_cast<uint32_t(*)[32]>(x));
-          tmem_ld32(s_at + 32, *reinterpret_cast<uint32_t(*)[32]>(x + 32));
         } else {
           tmem_ld16(s_at, *reinterpret_cast<uint32_t(*)[16]>(x));
         }
         tmem_wait_ld();
       }
       const int j = at.start(first + tile) + key;
-      const uint32_t here = *reinterpret_cast<volatile uint32_t*>(bits + (tile % kBits) * 4 + warp);
+      const uint32_t here = *reinterpret_cast<volatile uint32_t*>(bits + (tile % kBits) * 4 + (warp & 3));
       const bool seen = ok && j <= at.pmax && (j >= at.lo || j < at.ns) && ((here >> lane) & 1u);
+      // x - reference; a key that is not seen weighs nothing
+      const float2 sc = make_float2(p.scale2, p.scale2);
+      float top = -INFINITY;
 #pragma unroll
-      for (int h = 0; h < NH; ++h) x[h] = seen ? x[h] * p.scale2 : -INFINITY;
-      bool grow = tile == 0 || !ok;
-      if (tile > 0) {
-#pragma unroll
-        for (int h = 0; h < NH; h += 4) {
-          const float4 r = *reinterpret_cast<const float4*>(ref + h);
-          grow |= x[h] > r.x + kLazy || x[h + 1] > r.y + kLazy || x[h + 2] > r.z + kLazy || x[h + 3] > r.w + kLazy;
-        }
+      for (int h = 0; h < HW; h += 4) {
+        const float4 r = mine[h / 4];
+        const float2 a = fma2(make_float2(x[h], x[h + 1]), sc, make_float2(r.x, r.y));
+        const float2 c = fma2(make_float2(x[h + 2], x[h + 3]), sc, make_float2(r.z, r.w));
+        x[h] = seen ? a.x : -INFINITY;
+        x[h + 1] = seen ? a.y : -INFINITY;
+        x[h + 2] = seen ? c.x : -INFINITY;
+        x[h + 3] = seen ? c.y : -INFINITY;
+        top = max3(top, x[h], x[h + 1]);
+        top = max3(top, x[h + 2], x[h + 3]);
       }
-      if (any_of_128(grow)) {
-        if (any_of_128(!ok)) {                         // all leave together
+      if (any_of<N>(!started || !ok || top > kLazy)) {
+        if (any_of<N>(!ok)) {                          // all leave together
           ok = false;
           break;
         }
-        // every head's maximum over the tile; those that outgrew theirs move to it
+        // every head's maximum over the tile; the heads that outgrew their reference
+        // move to it (on the first tile that shows anything, all of them)
+        const bool first_seen = !started && any_of<N>(seen);
 #pragma unroll
-        for (int h = 0; h < NH; ++h) {
+        for (int h = 0; h < HW; ++h) {
           const float m = attn::warp_max_f32(x[h]);
-          if (lane == 0) red[warp * NH + h] = m;
+          if (lane == 0) red[(warp & 3) * NH + hb + h] = m;
         }
-        bar_128();
-        if (key < NH) {
-          const float m = fmaxf(fmaxf(red[key], red[NH + key]), fmaxf(red[2 * NH + key], red[3 * NH + key]));
-          const float old = tile == 0 ? -INFINITY : ref[key];
-          const bool move = m > old + kLazy || (old == -INFINITY && m > -INFINITY);
-          // nothing seen so far: the output is zero and any factor serves
-          factor[key] = move && old > -INFINITY ? exp2_approx(old - m) : 1.0f;
-          ref[key] = move ? m : old;
+        bar_of<N>();
+        if (threadIdx.x < NH) {
+          const int h = threadIdx.x;
+          const float m = fmaxf(fmaxf(red[h], red[NH + h]), fmaxf(red[2 * NH + h], red[3 * NH + h]));
+          shift[h] = m > kLazy || (first_seen && m > -INFINITY) ? m : 0.0f;
+          ref[h] -= shift[h];
         }
-        bar_128();
-        if (tile > 0) {
+        bar_of<N>();
 #pragma unroll
-          for (int h = 0; h < NH; ++h) l[h] *= factor[h];
+        for (int h = 0; h < HW; ++h) x[h] -= shift[hb + h];
+        if (started) {
+#pragma unroll
+          for (int h = 0; h < HW; h += 2) {
+            l[h / 2].x *= exp2_approx(-shift[hb + h]);
+            l[h / 2].y *= exp2_approx(-shift[hb + h + 1]);
+          }
           // the value products of the tile before ended before this tile's scores did
 #pragma unroll 1
-          for (int i = 0; i < D / 128 * (NH / 16); ++i) {
-            const uint32_t to = o_at + i / (NH / 16) * 64 + i % (NH / 16) * 16;
+          for (int i = 0; i < D / 128 * (HW / 16); ++i) {
+            const int c = i % (HW / 16) * 16;
+            const uint32_t to = o_at + i / (HW / 16) * 64 + c;
             uint32_t v[16];
             tmem_ld16(to, v);
             tmem_wait_ld();
 #pragma unroll
             for (int e = 0; e < 16; ++e)
-              v[e] = __float_as_uint(__uint_as_float(v[e]) * factor[i % (NH / 16) * 16 + e]);
+              v[e] = __float_as_uint(__uint_as_float(v[e]) * exp2_approx(-shift[hb + c + e]));
             tmem_st16(to, v);
           }
           tmem_wait_st();
         }
+        started |= first_seen;
       }
-      uint8_t* prow = smem + L::P;
+      uint8_t* const prow = smem + L::P;
 #pragma unroll
-      for (int h = 0; h < NH; h += 8) {
-        const float4 r0 = *reinterpret_cast<const float4*>(ref + h), r1 = *reinterpret_cast<const float4*>(ref + h + 4);
-        const float r[8] = {r0.x, r0.y, r0.z, r0.w, r1.x, r1.y, r1.z, r1.w};
-        float e[8];
+      for (int h = 0; h < HW; h += 8) {
+        uint32_t pk[4];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          e[i] = exp2_approx(x[h + i] - (r[i] == -INFINITY ? 0.0f : r[i]));
-          l[h + i] += e[i];
+        for (int i = 0; i < 4; ++i) {
+          const float2 e = make_float2(exp2_approx(x[h + 2 * i]), exp2_approx(x[h + 2 * i + 1]));
+          l[h / 2 + i] = add2(l[h / 2 + i], e);
+          pk[i] = Num<T>::down(e.x, e.y);
         }
-        *reinterpret_cast<uint4*>(prow + sw128_offset(key, h / 8)) =
-            make_uint4(Num<T>::down(e[0], e[1]), Num<T>::down(e[2], e[3]), Num<T>::down(e[4], e[5]), Num<T>::down(e[6], e[7]));
+        *reinterpret_cast<uint4*>(prow + sw128_offset(key, (hb + h) / 8)) = make_uint4(pk[0], pk[1], pk[2], pk[3]);
       }
       fence_proxy_async_smem();
       tc_fence_before();
@@ -392,57 +411,62 @@ __global__ void __launch_bounds__(kThreads, 1) paged_wide_kernel(const Params p,
     // row sums over the keys, through the ring (every product has ended)
     float* const sums = reinterpret_cast<float*>(smem + L::RING);      // [128][NH + 1]
 #pragma unroll
-    for (int h = 0; h < NH; ++h) sums[key * (NH + 1) + h] = l[h];
-    bar_128();
-    if (key < NH) {
+    for (int h = 0; h < HW; h += 2) {
+      sums[key * (NH + 1) + hb + h] = l[h / 2].x;
+      sums[key * (NH + 1) + hb + h + 1] = l[h / 2].y;
+    }
+    bar_of<N>();
+    if (threadIdx.x < NH) {
+      const int h = threadIdx.x;
       float s0 = 0.0f, s1 = 0.0f, s2 = 0.0f, s3 = 0.0f;
 #pragma unroll 8
       for (int i = 0; i < 128; i += 4) {
-        s0 += sums[i * (NH + 1) + key];
-        s1 += sums[(i + 1) * (NH + 1) + key];
-        s2 += sums[(i + 2) * (NH + 1) + key];
-        s3 += sums[(i + 3) * (NH + 1) + key];
+        s0 += sums[i * (NH + 1) + h];
+        s1 += sums[(i + 1) * (NH + 1) + h];
+        s2 += sums[(i + 2) * (NH + 1) + h];
+        s3 += sums[(i + 3) * (NH + 1) + h];
       }
-      factor[key] = tiles > 0 ? (s0 + s1) + (s2 + s3) : 0.0f;          // l
+      shift[h] = tiles > 0 ? (s0 + s1) + (s2 + s3) : 0.0f;             // l
     }
-    bar_128();
+    bar_of<N>();
     const int64_t row0 = static_cast<int64_t>(b) * p.Hq + kvh * p.G + h0;
     const bool partial = p.chunks > 1 && at.tiles > per;
 #pragma unroll 1
-    for (int i = 0; i < D / 128 * (NH / 16) && ok; ++i) {
-      const int db = i / (NH / 16), hb = i % (NH / 16) * 16;
+    for (int i = 0; i < D / 128 * (HW / 16) && ok; ++i) {
+      const int db = i / (HW / 16), c = hb + i % (HW / 16) * 16;
       uint32_t v[16];
       if (tiles > 0) {
-        tmem_ld16(o_at + db * 64 + hb, v);
+        tmem_ld16(tmem + lane_off + O_COL + db * 64 + c, v);
         tmem_wait_ld();
       }
 #pragma unroll
       for (int e = 0; e < 16; ++e) {
-        if (hb + e >= rows) break;
+        if (c + e >= rows) break;
         const float o = tiles > 0 ? __uint_as_float(v[e]) : 0.0f;
-        const int64_t row = row0 + hb + e;
+        const int64_t row = row0 + c + e;
         if (partial) {
           p.part_o[(row * p.chunks + chunk) * D + db * 128 + key] = o;
         } else {
-          const float s = factor[hb + e];
+          const float s = shift[c + e];
           const float inv = s > 0.0f ? 1.0f / s : (s == 0.0f ? 0.0f : s);
           p.out[row * D + db * 128 + key] = static_cast<uint16_t>(Num<T>::down(o * inv, 0.0f) & 0xffffu);
         }
       }
     }
-    if (key < rows && ok) {
-      const float s = factor[key], m = tiles > 0 ? ref[key] : -INFINITY;
+    if (threadIdx.x < rows && ok) {
+      const int h = threadIdx.x;
+      const float s = shift[h], m = -ref[h];
       if (partial)
-        p.part_ml[(row0 + key) * p.chunks + chunk] = make_float2(s > 0.0f || s != s ? m : -INFINITY, s);
+        p.part_ml[(row0 + h) * p.chunks + chunk] = make_float2(s == 0.0f ? -INFINITY : m, s);
       else if (p.lse)
-        p.lse[row0 + key] = s == 0.0f ? -INFINITY : (m + log2f(s)) * kLn2;
+        p.lse[row0 + h] = s == 0.0f ? -INFINITY : (m + log2f(s)) * kLn2;
     }
   }
   volatile int never = 0;                              // also when a wait gave up: the products still end
   wait_phase(all_done, 0, &never, p.kv.err);
   tc_fence_before();
   __syncthreads();
-  if (warp == 4) {
+  if (warp == SW) {
     tc_fence_after();
     tmem_dealloc(tmem, 512);
   }
@@ -458,7 +482,7 @@ csa2_status run(const Params& p, dim3 grid, const CUtensorMap (&maps)[2], cudaSt
   });
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = grid;
-  cfg.blockDim = dim3(kThreads);
+  cfg.blockDim = dim3(L::THREADS);
   cfg.dynamicSmemBytes = L::BYTES;
   cfg.stream = stream;
   cudaLaunchAttribute at[1] = {pdl_attribute()};
