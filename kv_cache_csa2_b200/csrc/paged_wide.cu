@@ -264,17 +264,21 @@ __global__ void __launch_bounds__(Lay<D, NH>::THREADS, 1)
     uint32_t u = 0;                                    // blocks taken
     bool ok = true;
     for (int tile = 0; tile < tiles && ok; ++tile) {
-      for (int i = 0; i < DB && ok; ++i) {
-        const uint32_t st = (u + i) % SLOTS;
-        ok = wait(full + st, ((u + i) / SLOTS) & 1);
+      // two blocks at a time: a wait costs about as much as one block's products
+      for (int i = 0; i < DB && ok; i += 2) {
+        const uint32_t st = (u + i) % SLOTS, parity = ((u + i) / SLOTS) & 1;
+        ok = wait(full + st, parity) && wait(full + st + 1, parity);
         tc_fence_after();
         if (ok && elect_one()) {
-          const uint64_t a = desc_at(k_desc, st * BLK), q = desc_at(q_desc, i * L::QB);
 #pragma unroll
-          for (int kk = 0; kk < 4; ++kk)
-            mma_bf16(tm, desc_at(a, kk * 32), desc_at(q, kk * 32), idesc_s, (i | kk) != 0);
-          if (!SHARED) mma_commit(empty + st);
-          if (i == DB - 1) mma_commit(s_full);
+          for (int e = 0; e < 2; ++e) {
+            const uint64_t a = desc_at(k_desc, (st + e) * BLK), q = desc_at(q_desc, (i + e) * L::QB);
+#pragma unroll
+            for (int kk = 0; kk < 4; ++kk)
+              mma_bf16(tm, desc_at(a, kk * 32), desc_at(q, kk * 32), idesc_s, (i | e | kk) != 0);
+            if (!SHARED) mma_commit(empty + st + e);
+          }
+          if (i == DB - 2) mma_commit(s_full);
         }
         __syncwarp();
       }
