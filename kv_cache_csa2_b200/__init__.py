@@ -409,41 +409,39 @@ def csa2_fp4_unpack(codes, scales, stream=None):
 # that stream: results and scratch memory are then allocated for it, and the
 # inputs are marked as in use by it.
 
-def _run_on(fn, tensors, stream, args, kw):
-    """None when the current device and stream already are the call's, else
-    (its result,) from a call made with them current."""
+def _elsewhere(fn, dev, tensors, stream, args):
+    """A call made again with its device and stream current (its arguments in order)."""
     torch = _torch()
-    dev = None
-    for t in tensors:
-        if t is None:
-            continue
-        if not t.is_cuda:
-            raise ValueError(f"{fn.__name__}: expected CUDA tensors, got one on {t.device}")
-        if dev is None:
-            dev = t.get_device()
-        elif t.get_device() != dev:
-            raise ValueError(f"{fn.__name__}: tensors on devices {dev} and {t.get_device()}")
-    if stream is not None:
-        if dev is not None and stream.device.index != dev:
-            raise ValueError(f"{fn.__name__}: a stream of device {stream.device.index} with tensors on {dev}")
-        if stream != torch.cuda.current_stream(dev):
-            for t in tensors:
-                if t is not None:
-                    t.record_stream(stream)
-        with torch.cuda.stream(stream):
-            return (fn(*args, **kw),)
-    if dev is not None and dev != torch.cuda.current_device():
+    if dev < 0:
+        raise ValueError(f"{fn.__name__}: expected CUDA tensors")
+    if stream is None:
         with torch.cuda.device(dev):
-            return (fn(*args, **kw),)
-    return None
+            return fn(*args)
+    if stream.device.index != dev:
+        raise ValueError(f"{fn.__name__}: a stream of device {stream.device.index} with tensors on {dev}")
+    if stream != torch.cuda.current_stream(dev):
+        for t in tensors:
+            if t is not None:
+                t.record_stream(stream)
+    with torch.cuda.stream(stream):
+        return fn(*args)
+
+
+def _same_device(fn, dev, *tensors):
+    for t in tensors:
+        if t is not None and t.get_device() != dev:
+            raise ValueError(f"{fn.__name__}: tensors on devices {dev} and {t.get_device()}")
+
+
+def _raw_stream(dev):
+    return _torch()._C._cuda_getCurrentRawStream(dev)
 
 
 def _rows(t, name, dtype=None):
     """csa2_heads of a [T, heads, D] tensor with adjacent channels."""
-    torch = _torch()
     if t is None:
         raise ValueError(f"{name} is required")
-    if t.dim() != 3 or (t.dtype != dtype if dtype is not None else t.dtype not in (torch.bfloat16, torch.float16)):
+    if t.dim() != 3 or (t.dtype != dtype if dtype is not None else t.dtype not in _dtype_ids()):
         raise ValueError(f"{name}: expected {dtype or 'bfloat16 or float16'} [T, heads, D], got {t.dtype} "
                          f"{tuple(t.shape)}")
     T, H, D = t.shape
@@ -457,12 +455,22 @@ def _rows(t, name, dtype=None):
     return CSA2Heads(t.data_ptr(), H, ts, hs)
 
 
-def _ints(t, name, shape):
-    torch = _torch()
-    if t is None or t.dtype != torch.int32 or tuple(t.shape) != shape or not t.is_contiguous():
+def _rows_out(t, out, name, T, H, D):
+    """An output of t's shape (allocated when None) and its rows."""
+    if out is None:
+        out = t.new_empty((T, H, D))
+        return out, CSA2Heads(out.data_ptr(), H, H * D, D)
+    if out.shape != t.shape:
+        raise ValueError(f"{name}: {tuple(out.shape)} for {tuple(t.shape)}")
+    return out, _rows(out, name, t.dtype)
+
+
+def _ints(t, name, n):
+    """The address of a contiguous int32 tensor of n values."""
+    if t is None or t.dtype is not _torch().int32 or t.dim() != 1 or t.shape[0] != n or not t.is_contiguous():
         got = None if t is None else (t.dtype, tuple(t.shape))
-        raise ValueError(f"{name}: expected contiguous int32 {shape}, got {got}")
-    return t
+        raise ValueError(f"{name}: expected contiguous int32 ({n},), got {got}")
+    return t.data_ptr()
 
 
 class Rope:
@@ -474,7 +482,9 @@ class Rope:
         torch = _torch()
         _need(inv_freq, torch.float32, 1, "inv_freq")
         self.inv_freq = inv_freq
+        self.device = inv_freq.get_device()
         self.desc = CSA2Rope(inv_freq.data_ptr(), inv_freq.numel(), offset, int(interleaved), int(inverse))
+        self.ref = ctypes.byref(self.desc)
 
 
 class PagedKv:
@@ -509,20 +519,32 @@ class PagedKv:
         if table is None or table.dtype != torch.int32 or table.dim() != 2 or (table.shape[1] > 1 and table.stride(1) != 1):
             raise ValueError("table: expected int32 [B, max_pages]")
         B, max_pages = table.shape
-        _ints(lens, "lens", (B,))
+        _ints(lens, "lens", B)
         if B > 1 and table.stride(0) < max_pages:
             raise ValueError("table: rows overlap")
         self.k, self.v, self.k_scales, self.v_scales, self.table, self.lens = k, v, k_scales, v_scales, table, lens
         self.tensors = (k, v, k_scales, v_scales, table, lens)
         if len({t.get_device() for t in self.tensors if t is not None}) != 1:
             raise ValueError("the cache's tensors must be on one device")
+        self.device = k.get_device()
         self.dtype = torch.bfloat16 if fp4 else k.dtype
+        self._workspaces = {}
         self.heads, self.dim, self.B = heads, dim, B
         self.desc = CSA2PagedKv(fmt, k.data_ptr(), None if v is None else v.data_ptr(),
                                 None if k_scales is None else k_scales.data_ptr(),
                                 None if v_scales is None else v_scales.data_ptr(), n_pages, strides[0], strides[1],
                                 strides[2], page, heads, dim, B, max_pages,
                                 table.stride(0) if B > 1 else max_pages, table.data_ptr(), lens.data_ptr(), max_len)
+        self.ref = ctypes.byref(self.desc)
+
+    def decode_workspace(self, Hq, window=0, sinks=0, chunk=0):
+        """Bytes of scratch a csa2_paged_decode_attn call takes (depends on the shapes only)."""
+        key = (Hq, window, sinks, chunk)
+        nb = self._workspaces.get(key)
+        if nb is None:
+            with _torch().cuda.device(self.device):
+                nb = self._workspaces[key] = lib().csa2_paged_decode_attn_workspace(self.ref, *key)
+        return nb
 
     @staticmethod
     def _strides(t, name, unit, dim):
@@ -543,19 +565,19 @@ class PagedKv:
 _DTYPE_ID = {}
 
 
-def _dtype_id(dtype):
+def _dtype_ids():
     if not _DTYPE_ID:
         torch = _torch()
         _DTYPE_ID.update({torch.bfloat16: 0, torch.float16: 1})
-    return _DTYPE_ID[dtype]
+    return _DTYPE_ID
 
 
 def _weight(w, name, D):
-    if w is not None:
-        _need(w, _torch().float32, 1, name)
-        if w.numel() != D:
-            raise ValueError(f"{name}: {w.numel()} values for rows of {D}")
-    return _ptr(w)
+    if w is None:
+        return None
+    if w.dtype is not _torch().float32 or w.dim() != 1 or w.shape[0] != D or not w.is_contiguous():
+        raise ValueError(f"{name}: expected contiguous float32 ({D},), got {w.dtype} {tuple(w.shape)}")
+    return w.data_ptr()
 
 
 def csa2_qk_norm_rope(q, k, positions=None, q_weight=None, k_weight=None, eps: float = 1e-6, rope=None, q_out=None,
@@ -563,66 +585,69 @@ def csa2_qk_norm_rope(q, k, positions=None, q_weight=None, k_weight=None, eps: f
     """RMS norm of every head row (weight f32 [D] or None) and its rotation to
     positions[t] (int32 [T]); q, k [T, heads, D] bf16 / f16 (either may be None).
     q_out / k_out may be q / k (in place).  Returns (q_out, k_out)."""
-    done = _run_on(csa2_qk_norm_rope, (q, k, positions, q_weight, k_weight, q_out, k_out, rope and rope.inv_freq),
-                   stream, (q, k, positions, q_weight, k_weight, eps, rope, q_out, k_out), {})
-    if done:
-        return done[0]
     torch = _torch()
     x = q if q is not None else k
     if x is None:
         raise ValueError("csa2_qk_norm_rope: neither q nor k given")
-    T, _, D = x.shape if x.dim() == 3 else (0, 0, 0)
-    args = []
-    outs = []
-    for t, w, out, name in ((q, q_weight, q_out, "q"), (k, k_weight, k_out, "k")):
-        if t is None:
-            args += [None, None, None]
-            outs.append(None)
-            continue
-        rows = _rows(t, name, x.dtype)
-        if t.shape[0] != T or t.shape[2] != D:
-            raise ValueError(f"{name}: {tuple(t.shape)} beside {T} rows of {D} channels")
-        if out is None:
-            out = torch.empty(t.shape, dtype=t.dtype, device=t.device)
-        elif out.shape != t.shape:
-            raise ValueError(f"{name}_out: {tuple(out.shape)} for {name} {tuple(t.shape)}")
-        args += [ctypes.byref(rows), _weight(w, name + "_weight", D), ctypes.byref(_rows(out, name + "_out", x.dtype))]
-        outs.append(out)
-    if positions is not None:
-        _ints(positions, "positions", (T,))
-    _check(lib().csa2_qk_norm_rope(_dtype_id(x.dtype), *args, T, D, eps, _ptr(positions),
-                                   None if rope is None else ctypes.byref(rope.desc), _stream()))
-    return outs[0], outs[1]
+    dev = x.get_device()
+    _same_device(csa2_qk_norm_rope, dev, q, k, positions, q_weight, k_weight, q_out, k_out)
+    if rope is not None and rope.device != dev:
+        raise ValueError(f"csa2_qk_norm_rope: rotation on device {rope.device}, tensors on {dev}")
+    if dev < 0 or stream is not None or dev != torch.cuda.current_device():
+        return _elsewhere(csa2_qk_norm_rope, dev, (q, k, positions, q_weight, k_weight, q_out, k_out,
+                                                   None if rope is None else rope.inv_freq), stream,
+                          (q, k, positions, q_weight, k_weight, eps, rope, q_out, k_out))
+    dtype = x.dtype
+    xr = _rows(x, "q" if x is q else "k")
+    T, _, D = x.shape
+    qa = qo = ka = ko = None
+    if q is not None:
+        q_out, r = _rows_out(q, q_out, "q_out", T, xr.heads, D)
+        qa, qo = ctypes.byref(xr), ctypes.byref(r)
+    if k is not None:
+        if k.shape[0] != T or k.shape[2] != D:
+            raise ValueError(f"k: {tuple(k.shape)} beside {T} rows of {D} channels")
+        kr = xr if x is k else _rows(k, "k", dtype)
+        k_out, r2 = _rows_out(k, k_out, "k_out", T, kr.heads, D)
+        ka, ko = ctypes.byref(kr), ctypes.byref(r2)
+    st = lib().csa2_qk_norm_rope(_dtype_ids()[dtype], qa, _weight(q_weight, "q_weight", D), qo, ka,
+                                 _weight(k_weight, "k_weight", D), ko, T, D, eps,
+                                 None if positions is None else _ints(positions, "positions", T),
+                                 None if rope is None else rope.ref, _raw_stream(dev))
+    if st:
+        _check(st)
+    return q_out if q is not None else None, k_out if k is not None else None
 
 
 def csa2_paged_append(cache, k, v, seq, pos, rope=None, stream=None):
     """Write rows k (rotated to pos when `rope`), v [T, heads, D] to tokens pos[t] of
     sequences seq[t] (int32 [T]; seq -1: skip) of a PagedKv; v None for a shared cache."""
-    done = _run_on(csa2_paged_append, (k, v, seq, pos, rope and rope.inv_freq) + cache.tensors, stream,
-                   (cache, k, v, seq, pos, rope), {})
-    if done:
-        return done[0]
+    dev = cache.device
+    _same_device(csa2_paged_append, dev, k, v, seq, pos)
+    if rope is not None and rope.device != dev:
+        raise ValueError(f"csa2_paged_append: rotation on device {rope.device}, cache on {dev}")
+    if stream is not None or dev != _torch().cuda.current_device():
+        return _elsewhere(csa2_paged_append, dev, (k, v, seq, pos, None if rope is None else rope.inv_freq) + cache.tensors,
+                          stream, (cache, k, v, seq, pos, rope))
     kr = _rows(k, "k", cache.dtype)
     T = k.shape[0]
     if k.shape[2] != cache.dim or (v is not None and v.shape != k.shape):
         raise ValueError(f"k, v: {tuple(k.shape)}, {None if v is None else tuple(v.shape)} for a cache of width {cache.dim}")
-    vr = None if v is None else ctypes.byref(_rows(v, "v", cache.dtype))
-    _ints(seq, "seq", (T,))
-    _ints(pos, "pos", (T,))
-    _check(lib().csa2_paged_append(_dtype_id(cache.dtype), ctypes.byref(kr), vr, _ptr(seq), _ptr(pos), T,
-                                   None if rope is None else ctypes.byref(rope.desc), ctypes.byref(cache.desc),
-                                   _stream()))
+    st = lib().csa2_paged_append(_dtype_ids()[cache.dtype], ctypes.byref(kr),
+                                 None if v is None else ctypes.byref(_rows(v, "v", cache.dtype)), _ints(seq, "seq", T),
+                                 _ints(pos, "pos", T), T, None if rope is None else rope.ref, cache.ref, _raw_stream(dev))
+    if st:
+        _check(st)
 
 
 def _attn_out(q, out, lse):
-    torch = _torch()
     if out is None:
-        out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+        out = q.new_empty(q.shape)
     elif out.dtype != q.dtype or out.shape != q.shape or not out.is_contiguous():
         raise ValueError(f"out: expected contiguous {q.dtype} {tuple(q.shape)}")
     if lse is None:
-        lse = torch.empty(q.shape[:2], dtype=torch.float32, device=q.device)
-    elif lse.dtype != torch.float32 or lse.shape != q.shape[:2] or not lse.is_contiguous():
+        lse = q.new_empty(q.shape[:2], dtype=_torch().float32)
+    elif lse.dtype != _torch().float32 or lse.shape != q.shape[:2] or not lse.is_contiguous():
         raise ValueError(f"lse: expected contiguous float32 {tuple(q.shape[:2])}")
     return out, lse
 
@@ -631,21 +656,22 @@ def csa2_paged_decode_attn(q, cache, scale: float, window: int = 0, sinks: int =
                            stream=None):
     """Attention of one new token per sequence (q [B, Hq, D], at position lens[b] - 1)
     over a PagedKv: the last `window` tokens (0: all) and the first `sinks`."""
-    done = _run_on(csa2_paged_decode_attn, (q, out, lse) + cache.tensors, stream,
-                   (q, cache, scale, window, sinks, chunk, out, lse), {})
-    if done:
-        return done[0]
+    dev = cache.device
+    _same_device(csa2_paged_decode_attn, dev, q, out, lse)
+    if stream is not None or dev != _torch().cuda.current_device():
+        return _elsewhere(csa2_paged_decode_attn, dev, (q, out, lse) + cache.tensors, stream,
+                          (q, cache, scale, window, sinks, chunk, out, lse))
     rows = _rows(q, "q", cache.dtype)
     B, Hq, D = q.shape
     if B != cache.B or D != cache.dim:
         raise ValueError(f"q: {tuple(q.shape)} for a cache of {cache.B} sequences of width {cache.dim}")
     out, lse = _attn_out(q, out, lse)
-    L = lib()
-    desc = ctypes.byref(cache.desc)
-    nb = L.csa2_paged_decode_attn_workspace(desc, Hq, window, sinks, chunk)
-    ws = _workspace(nb, q.device)
-    _check(L.csa2_paged_decode_attn(ctypes.byref(rows), desc, scale, window, sinks, chunk, _ptr(out), _ptr(lse),
-                                    _ptr(ws), nb, _stream()))
+    nb = cache.decode_workspace(Hq, window, sinks, chunk)
+    ws = q.new_empty(nb, dtype=_torch().uint8) if nb else None
+    st = lib().csa2_paged_decode_attn(ctypes.byref(rows), cache.ref, scale, window, sinks, chunk, out.data_ptr(),
+                                      lse.data_ptr(), ws.data_ptr() if nb else None, nb, _raw_stream(dev))
+    if st:
+        _check(st)
     return out, lse
 
 
@@ -653,18 +679,20 @@ def csa2_paged_window_attn(q, cu_q, cache, scale: float, window: int = 0, sinks:
                            stream=None):
     """Causal attention of a prompt chunk: sequence b's new tokens are rows
     cu_q[b]..cu_q[b+1] of q [T, Hq, D], the last at position lens[b] - 1."""
-    done = _run_on(csa2_paged_window_attn, (q, cu_q, out, lse) + cache.tensors, stream,
-                   (q, cu_q, cache, scale, window, sinks, out, lse), {})
-    if done:
-        return done[0]
+    dev = cache.device
+    _same_device(csa2_paged_window_attn, dev, q, cu_q, out, lse)
+    if stream is not None or dev != _torch().cuda.current_device():
+        return _elsewhere(csa2_paged_window_attn, dev, (q, cu_q, out, lse) + cache.tensors, stream,
+                          (q, cu_q, cache, scale, window, sinks, out, lse))
     rows = _rows(q, "q", cache.dtype)
     T, _, D = q.shape
     if D != cache.dim:
         raise ValueError(f"q: {tuple(q.shape)} for a cache of width {cache.dim}")
-    _ints(cu_q, "cu_q", (cache.B + 1,))
     out, lse = _attn_out(q, out, lse)
-    _check(lib().csa2_paged_window_attn(ctypes.byref(rows), _ptr(cu_q), T, ctypes.byref(cache.desc), scale, window,
-                                        sinks, _ptr(out), _ptr(lse), _stream()))
+    st = lib().csa2_paged_window_attn(ctypes.byref(rows), _ints(cu_q, "cu_q", cache.B + 1), T, cache.ref, scale, window,
+                                      sinks, out.data_ptr(), lse.data_ptr(), _raw_stream(dev))
+    if st:
+        _check(st)
     return out, lse
 
 

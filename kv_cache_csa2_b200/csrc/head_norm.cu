@@ -17,6 +17,7 @@ namespace {
 using namespace rope;
 
 constexpr int kThreads = 256;
+constexpr int kMaxTokens = 8;
 
 struct Side {
   const uint16_t* in;
@@ -135,11 +136,10 @@ csa2_status launch_head_norm(csa2_dtype dtype, const HeadRows& q, const float* q
   while (p.lanes < p.items) p.lanes *= 2;
   const int per_pass = kThreads / p.lanes;
   const int sms = sm_count();
-  // as many tokens per CTA (up to 4, whose angles are one per thread at 64
-  // pairs) as still leave four CTAs per SM; with fewer tokens than that, a
-  // token's heads are cut over grid.y
-  p.tokens = 4;
-  while (p.tokens > 1 && T / p.tokens < 4 * sms) p.tokens /= 2;
+  // as many tokens per CTA as still leave four CTAs per SM (or as fill its
+  // threads once); with fewer tokens than that, a token's heads are cut over grid.y
+  p.tokens = kMaxTokens;
+  while (p.tokens > 1 && p.tokens * p.H > per_pass && T / p.tokens < 4 * sms) p.tokens /= 2;
   const int64_t gx = (T + p.tokens - 1) / p.tokens;
   const int passes = (p.tokens * p.H + per_pass - 1) / per_pass;
   int ny = 1;

@@ -17,7 +17,7 @@ namespace {
 using namespace rope;
 
 constexpr int kThreads = 256;
-constexpr int kMaxTokens = 4;
+constexpr int kMaxTokens = 8;
 
 struct Params {
   const uint16_t *k, *v;
@@ -173,7 +173,7 @@ csa2_status launch_paged_append(csa2_dtype dtype, const HeadRows& k, const HeadR
   const int sms = sm_count();
   // tokens per CTA as in the head norm
   p.tokens = kMaxTokens;
-  while (p.tokens > 1 && T / p.tokens < 4 * sms) p.tokens /= 2;
+  while (p.tokens > 1 && p.tokens * p.H > per_pass && T / p.tokens < 4 * sms) p.tokens /= 2;
   const int64_t gx = (T + p.tokens - 1) / p.tokens;
   const int passes = (p.tokens * p.H + per_pass - 1) / per_pass;
   int ny = 1;

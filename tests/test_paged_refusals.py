@@ -126,4 +126,4 @@ def test_binding_refuses_wrong_tensors():
     with pytest.raises(ValueError):
         K._rows(torch.zeros(4, 2, 64), "x")
     with pytest.raises(ValueError):
-        K._ints(torch.zeros(4, dtype=torch.int64), "x", (4,))
+        K._ints(torch.zeros(4, dtype=torch.int64), "x", 4)
