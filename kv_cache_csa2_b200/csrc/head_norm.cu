@@ -31,14 +31,24 @@ struct Params {
   const int32_t* positions;
   int64_t T;
   int Hq, H, D, items, lanes;        // H = query plus key heads; lanes per row (power of two)
+  int step_t, step_h;                // a pass's rows in tokens and heads
   int tokens, rows_cta;              // tokens per CTA, rows per CTA (grid.y cuts a token's heads)
   float eps;
   RopeArgs rope;
 };
 
+__device__ __forceinline__ void scale8(float2 (&x)[4], float inv, const float* w) {
+  const float4 a = __ldg(reinterpret_cast<const float4*>(w)), b = __ldg(reinterpret_cast<const float4*>(w) + 1);
+  const float2 i2 = make_float2(inv, inv);
+  x[0] = mul2(mul2(x[0], i2), make_float2(a.x, a.y));
+  x[1] = mul2(mul2(x[1], i2), make_float2(a.z, a.w));
+  x[2] = mul2(mul2(x[2], i2), make_float2(b.x, b.y));
+  x[3] = mul2(mul2(x[3], i2), make_float2(b.z, b.w));
+}
+
 template <class T>
 __global__ void __launch_bounds__(kThreads) head_norm_kernel(const Params p) {
-  extern __shared__ float2 cs[];                                   // [tokens][half]
+  extern __shared__ float4 cs[];                                   // [tokens][half / 2]
   const int64_t t0 = static_cast<int64_t>(blockIdx.x) * p.tokens;
   const int nt = static_cast<int>(min(static_cast<int64_t>(p.tokens), p.T - t0));
   const int per_pass = kThreads / p.lanes;
@@ -49,12 +59,10 @@ __global__ void __launch_bounds__(kThreads) head_norm_kernel(const Params p) {
   if (sub >= p.items) it.c0 = it.c1 = it.freq = -1;
 
   uint4 v0, v1;
-  int tl = 0, head = 0;
+  int tl = r / p.H, head = r - tl * p.H;
   auto request = [&](int row) {
     v0 = v1 = make_uint4(0, 0, 0, 0);
     if (row >= r_end) return;
-    tl = row / p.H;
-    head = row - tl * p.H;
     const uint16_t* src = head < p.Hq ? p.q.in + (t0 + tl) * p.q.in_t + head * p.q.in_h
                                       : p.k.in + (t0 + tl) * p.k.in_t + (head - p.Hq) * p.k.in_h;
     if (it.c0 >= 0) v0 = *reinterpret_cast<const uint4*>(src + it.c0);
@@ -65,13 +73,14 @@ __global__ void __launch_bounds__(kThreads) head_norm_kernel(const Params p) {
   if (p.rope.inv_freq) {
     for (int i = threadIdx.x; i < nt * p.rope.half; i += kThreads) {
       const int t = i / p.rope.half, f = i - t * p.rope.half;
-      cs[i] = angle_of(__ldg(p.positions + t0 + t), __ldg(p.rope.inv_freq + f), p.rope.inverse);
+      put_angle(cs + t * (p.rope.half / 2), f, p.rope.half,
+                angle_of(__ldg(p.positions + t0 + t), __ldg(p.rope.inv_freq + f), p.rope.inverse));
     }
     __syncthreads();
   }
   // all lanes of a warp stay in the loop together (the shuffles need them)
   for (int base = blockIdx.y * p.rows_cta; base < r_end; base += per_pass, r += per_pass) {
-    float x0[8], x1[8];
+    float2 x0[4], x1[4];
     unpack8<T>(v0, x0);
     unpack8<T>(v1, x1);
     const bool live = r < r_end, is_q = head < p.Hq;
@@ -79,30 +88,21 @@ __global__ void __launch_bounds__(kThreads) head_norm_kernel(const Params p) {
     const float* w = is_q ? p.q.weight : p.k.weight;
     float sum = 0.0f;
 #pragma unroll
-    for (int u = 0; u < 8; ++u) sum += x0[u] * x0[u] + x1[u] * x1[u];
+    for (int u = 0; u < 4; ++u) sum += (x0[u].x * x0[u].x + x0[u].y * x0[u].y) + (x1[u].x * x1[u].x + x1[u].y * x1[u].y);
     for (int o = p.lanes >> 1; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
     // a row is read whole by its lanes before any of them stores (the shuffle
     // above), so an output may be its input
+    tl += p.step_t;                                    // the row a pass further
+    head += p.step_h;
+    if (head >= p.H) head -= p.H, ++tl;
     request(r + per_pass);
     if (!live) continue;
     if (w) {
       const float inv = rsqrtf(sum / static_cast<float>(p.D) + p.eps);
-      if (it.c0 >= 0) {
-        const float4 a = __ldg(reinterpret_cast<const float4*>(w + it.c0));
-        const float4 b = __ldg(reinterpret_cast<const float4*>(w + it.c0) + 1);
-        const float g[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
-#pragma unroll
-        for (int u = 0; u < 8; ++u) x0[u] = __fmul_rn(__fmul_rn(x0[u], inv), g[u]);
-      }
-      if (it.c1 >= 0) {
-        const float4 a = __ldg(reinterpret_cast<const float4*>(w + it.c1));
-        const float4 b = __ldg(reinterpret_cast<const float4*>(w + it.c1) + 1);
-        const float g[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
-#pragma unroll
-        for (int u = 0; u < 8; ++u) x1[u] = __fmul_rn(__fmul_rn(x1[u], inv), g[u]);
-      }
+      if (it.c0 >= 0) scale8(x0, inv, w + it.c0);
+      if (it.c1 >= 0) scale8(x1, inv, w + it.c1);
     }
-    if (p.rope.inv_freq) rotate_item(x0, x1, it, p.rope.half, p.rope.interleaved, cs + my_t * p.rope.half);
+    if (p.rope.inv_freq) rotate_item(x0, x1, it, p.rope.half, p.rope.interleaved, cs + my_t * (p.rope.half / 2));
     uint16_t* dst = is_q ? p.q.out + (t0 + my_t) * p.q.out_t + my_h * p.q.out_h
                          : p.k.out + (t0 + my_t) * p.k.out_t + (my_h - p.Hq) * p.k.out_h;
     if (it.c0 >= 0) *reinterpret_cast<uint4*>(dst + it.c0) = pack8<T>(x0);
@@ -135,6 +135,8 @@ csa2_status launch_head_norm(csa2_dtype dtype, const HeadRows& q, const float* q
   p.lanes = 1;
   while (p.lanes < p.items) p.lanes *= 2;
   const int per_pass = kThreads / p.lanes;
+  p.step_t = per_pass / p.H;
+  p.step_h = per_pass % p.H;
   const int sms = sm_count();
   // as many tokens per CTA as still leave four CTAs per SM (or as fill its
   // threads once); with fewer tokens than that, a token's heads are cut over grid.y

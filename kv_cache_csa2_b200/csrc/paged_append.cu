@@ -25,6 +25,7 @@ struct Params {
   const int32_t *seq, *pos;
   int64_t T;
   int H, D, items, lanes;            // H = heads of k plus heads of v
+  int step_t, step_h;                // a pass's rows in tokens and heads
   int tokens, rows_cta;
   RopeArgs rope;
   PagedView cache;
@@ -57,7 +58,7 @@ __device__ __forceinline__ uint32_t pack_half_block(const uint4& v, uint32_t* sc
 
 template <class T, bool FP4>
 __global__ void __launch_bounds__(kThreads) paged_append_kernel(const Params p) {
-  extern __shared__ float2 cs[];                                   // [tokens][half]
+  extern __shared__ float4 cs[];                                   // [tokens][half / 2]
   __shared__ int64_t s_row[kMaxTokens];                            // the token's place (head 0), -1: skip
   const int64_t t0 = static_cast<int64_t>(blockIdx.x) * p.tokens;
   const int nt = static_cast<int>(min(static_cast<int64_t>(p.tokens), p.T - t0));
@@ -70,12 +71,10 @@ __global__ void __launch_bounds__(kThreads) paged_append_kernel(const Params p) 
   const int hk = p.cache.heads;
 
   uint4 v0, v1;
-  int tl = 0, head = 0;
+  int tl = r / p.H, head = r - tl * p.H;
   auto request = [&](int row) {
     v0 = v1 = make_uint4(0, 0, 0, 0);
     if (row >= r_end) return;
-    tl = row / p.H;
-    head = row - tl * p.H;
     const uint16_t* src = head < hk ? p.k + (t0 + tl) * p.k_t + head * p.k_h
                                     : p.v + (t0 + tl) * p.v_t + (head - hk) * p.v_h;
     if (it.c0 >= 0) v0 = __ldg(reinterpret_cast<const uint4*>(src + it.c0));
@@ -102,7 +101,8 @@ __global__ void __launch_bounds__(kThreads) paged_append_kernel(const Params p) 
   if (p.rope.inv_freq) {
     for (int i = threadIdx.x; i < nt * p.rope.half; i += kThreads) {
       const int t = i / p.rope.half, f = i - t * p.rope.half;
-      cs[i] = angle_of(__ldg(p.pos + t0 + t), __ldg(p.rope.inv_freq + f), p.rope.inverse);
+      put_angle(cs + t * (p.rope.half / 2), f, p.rope.half,
+                angle_of(__ldg(p.pos + t0 + t), __ldg(p.rope.inv_freq + f), p.rope.inverse));
     }
   }
   __syncthreads();
@@ -111,12 +111,15 @@ __global__ void __launch_bounds__(kThreads) paged_append_kernel(const Params p) 
     uint4 a = v0, b = v1;
     const bool live = r < r_end, is_k = head < hk;
     const int my_t = tl, my_h = is_k ? head : head - hk;
+    tl += p.step_t;                                    // the row a pass further
+    head += p.step_h;
+    if (head >= p.H) head -= p.H, ++tl;
     request(r + per_pass);
     if (live && is_k && p.rope.inv_freq && it.freq >= 0) {
-      float x0[8], x1[8];
+      float2 x0[4], x1[4];
       unpack8<T>(a, x0);
       unpack8<T>(b, x1);
-      rotate_item(x0, x1, it, p.rope.half, p.rope.interleaved, cs + my_t * p.rope.half);
+      rotate_item(x0, x1, it, p.rope.half, p.rope.interleaved, cs + my_t * (p.rope.half / 2));
       a = pack8<T>(x0);
       b = pack8<T>(x1);
     }
@@ -170,6 +173,8 @@ csa2_status launch_paged_append(csa2_dtype dtype, const HeadRows& k, const HeadR
   p.lanes = 1;
   while (p.lanes < p.items) p.lanes *= 2;
   const int per_pass = kThreads / p.lanes;
+  p.step_t = per_pass / p.H;
+  p.step_h = per_pass % p.H;
   const int sms = sm_count();
   // tokens per CTA as in the head norm
   p.tokens = kMaxTokens;

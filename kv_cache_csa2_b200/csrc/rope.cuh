@@ -46,19 +46,16 @@ struct Num<__half> {
 };
 
 template <class T>
-__device__ __forceinline__ void unpack8(const uint4& v, float (&x)[8]) {
-  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    const float2 f = Num<T>::up(w[j]);
-    x[2 * j] = f.x;
-    x[2 * j + 1] = f.y;
-  }
+__device__ __forceinline__ void unpack8(const uint4& v, float2 (&x)[4]) {
+  x[0] = Num<T>::up(v.x);
+  x[1] = Num<T>::up(v.y);
+  x[2] = Num<T>::up(v.z);
+  x[3] = Num<T>::up(v.w);
 }
 template <class T>
-__device__ __forceinline__ uint4 pack8(const float (&x)[8]) {
-  return make_uint4(Num<T>::down(x[0], x[1]), Num<T>::down(x[2], x[3]), Num<T>::down(x[4], x[5]),
-                    Num<T>::down(x[6], x[7]));
+__device__ __forceinline__ uint4 pack8(const float2 (&x)[4]) {
+  return make_uint4(Num<T>::down(x[0].x, x[0].y), Num<T>::down(x[1].x, x[1].y), Num<T>::down(x[2].x, x[2].y),
+                    Num<T>::down(x[3].x, x[3].y));
 }
 
 // cos and sin of pos * f, the product and the reduction to one turn in 64 bits
@@ -100,26 +97,59 @@ __device__ __forceinline__ Item item_at(int i, int D, int half, int offset) {
   return it;
 }
 
-// Turns an item's pairs.  Every product and sum is rounded by itself, so the
-// result does not depend on how a compiler contracts them.
-__device__ __forceinline__ void turn(float& a, float& b, float2 cs) {
-  const float x = __fsub_rn(__fmul_rn(a, cs.x), __fmul_rn(b, cs.y));
-  const float y = __fadd_rn(__fmul_rn(b, cs.x), __fmul_rn(a, cs.y));
+// Pairs of f32 in one instruction, each rounded to nearest.
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+  float2 d;
+  asm("{.reg .b64 x, y, w; mov.b64 x, {%2, %3}; mov.b64 y, {%4, %5}; mul.rn.f32x2 w, x, y; mov.b64 {%0, %1}, w;}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return d;
+}
+__device__ __forceinline__ float2 sum2(float2 a, float2 b) {
+  float2 d;
+  asm("{.reg .b64 x, y, w; mov.b64 x, {%2, %3}; mov.b64 y, {%4, %5}; add.rn.f32x2 w, x, y; mov.b64 {%0, %1}, w;}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return d;
+}
+
+// A token's angles: entry e holds pairs 2 e and 2 e + 1 as (cos, cos, sin, sin), the
+// four entries of eight neighbouring pairs spread over four rows of half / 8, so
+// that neighbouring lanes read side by side (all in one row, four would share a bank).
+__device__ __forceinline__ int angle_slot(int f, int half) { return ((f >> 1) & 3) * (half >> 3) + (f >> 3); }
+__device__ __forceinline__ void put_angle(float4* cs, int f, int half, float2 v) {
+  float* e = reinterpret_cast<float*>(cs + angle_slot(f, half)) + (f & 1);
+  e[0] = v.x;
+  e[2] = v.y;
+}
+
+// Turns an item's pairs, two at a time.  Every product and sum is rounded by itself
+// (the product with -sin is the negative of the product with sin).
+__device__ __forceinline__ void turn2(float2& a, float2& b, const float4& cs) {
+  const float2 c = make_float2(cs.x, cs.y), s = make_float2(cs.z, cs.w), n = make_float2(-cs.z, -cs.w);
+  const float2 x = sum2(mul2(a, c), mul2(b, n));
+  const float2 y = sum2(mul2(b, c), mul2(a, s));
   a = x;
   b = y;
 }
-__device__ __forceinline__ void rotate_item(float (&x0)[8], float (&x1)[8], const Item& it, int half,
-                                            bool interleaved, const float2* cs) {
+__device__ __forceinline__ void rotate_item(float2 (&x0)[4], float2 (&x1)[4], const Item& it, int half,
+                                            bool interleaved, const float4* cs) {
   if (it.freq < 0) return;
   if (!interleaved) {
 #pragma unroll
-    for (int u = 0; u < 8; ++u) turn(x0[u], x1[u], cs[it.freq + u]);
+    for (int u = 0; u < 4; ++u) turn2(x0[u], x1[u], cs[angle_slot(it.freq + 2 * u, half)]);
   } else {
     const int f0 = it.freq >> 1, f1 = (it.freq + half) >> 1;
 #pragma unroll
-    for (int u = 0; u < 4; ++u) {
-      turn(x0[2 * u], x0[2 * u + 1], cs[f0 + u]);
-      turn(x1[2 * u], x1[2 * u + 1], cs[f1 + u]);
+    for (int u = 0; u < 4; u += 2) {
+      float2 a = make_float2(x0[u].x, x0[u + 1].x), b = make_float2(x0[u].y, x0[u + 1].y);
+      turn2(a, b, cs[angle_slot(f0 + u, half)]);
+      x0[u] = make_float2(a.x, b.x);
+      x0[u + 1] = make_float2(a.y, b.y);
+      a = make_float2(x1[u].x, x1[u + 1].x), b = make_float2(x1[u].y, x1[u + 1].y);
+      turn2(a, b, cs[angle_slot(f1 + u, half)]);
+      x1[u] = make_float2(a.x, b.x);
+      x1[u + 1] = make_float2(a.y, b.y);
     }
   }
 }
