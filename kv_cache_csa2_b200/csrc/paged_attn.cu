@@ -482,7 +482,7 @@ struct Split {
 // The chunk length of a decode launch.
 //  - wide rows on the tensor cores: one CTA per SM, so the number of chunks that
 //    wastes least, counting a chunk's start and partial output as 4 tiles
-//  - else about four CTAs per SM
+//  - else see below
 Split split_of(const PagedAttn& a, int64_t max_len, int chunk) {
   const int64_t seen = std::max<int64_t>(1, seen_bound(a, max_len));
   Split s;
@@ -511,8 +511,15 @@ Split split_of(const PagedAttn& a, int64_t max_len, int chunk) {
   const int64_t units = static_cast<int64_t>(a.kv.B) * a.kv.heads * ((a.G + 15) / 16);
   int64_t c = chunk;
   if (c == 0) {
-    const int64_t want = std::max<int64_t>(1, 4LL * sm_count() / std::max<int64_t>(1, units));
-    c = std::max<int64_t>(256, ((seen + want - 1) / want + 63) / 64 * 64);
+    // two CTAs per SM, but no chunk above 2048 tokens, so that long and short
+    // sequences side by side even out, and at most 64 chunks to join unless they
+    // hold 256 tokens.  Measured (us at chunks of 256 / 1024 / 2048 / 8192): 64
+    // ragged sequences up to 16K, 8 cache heads 338 / 243 / 236 / 285; one of 32K, 8
+    // heads 46 / 31 / 34 / 108; 64 of 2K, 4 heads 66 / 53 / 49 / 49; one of 8K, one
+    // head 9.6 / 17 / 27 / 90 (128: 9.3, 64: 10.3)
+    const int64_t n = std::max<int64_t>(1, 2LL * sm_count() / std::max<int64_t>(1, units));
+    c = std::max<int64_t>((seen + n - 1) / n, std::min<int64_t>(256, (seen + 63) / 64));
+    c = std::min<int64_t>(2048, std::max<int64_t>(64, (c + 63) / 64 * 64));
   }
   s.chunk = static_cast<int>(std::min<int64_t>(c, 0x7fffffc0));
   s.chunks = static_cast<int>((seen + s.chunk - 1) / s.chunk);
