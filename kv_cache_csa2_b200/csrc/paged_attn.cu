@@ -297,6 +297,9 @@ __global__ void __launch_bounds__(kThreads) paged_attn_kernel(const Params p) {
   }
   __syncthreads();
   const bool partial = decode && p.chunks > 1 && seen.total > p.chunk;
+  __shared__ uint8_t bad[16];                          // prompt rows to look at again
+  if (tid < 16) bad[tid] = 0;
+  __syncthreads();
 #pragma unroll
   for (int u = 0; u < 2; ++u) {
     const int r = (lane >> 2) + 8 * u;
@@ -313,12 +316,27 @@ __global__ void __launch_bounds__(kThreads) paged_attn_kernel(const Params p) {
     } else {
       const float inv = lr > 0.0f ? 1.0f / lr : (lr == 0.0f ? 0.0f : lr);
       uint16_t* po = p.out + at * D;
+      if (!FP4 && !decode && (__float_as_uint(lr) & 0x7f800000u) != 0x7f800000u) {
+        bool odd = false;
+#pragma unroll
+        for (int i = 0; i < NC / 8; ++i)
+          odd |= (__float_as_uint(o[i][2 * u]) & 0x7f800000u) == 0x7f800000u ||
+                 (__float_as_uint(o[i][2 * u + 1]) & 0x7f800000u) == 0x7f800000u;
+        if (odd) bad[r] = 1;
+      }
 #pragma unroll
       for (int i = 0; i < NC / 8; ++i)
         *reinterpret_cast<uint32_t*>(po + warp * NC + i * 8 + (lane & 3) * 2) =
             Num<T>::down(o[i][2 * u] * inv, o[i][2 * u + 1] * inv);
       if (p.lse && warp == 0 && (lane & 3) == 0)
         p.lse[at] = lr == 0.0f ? -INFINITY : (m[u] + log2f(lr)) * kLn2;
+    }
+  }
+  if (!FP4 && !decode) {
+    if (__syncthreads_or(tid < rows && bad[tid])) {
+      const MendRows m = {p.q + q_row0 * p.q_token, p.q_token, p.q_head, p.out + q_row0 * p.Hq * D, p.scale2, p.Hq, p.G, kvh,
+                          static_cast<int>(r0), base, p.window, p.sinks, seen.lo, seen.ns, pmax, b};
+      mend_rows<T, D>(m, p.kv, bad, static_cast<int>(rows), reinterpret_cast<uint32_t*>(sK), 2 * L::STAGE * 8);
     }
   }
 }

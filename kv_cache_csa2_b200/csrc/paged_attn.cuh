@@ -211,5 +211,87 @@ __device__ __forceinline__ bool wait_phase(uint64_t* bar, uint32_t parity, volat
   return __all_sync(0xffffffffu, ok);
 }
 
+// A weight of 0 times a value that is not finite is NaN, so in a tile such a value
+// reaches rows that do not see its token.  mend_rows finds those rows and computes
+// them again one by one; it runs only when an output is not finite although its row
+// sum is (a key that is not finite shows in the sum, and only where it is seen).
+//
+// All threads of the block take part (blockDim.x a multiple of 32), after every
+// output is stored.  bad[r] != 0: row r of n_rows wants a look.  Tokens [0, ns) and
+// [lo, pmax] are what the block has loaded; one bit each in `bitmap` says which hold
+// such a value (more tokens than `capacity` bits: the rows stay as they are).  A row
+// that sees one stays as it is; each other row is the f32 softmax over its own tokens.
+struct MendRows {
+  const uint16_t* q;                 // the sequence's first q row
+  int64_t q_token, q_head;
+  uint16_t* out;                     // its first output row, [token][Hq][D]
+  float scale2;                      // signed scale * log2(e)
+  int Hq, G, kvh, r0, base, window, sinks, lo, ns, pmax, b;
+};
+template <class T, int D>
+__device__ __noinline__ void mend_rows(const MendRows m, const PagedView& kv, const volatile uint8_t* bad, int n_rows,
+                                       uint32_t* bitmap, int capacity) {
+  constexpr int PER = D / 32;                          // channels per lane
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, warps = blockDim.x >> 5;
+  const int slots = m.ns + (m.pmax + 1 - m.lo);
+  if (slots > capacity) return;
+  for (int i = threadIdx.x; i < (slots + 31) / 32; i += blockDim.x) bitmap[i] = 0;
+  __syncthreads();
+  auto row_at = [&](const uint8_t* rows, int j) -> const uint16_t* {
+    const int64_t r = token_row(kv, m.b, j);
+    return r < 0 ? nullptr : reinterpret_cast<const uint16_t*>(rows) + r + m.kvh * kv.head_stride + lane * PER;
+  };
+  constexpr uint16_t EXP = std::is_same<T, __half>::value ? 0x7c00 : 0x7f80;
+  for (int i = warp; i < slots; i += warps) {
+    const uint16_t* v = row_at(kv.v, i < m.ns ? i : i - m.ns + m.lo);
+    bool odd = false;
+    if (v)
+      for (int e = 0; e < PER; ++e) odd |= (v[e] & EXP) == EXP;
+    if (__any_sync(0xffffffffu, odd) && lane == 0) atomicOr(bitmap + i / 32, 1u << (i % 32));
+  }
+  __syncthreads();
+  for (int r = warp; r < n_rows; r += warps) {
+    if (!bad[r]) continue;
+    const int tok = (m.r0 + r) / m.G, pos = m.base + tok, head = m.kvh * m.G + (m.r0 + r) % m.G;
+    bool reached = false;
+    for (int i = lane; i < slots; i += 32) {
+      const int j = i < m.ns ? i : i - m.ns + m.lo;
+      reached |= sees(pos, j, m.window, m.sinks) && ((bitmap[i / 32] >> (i % 32)) & 1u);
+    }
+    if (__any_sync(0xffffffffu, reached)) continue;
+    float qr[PER], acc[PER], mx = -INFINITY, l = 0.0f;
+    const uint16_t* q = m.q + tok * m.q_token + head * m.q_head + lane * PER;
+#pragma unroll
+    for (int e = 0; e < PER; ++e) {
+      const float2 f = rope::Num<T>::up(q[e]);
+      qr[e] = f.x;
+      acc[e] = 0.0f;
+    }
+    for (int i = 0; i < slots; ++i) {
+      const int j = i < m.ns ? i : i - m.ns + m.lo;
+      if (!sees(pos, j, m.window, m.sinks)) continue;
+      const uint16_t* k = row_at(kv.k, j);
+      if (!k) continue;
+      float s = 0.0f;
+#pragma unroll
+      for (int e = 0; e < PER; ++e) s += qr[e] * rope::Num<T>::up(k[e]).x;
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+      s *= m.scale2;
+      const float now = fmaxf(mx, s), ref = now == -INFINITY ? 0.0f : now;
+      const float f = exp2_approx(mx - ref), w = exp2_approx(s - ref);
+      const uint16_t* v = row_at(kv.v, j);
+      mx = now;
+      l = l * f + w;
+#pragma unroll
+      for (int e = 0; e < PER; ++e) acc[e] = acc[e] * f + w * rope::Num<T>::up(v[e]).x;
+    }
+    const float inv = l > 0.0f ? 1.0f / l : (l == 0.0f ? 0.0f : l);
+    uint16_t* o = m.out + (static_cast<int64_t>(tok) * m.Hq + head) * D + lane * PER;
+#pragma unroll
+    for (int e = 0; e < PER; ++e) o[e] = static_cast<uint16_t>(rope::Num<T>::down(acc[e] * inv, 0.0f) & 0xffffu);
+  }
+}
+
 }  // namespace paged
 }  // namespace csa2

@@ -65,7 +65,8 @@ struct Lay {
   static constexpr int NBAR = 2 * KST + 2 * VST + 4 + 4 + 4 + 2 + 1 + 1;
   static constexpr int BITS = BAR + NBAR * 8;
   static constexpr int MISC = BITS + kBits * 4 * 4;
-  static constexpr int BYTES = MISC + 16 + 1024;
+  static constexpr int BAD = MISC + 16;                // rows to look at again
+  static constexpr int BYTES = BAD + 2 * RT + 1024;
 };
 
 struct Params {
@@ -691,6 +692,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_window_kernel(const Params 
       // through the row tile's q rows, which no product reads any more, so that a
       // warp stores whole rows
       uint8_t* const stage = smem + L::Q + w * L::TILE;
+      bool odd = false;                                // an output that is not finite
 #pragma unroll
       for (int c = 0; c < D / 32; ++c) {
         uint32_t v[32];
@@ -701,6 +703,9 @@ __global__ void __launch_bounds__(kThreads, 1) paged_window_kernel(const Params 
 #pragma unroll
           for (int i = 0; i < 32; ++i) v[i] = 0;
         }
+        if (!FP4)
+#pragma unroll
+          for (int i = 0; i < 32; ++i) odd |= (v[i] & 0x7f800000u) == 0x7f800000u;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           uint32_t x[4];
@@ -720,8 +725,13 @@ __global__ void __launch_bounds__(kThreads, 1) paged_window_kernel(const Params 
         const uint4 x = *reinterpret_cast<const uint4*>(stage + (c / 8) * L::BLK + sw128_offset(row, c % 8));
         if (to >= 0) reinterpret_cast<uint4*>(p.out + to)[c] = x;
       }
+      if (!FP4) smem[L::BAD + w * RT + r] = odd && live && (__float_as_uint(sum) & 0x7f800000u) != 0x7f800000u;
       if (live && p.lse) p.lse[at] = sum == 0.0f ? -INFINITY : (m + log2f(sum)) * kLn2;
     }
+    // back to the launch's registers: what mend_rows below counts on.  The other
+    // warps take theirs only behind the barrier: an idle one that took them back
+    // earlier would keep them from this role's start.
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 128;");
   }
   // every product has completed before TMEM and shared memory go
   volatile int never = 0;                              // also when a wait gave up: the products still end
@@ -732,6 +742,17 @@ __global__ void __launch_bounds__(kThreads, 1) paged_window_kernel(const Params 
   if (warp == 8) {
     tc_fence_after();
     tmem_dealloc(tmem, 512);
+  }
+  if (!FP4) {
+    const bool look = !*abort_flag && threadIdx.x < wk.n_rows && smem[L::BAD + threadIdx.x];
+    if (__syncthreads_or(look)) {
+      if (warp >= 8) asm volatile("setmaxnreg.inc.sync.aligned.u32 128;");
+      const MendRows m = {p.q + static_cast<int64_t>(wk.q_row0) * p.q_token, p.q_token, p.q_head,
+                    p.out + static_cast<int64_t>(wk.q_row0) * p.Hq * D, p.flip ? -p.scale2 : p.scale2, p.Hq, p.G, kvh, wk.r0,
+                    wk.base, p.window, p.sinks, wk.lo, wk.ns, wk.pmax, wk.b};
+      mend_rows<T, D>(m, p.kv, smem + L::BAD, wk.n_rows, reinterpret_cast<uint32_t*>(smem + L::K),
+                      (L::KST + L::VST) * L::TILE * 8);
+    }
   }
 }
 

@@ -320,6 +320,35 @@ def test_window_ignores_what_ran_before(D, page, shared):
         P.check_attn(out, lse, want, P.f64(q), host[0][0], 0.1, torch.bfloat16, 300)
 
 
+@pytest.mark.parametrize("kind,D,G,page,shared,window,sinks,scale", [
+    ("bf16", 128, 8, 16, False, 0, 0, 0.1), ("f16", 64, 3, 64, False, 50, 4, 0.1), ("bf16", 64, 1, 4, False, 33, 0, -0.1),
+    ("bf16", 128, 16, 32, True, 40, 0, 0.1), ("f16", 256, 2, 16, False, 50, 4, 0.1), ("bf16", 512, 4, 16, True, 0, 0, -0.1)])
+def test_window_masked_values_that_are_not_finite(kind, D, G, page, shared, window, sinks, scale):
+    """A NaN or infinite row reaches only the queries that see its token."""
+    n, L = 150, 260
+    cache, host = P.make_cache(kind, [L], page, 1, D, shared=shared, seed=93)
+    dt = cache.dtype
+    table = cache.table.cpu().numpy()
+    odd = {141: float("nan"), 200: float("inf"), 201: float("-inf"), 259: float("nan")}
+    for j, x in odd.items():
+        rows = cache.k if shared else cache.v
+        rows[table[0, j // page], j % page, 0, 3 * j % D] = x
+    q = P.rng_normal(94, n, G, D, dt=dt)
+    out, lse = K.csa2_paged_window_attn(q, torch.tensor([0, n], dtype=torch.int32, device="cuda"), cache, scale,
+                                        window=window, sinks=sinks)
+    pos = np.arange(L - n, L)
+    sees = lambda j: (j <= pos) & ((window == 0) | (pos - j < window) | (j < sinks))
+    clean = ~np.any([sees(j) for j in odd], 0)
+    assert 20 < clean.sum() < n
+    rows = torch.from_numpy(np.flatnonzero(clean)).cuda()
+    want = O.causal_attn(P.f64(q[rows]), pos[clean], *host[0], scale, window, sinks)
+    P.check_attn(out[rows], lse[rows], want, P.f64(q[rows]), host[0][0], abs(scale), dt, L)
+    if not shared:
+        got = P.f64(out)
+        for j in odd:
+            assert not np.isfinite(got[sees(j)][:, :, 3 * j % D]).any()
+
+
 def test_window_bad_cu_q():
     cache, _ = P.make_cache("bf16", [50, 50, 50], 16, 1, 64, seed=85)
     q = P.rng_normal(86, 40, 2, 64)
