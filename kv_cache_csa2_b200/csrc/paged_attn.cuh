@@ -229,7 +229,7 @@ struct MendRows {
   int Hq, G, kvh, r0, base, window, sinks, lo, ns, pmax, b;
 };
 template <class T, int D>
-__device__ __noinline__ void mend_rows(const MendRows m, const PagedView& kv, const volatile uint8_t* bad, int n_rows,
+__device__ __forceinline__ void mend_rows(const MendRows m, const PagedView& kv, const volatile uint8_t* bad, int n_rows,
                                        uint32_t* bitmap, int capacity) {
   constexpr int PER = D / 32;                          // channels per lane
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, warps = blockDim.x >> 5;

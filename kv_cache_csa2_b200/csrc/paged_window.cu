@@ -704,8 +704,13 @@ __global__ void __launch_bounds__(kThreads, 1) paged_window_kernel(const Params 
           for (int i = 0; i < 32; ++i) v[i] = 0;
         }
         if (!FP4)
+        {
+          float2 z = make_float2(0.0f, 0.0f);          // stays 0 for finite values
 #pragma unroll
-          for (int i = 0; i < 32; ++i) odd |= (v[i] & 0x7f800000u) == 0x7f800000u;
+          for (int i = 0; i < 16; ++i)
+            z = fma2(make_float2(__uint_as_float(v[2 * i]), __uint_as_float(v[2 * i + 1])), make_float2(0.0f, 0.0f), z);
+          odd |= !(z.x + z.y == 0.0f);
+        }
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           uint32_t x[4];
@@ -728,10 +733,6 @@ __global__ void __launch_bounds__(kThreads, 1) paged_window_kernel(const Params 
       if (!FP4) smem[L::BAD + w * RT + r] = odd && live && (__float_as_uint(sum) & 0x7f800000u) != 0x7f800000u;
       if (live && p.lse) p.lse[at] = sum == 0.0f ? -INFINITY : (m + log2f(sum)) * kLn2;
     }
-    // back to the launch's registers: what mend_rows below counts on.  The other
-    // warps take theirs only behind the barrier: an idle one that took them back
-    // earlier would keep them from this role's start.
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 128;");
   }
   // every product has completed before TMEM and shared memory go
   volatile int never = 0;                              // also when a wait gave up: the products still end
@@ -744,13 +745,16 @@ __global__ void __launch_bounds__(kThreads, 1) paged_window_kernel(const Params 
     tmem_dealloc(tmem, 512);
   }
   if (!FP4) {
-    const bool look = !*abort_flag && threadIdx.x < wk.n_rows && smem[L::BAD + threadIdx.x];
+    const bool look = !*abort_flag && threadIdx.x < 2 * RT && smem[L::BAD + threadIdx.x];
     if (__syncthreads_or(look)) {
-      if (warp >= 8) asm volatile("setmaxnreg.inc.sync.aligned.u32 128;");
-      const MendRows m = {p.q + static_cast<int64_t>(wk.q_row0) * p.q_token, p.q_token, p.q_head,
-                    p.out + static_cast<int64_t>(wk.q_row0) * p.Hq * D, p.flip ? -p.scale2 : p.scale2, p.Hq, p.G, kvh, wk.r0,
-                    wk.base, p.window, p.sinks, wk.lo, wk.ns, wk.pmax, wk.b};
-      mend_rows<T, D>(m, p.kv, smem + L::BAD, wk.n_rows, reinterpret_cast<uint32_t*>(smem + L::K),
+      // located anew: keeping the work alive to here cost 13 us of 291
+      Work again;
+      locate(p, blockIdx.x, again);
+      const MendRows m = {p.q + static_cast<int64_t>(again.q_row0) * p.q_token, p.q_token, p.q_head,
+                          p.out + static_cast<int64_t>(again.q_row0) * p.Hq * D, p.flip ? -p.scale2 : p.scale2, p.Hq, p.G,
+                          static_cast<int>(blockIdx.y), again.r0, again.base, p.window, p.sinks, again.lo, again.ns,
+                          again.pmax, again.b};
+      mend_rows<T, D>(m, p.kv, smem + L::BAD, again.n_rows, reinterpret_cast<uint32_t*>(smem + L::K),
                       (L::KST + L::VST) * L::TILE * 8);
     }
   }
