@@ -349,6 +349,28 @@ def test_window_masked_values_that_are_not_finite(kind, D, G, page, shared, wind
             assert not np.isfinite(got[sees(j)][:, :, 3 * j % D]).any()
 
 
+def test_window_scores_far_below_the_maximum():
+    """Scores thousands below the row's largest weigh nothing; equal scores weigh the same."""
+    cache, host = P.make_cache("bf16", [200], 16, 1, 64, seed=97, std=20.0)
+    q = P.rng_normal(98, 70, 4, 64, std=20.0)
+    cu = torch.tensor([0, 70], dtype=torch.int32, device="cuda")
+    out, lse = K.csa2_paged_window_attn(q, cu, cache, 1.0)
+    qh, pos = P.f64(q), np.arange(130, 200)
+    want = O.causal_attn(qh, pos, *host[0], 1.0)
+    s = np.einsum("qhd,kd->qhk", qh, host[0][0][:, 0])
+    s = np.where(np.arange(200) > pos[:, None, None], -np.inf, s)
+    order = np.sort(s, -1)
+    alone = order[..., -1] - order[..., -2] > 40                     # the other weights are below e^-40
+    assert alone.mean() > 0.5
+    np.testing.assert_array_equal(P.f64(out)[alone], host[0][1][np.argmax(s, -1), 0][alone])
+    np.testing.assert_allclose(P.f64(lse)[alone], want[1][alone], rtol=2.0 ** -20)
+    out, lse = K.csa2_paged_window_attn(torch.zeros_like(q), cu, cache, 1.0)
+    for i in (0, 69):
+        mean, mag = host[0][1][:pos[i] + 1, 0].mean(0), np.abs(host[0][1][:pos[i] + 1, 0]).mean(0)
+        assert np.all(np.abs(P.f64(out[i]) - mean) <= P.half_step(torch.bfloat16) * (np.abs(mean) + 1.02 * mag) + 2e-5 * mag)
+    np.testing.assert_allclose(P.f64(lse), np.log(pos + 1.0)[:, None].repeat(4, 1), rtol=2.0 ** -20)
+
+
 def test_window_bad_cu_q():
     cache, _ = P.make_cache("bf16", [50, 50, 50], 16, 1, 64, seed=85)
     q = P.rng_normal(86, 40, 2, 64)
