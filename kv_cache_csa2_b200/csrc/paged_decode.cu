@@ -4,7 +4,7 @@
 //
 // HBM-bound: every cached row is read once and meets 16 query rows.  What counts
 // is bytes in flight, so every warp works alone: it streams its own slices of 16
-// tokens through a private ring in shared memory (cp.async, no block barrier in
+// tokens (32 of FP4 rows) through a private ring in shared memory (cp.async, no block barrier in
 // the loop) and keeps its own running maximum, sum and output in registers; the
 // 4 warps meet once at the end.  A page lookup runs one slice ahead of its loads.
 //   S[16 heads, 16 tokens] = q k^T, P = 2^(S - m), O[16 heads, D] += P v
@@ -30,14 +30,14 @@ using rope::Num;
 
 constexpr int kWarps = 4;
 constexpr int kThreads = kWarps * 32;
-constexpr int KS = 16;                                 // tokens per slice
 
 template <int D, bool FP4>
 struct Lay {
+  static constexpr int KS = FP4 && D <= 128 ? 32 : 16;             // tokens per slice
   static constexpr int ROW = FP4 ? D / 2 + 16 : 2 * D + 16;        // padded row in shared memory
   static constexpr int SC = FP4 ? KS * (D / 16) : 0;               // a slice's scales
   static constexpr int HALF = KS * ROW + SC;                       // keys (or values) of a slice
-  static constexpr int STAGES = FP4 ? 6 : D == 64 ? 6 : D == 128 ? 3 : 2;
+  static constexpr int STAGES = FP4 ? (D <= 128 ? 3 : 6) : D == 64 ? 6 : D == 128 ? 3 : 2;
   static constexpr int warp_bytes(bool shared) { return STAGES * HALF * (shared ? 1 : 2); }
   static constexpr int MERGE = kWarps * 16 * (D + 4) * 4 + kWarps * 16 * 8;
   static constexpr int bytes(bool shared) {
@@ -89,6 +89,7 @@ struct Params {
 template <class T, int D, bool FP4, bool SHARED>
 __global__ void __launch_bounds__(kThreads) paged_decode_kernel(const Params p) {
   using L = Lay<D, FP4>;
+  constexpr int KS = L::KS;
   extern __shared__ __align__(16) uint8_t smem[];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int n8 = lane >> 2, c4 = lane & 3;             // fragment coordinates
@@ -109,7 +110,7 @@ __global__ void __launch_bounds__(kThreads) paged_decode_kernel(const Params p) 
 
   // the row (channel offset) of this lane's token in slice s; -1: none
   auto row_of = [&](int s) -> int64_t {
-    const int i = v0 + s * KS + (lane & 15);
+    const int i = v0 + s * KS + (lane & (KS - 1));
     if (s >= slices || i >= v1) return -1;
     const int64_t r = token_row(p.kv, b, seen.token(i));
     return r < 0 ? -1 : r + kvh * p.kv.head_stride;
@@ -142,7 +143,7 @@ __global__ void __launch_bounds__(kThreads) paged_decode_kernel(const Params p) 
         }
       }
     }
-    return __ballot_sync(0xffffffffu, row >= 0) & 0xffffu;
+    return __ballot_sync(0xffffffffu, row >= 0);
   };
 
   // q fragments.  16-bit rows: the plain order.  FP4: the order of the code words:
@@ -212,14 +213,15 @@ __global__ void __launch_bounds__(kThreads) paged_decode_kernel(const Params p) 
     }
     const uint32_t kb = ring + stage * STAGE, vb = SHARED ? kb : kb + L::HALF;
 
-    float sc[2][4];
+    constexpr int NT = KS / 8;                         // 8-token tiles of a slice
+    float sc[NT][4];
 #pragma unroll
-    for (int i = 0; i < 2; ++i) sc[i][0] = sc[i][1] = sc[i][2] = sc[i][3] = 0.0f;
+    for (int i = 0; i < NT; ++i) sc[i][0] = sc[i][1] = sc[i][2] = sc[i][3] = 0.0f;
     if (!FP4) {
 #pragma unroll
       for (int k = 0; k < D / 16; k += 2) {
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {                  // 8 tokens x 32 channels
+        for (int i = 0; i < NT; ++i) {                 // 8 tokens x 32 channels
           uint32_t bb[4];
           ldsm4(bb, kb + (i * 8 + (lane & 7)) * L::ROW + k * 32 + (lane >> 3) * 16);
           mma16816<T>(sc[i], qa[k], bb[0], bb[1]);
@@ -230,7 +232,7 @@ __global__ void __launch_bounds__(kThreads) paged_decode_kernel(const Params p) 
 #pragma unroll
       for (int g = 0; g < D / 32; ++g) {
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
+        for (int i = 0; i < NT; ++i) {
           const int r = i * 8 + n8;
           const uint32_t w = lds32(kb + r * L::ROW + (4 * g + c4) * 4);
           const uint32_t s2 = scale_2p63(lds8(kb + KS * L::ROW + r * (D / 16) + 2 * g + (c4 >> 1)));
@@ -241,7 +243,7 @@ __global__ void __launch_bounds__(kThreads) paged_decode_kernel(const Params p) 
     }
     float mx[2] = {-INFINITY, -INFINITY};
 #pragma unroll
-    for (int i = 0; i < 2; ++i)
+    for (int i = 0; i < NT; ++i)
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
         const bool ok = (mask >> (i * 8 + c4 * 2 + (e & 1))) & 1u;
@@ -259,18 +261,21 @@ __global__ void __launch_bounds__(kThreads) paged_decode_kernel(const Params p) 
       m[u] = mn;
       l[u] *= alpha[u];
 #pragma unroll
-      for (int i = 0; i < 2; ++i)
+      for (int i = 0; i < NT; ++i)
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
           sc[i][2 * u + e] = exp2_approx(sc[i][2 * u + e] - ref);
           l[u] += sc[i][2 * u + e];
         }
     }
-    uint32_t pa[4];                                    // P as the next product's left operand
-    pa[0] = Num<T>::down(sc[0][0], sc[0][1]);
-    pa[1] = Num<T>::down(sc[0][2], sc[0][3]);
-    pa[2] = Num<T>::down(sc[1][0], sc[1][1]);
-    pa[3] = Num<T>::down(sc[1][2], sc[1][3]);
+    uint32_t pa[KS / 16][4];                           // P as the next product's left operand
+#pragma unroll
+    for (int t = 0; t < KS / 16; ++t) {
+      pa[t][0] = Num<T>::down(sc[2 * t][0], sc[2 * t][1]);
+      pa[t][1] = Num<T>::down(sc[2 * t][2], sc[2 * t][3]);
+      pa[t][2] = Num<T>::down(sc[2 * t + 1][0], sc[2 * t + 1][1]);
+      pa[t][3] = Num<T>::down(sc[2 * t + 1][2], sc[2 * t + 1][3]);
+    }
     if (__any_sync(0xffffffffu, alpha[0] != 1.0f || alpha[1] != 1.0f)) {
 #pragma unroll
       for (int i = 0; i < D / 8; ++i) {
@@ -280,31 +285,34 @@ __global__ void __launch_bounds__(kThreads) paged_decode_kernel(const Params p) 
         o[i][3] *= alpha[1];
       }
     }
-    if (!FP4) {
 #pragma unroll
-      for (int i = 0; i < D / 16; ++i) {               // 16 tokens x 16 channels
-        uint32_t bb[4];
-        ldsm4t(bb, vb + (lane & 15) * L::ROW + (i * 16 + (lane >> 4) * 8) * 2);
-        mma16816<T>(o[2 * i], pa, bb[0], bb[1]);
-        mma16816<T>(o[2 * i + 1], pa, bb[2], bb[3]);
-      }
-    } else {
-      // word n8 of a group of 64 channels, of tokens 2 c4, 2 c4 + 1, 2 c4 + 8, 2 c4 + 9
+    for (int t = 0; t < KS / 16; ++t) {
+      if (!FP4) {
 #pragma unroll
-      for (int g = 0; g < D / 64; ++g) {
-        uint32_t w[4], s2[4];
-#pragma unroll
-        for (int u = 0; u < 4; ++u) {
-          const int r = 2 * c4 + (u & 1) + 8 * (u >> 1);
-          w[u] = lds32(vb + r * L::ROW + (8 * g + n8) * 4);
-          s2[u] = scale_2p63(lds8(vb + KS * L::ROW + r * (D / 16) + 4 * g + (n8 >> 1)));
+        for (int i = 0; i < D / 16; ++i) {             // 16 tokens x 16 channels
+          uint32_t bb[4];
+          ldsm4t(bb, vb + (t * 16 + (lane & 15)) * L::ROW + (i * 16 + (lane >> 4) * 8) * 2);
+          mma16816<T>(o[2 * i], pa[t], bb[0], bb[1]);
+          mma16816<T>(o[2 * i + 1], pa[t], bb[2], bb[3]);
         }
+      } else {
+        // word n8 of a group of 64 channels, of tokens 2 c4, 2 c4 + 1, 2 c4 + 8, 2 c4 + 9
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {                  // channels k and k + 4 of the word
-          const uint32_t x0 = code_pair(w[0], k, s2[0]), x1 = code_pair(w[1], k, s2[1]);
-          const uint32_t y0 = code_pair(w[2], k, s2[2]), y1 = code_pair(w[3], k, s2[3]);
-          mma16816<T>(o[8 * g + k], pa, __byte_perm(x0, x1, 0x5410), __byte_perm(y0, y1, 0x5410));
-          mma16816<T>(o[8 * g + k + 4], pa, __byte_perm(x0, x1, 0x7632), __byte_perm(y0, y1, 0x7632));
+        for (int g = 0; g < D / 64; ++g) {
+          uint32_t w[4], s2[4];
+#pragma unroll
+          for (int u = 0; u < 4; ++u) {
+            const int r = t * 16 + 2 * c4 + (u & 1) + 8 * (u >> 1);
+            w[u] = lds32(vb + r * L::ROW + (8 * g + n8) * 4);
+            s2[u] = scale_2p63(lds8(vb + KS * L::ROW + r * (D / 16) + 4 * g + (n8 >> 1)));
+          }
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {                // channels k and k + 4 of the word
+            const uint32_t x0 = code_pair(w[0], k, s2[0]), x1 = code_pair(w[1], k, s2[1]);
+            const uint32_t y0 = code_pair(w[2], k, s2[2]), y1 = code_pair(w[3], k, s2[3]);
+            mma16816<T>(o[8 * g + k], pa[t], __byte_perm(x0, x1, 0x5410), __byte_perm(y0, y1, 0x5410));
+            mma16816<T>(o[8 * g + k + 4], pa[t], __byte_perm(x0, x1, 0x7632), __byte_perm(y0, y1, 0x7632));
+          }
         }
       }
     }
