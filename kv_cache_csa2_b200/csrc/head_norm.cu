@@ -47,7 +47,7 @@ __device__ __forceinline__ void scale8(float2 (&x)[4], float inv, const float* w
 }
 
 template <class T>
-__global__ void __launch_bounds__(kThreads) head_norm_kernel(const Params p) {
+__global__ void __launch_bounds__(kThreads, 4) head_norm_kernel(const Params p) {
   extern __shared__ float4 cs[];                                   // [tokens][half / 2]
   const int64_t t0 = static_cast<int64_t>(blockIdx.x) * p.tokens;
   const int nt = static_cast<int>(min(static_cast<int64_t>(p.tokens), p.T - t0));

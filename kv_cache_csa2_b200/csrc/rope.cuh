@@ -105,13 +105,6 @@ __device__ __forceinline__ float2 mul2(float2 a, float2 b) {
       : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
   return d;
 }
-__device__ __forceinline__ float2 sum2(float2 a, float2 b) {
-  float2 d;
-  asm("{.reg .b64 x, y, w; mov.b64 x, {%2, %3}; mov.b64 y, {%4, %5}; add.rn.f32x2 w, x, y; mov.b64 {%0, %1}, w;}"
-      : "=f"(d.x), "=f"(d.y)
-      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
-  return d;
-}
 
 // A token's angles: entry e holds pairs 2 e and 2 e + 1 as (cos, cos, sin, sin), the
 // four entries of eight neighbouring pairs spread over four rows of half / 8, so
@@ -123,14 +116,14 @@ __device__ __forceinline__ void put_angle(float4* cs, int f, int half, float2 v)
   e[2] = v.y;
 }
 
-// Turns an item's pairs, two at a time.  Every product and sum is rounded by itself
-// (the product with -sin is the negative of the product with sin).
+// Turns an item's pairs, two at a time.  Every product and sum is rounded by itself;
+// the sums are not paired, because the assembler joins a paired product with a
+// paired sum that takes it, .rn or not, and then rounds once.
 __device__ __forceinline__ void turn2(float2& a, float2& b, const float4& cs) {
-  const float2 c = make_float2(cs.x, cs.y), s = make_float2(cs.z, cs.w), n = make_float2(-cs.z, -cs.w);
-  const float2 x = sum2(mul2(a, c), mul2(b, n));
-  const float2 y = sum2(mul2(b, c), mul2(a, s));
-  a = x;
-  b = y;
+  const float2 c = make_float2(cs.x, cs.y), s = make_float2(cs.z, cs.w);
+  const float2 ac = mul2(a, c), bs = mul2(b, s), bc = mul2(b, c), as = mul2(a, s);
+  a = make_float2(__fsub_rn(ac.x, bs.x), __fsub_rn(ac.y, bs.y));
+  b = make_float2(__fadd_rn(bc.x, as.x), __fadd_rn(bc.y, as.y));
 }
 __device__ __forceinline__ void rotate_item(float2 (&x0)[4], float2 (&x1)[4], const Item& it, int half,
                                             bool interleaved, const float4* cs) {

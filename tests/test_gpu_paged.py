@@ -485,3 +485,22 @@ def test_calls_on_a_side_stream():
     s.synchronize()
     for o, l in got:
         assert torch.equal(o, want[0]) and torch.equal(l, want[1])
+
+
+@pytest.mark.parametrize("inter", [False, True])
+def test_rotation_rounds_every_step(inter):
+    """The rotation's f32 steps one by one (products, then their sum, then the 16-bit type), as
+    the header states them: the same bits as separate torch operations."""
+    T, H, D, half = 500, 8, 128, 64
+    x = P.rng_normal(121, T, H, D, dt=torch.float16)
+    pos = torch.arange(T, dtype=torch.int32, device="cuda") * 1931
+    f = _freq(half)
+    got = K.csa2_qk_norm_rope(x, None, pos, rope=K.Rope(f, interleaved=inter))[0]
+    angle = pos.double()[:, None, None] * f.double()
+    cos, sin = angle.cos().float(), angle.sin().float()
+    y = x.float()
+    a, b = (y[..., 0::2], y[..., 1::2]) if inter else (y[..., :half], y[..., half:])
+    a, b = a * cos - b * sin, b * cos + a * sin
+    want = (torch.stack((a, b), -1).flatten(-2) if inter else torch.cat((a, b), -1)).half()
+    # the angle's sine may round to its neighbour (64-bit sines differ in their last bit)
+    assert (got != want).sum().item() <= 2
