@@ -223,6 +223,8 @@ csa2_status csa2_paged_decode_attn(const csa2_heads* q, const csa2_paged_kv* cac
   REQUIRE(chunk >= 0 && chunk % 64 == 0, "%s: chunk=%d must be a multiple of 64", fn, chunk);
   if (cache->B == 0) return CSA2_OK;
   REQUIRE(cache->B <= 65535, "%s: B=%d above 65535", fn, cache->B);
+  if (static_cast<int64_t>(a.kv.heads) * ((a.G + 15) / 16) > 65535)
+    return fail(CSA2_ERR_UNSUPPORTED, "%s: %d query heads over %d cache heads", fn, a.Hq, a.kv.heads);
   REQUIRE(out != nullptr && aligned16(out), "%s: out is null or not 16-byte aligned", fn);
   const size_t need = paged_decode_workspace(a, max_len, chunk);
   if (workspace_bytes < need || (need > 0 && (!workspace || !aligned16(workspace))))

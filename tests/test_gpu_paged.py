@@ -504,3 +504,49 @@ def test_rotation_rounds_every_step(inter):
     want = (torch.stack((a, b), -1).flatten(-2) if inter else torch.cat((a, b), -1)).half()
     # the angle's sine may round to its neighbour (64-bit sines differ in their last bit)
     assert (got != want).sum().item() <= 2
+
+
+def test_two_graphs_interleaved_and_two_streams():
+    """Split decode calls captured in two graphs, replayed in turn and on two streams at once:
+    each call has scratch of its own."""
+    caches = [P.make_cache("bf16", [4000, 900], 64, 1, 128, shared=True, seed=130 + i)[0] for i in range(2)]
+    qs = [P.rng_normal(135 + i, 2, 16, 128) for i in range(2)]
+    want = [K.csa2_paged_decode_attn(q, c, 0.1) for q, c in zip(qs, caches)]
+    graphs, outs = [], []
+    for q, c in zip(qs, caches):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            outs.append(K.csa2_paged_decode_attn(q, c, 0.1))
+        graphs.append(g)
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    torch.cuda.synchronize()
+    for _ in range(5):
+        for o, l in outs:
+            o.zero_(), l.zero_()
+        torch.cuda.synchronize()
+        for g, s in zip(graphs, streams):
+            with torch.cuda.stream(s):
+                g.replay()
+        torch.cuda.synchronize()
+        for (o, l), (wo, wl) in zip(outs, want):
+            assert torch.equal(o, wo) and torch.equal(l, wl)
+
+
+def test_empty_batches_do_nothing():
+    k = torch.zeros(4, 16, 2, 64, dtype=torch.bfloat16, device="cuda")
+    none = torch.zeros(0, dtype=torch.int32, device="cuda")
+    cache = K.PagedKv(k, torch.zeros(0, 3, dtype=torch.int32, device="cuda"), none, v=torch.zeros_like(k))
+    q = torch.zeros(0, 4, 64, dtype=torch.bfloat16, device="cuda")
+    assert K.csa2_paged_decode_attn(q, cache, 1.0)[0].shape == (0, 4, 64)
+    one = torch.zeros(1, dtype=torch.int32, device="cuda")
+    assert K.csa2_paged_window_attn(q, one, cache, 1.0)[1].shape == (0, 4)
+    K.csa2_paged_append(cache, q[:, :2], q[:, :2], none, none)
+    assert K.csa2_qk_norm_rope(q, q[:, :2])[1].shape == (0, 2, 64)
+    # no pages at all: every sequence is empty
+    bare = K.PagedKv(k[:0], torch.zeros(3, 0, dtype=torch.int32, device="cuda"),
+                     torch.zeros(3, dtype=torch.int32, device="cuda"), v=k[:0])
+    out, lse = K.csa2_paged_decode_attn(torch.ones(3, 4, 64, dtype=torch.bfloat16, device="cuda"), bare, 1.0)
+    assert torch.all(out == 0) and torch.all(torch.isneginf(lse))
+    out, lse = K.csa2_paged_window_attn(torch.ones(3, 4, 64, dtype=torch.bfloat16, device="cuda"),
+                                        torch.arange(4, dtype=torch.int32, device="cuda"), bare, 1.0)
+    assert torch.all(out == 0) and torch.all(torch.isneginf(lse))
