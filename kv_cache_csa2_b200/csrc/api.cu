@@ -239,7 +239,7 @@ const char* csa2_status_string(csa2_status s) {
 
 const char* csa2_last_error(void) { return t_msg; }
 
-int csa2_version(void) { return 2; }
+int csa2_version(void) { return 3; }
 
 csa2_status csa2_set_device_wait(uint64_t limit_ns, int unreachable) {
   g_wait_ns.store(limit_ns);

@@ -80,6 +80,9 @@ csa2_status launch_paged_window_tc(const PagedAttn& a, const int32_t* cu_q, int6
 // 128 tokens; the caller joins them.
 bool paged_wide_applies(const PagedAttn& a);
 int paged_wide_heads(const PagedAttn& a);            // query heads per CTA
+// A prompt by the same kernel, one CTA per token.
+bool paged_wide_prompt_applies(const PagedAttn& a);
+csa2_status launch_paged_wide_prompt(const PagedAttn& a, const int32_t* cu_q, int64_t T, cudaStream_t stream);
 csa2_status launch_paged_wide(const PagedAttn& a, int chunk, int chunks, float* part_o, float2* part_ml,
                               cudaStream_t stream);
 csa2_status launch_paged_window(const PagedAttn& a, const int32_t* cu_q, int64_t T, cudaStream_t stream);

@@ -245,6 +245,8 @@ csa2_status csa2_paged_window_attn(const csa2_heads* q, const int32_t* cu_q, int
   CSA2_TRY(attn_of(fn, q, T, cache, scale, window, sinks, &a, nullptr));
   if (T == 0 || cache->B == 0) return CSA2_OK;
   REQUIRE(cu_q != nullptr, "%s: cu_q is null", fn);
+  if (static_cast<int64_t>(a.kv.heads) * ((a.G + 15) / 16) > 65535)
+    return fail(CSA2_ERR_UNSUPPORTED, "%s: %d query heads over %d cache heads", fn, a.Hq, a.kv.heads);
   REQUIRE(out != nullptr && aligned16(out), "%s: out is null or not 16-byte aligned", fn);
   a.out = out;
   a.lse = lse;

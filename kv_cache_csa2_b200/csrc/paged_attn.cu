@@ -578,6 +578,7 @@ csa2_status launch_paged_decode(const PagedAttn& a, int64_t max_len, int chunk, 
 
 csa2_status launch_paged_window(const PagedAttn& a, const int32_t* cu_q, int64_t T, cudaStream_t stream) {
   if (paged_window_tc_applies(a)) return launch_paged_window_tc(a, cu_q, T, stream);
+  if (paged_wide_prompt_applies(a)) return launch_paged_wide_prompt(a, cu_q, T, stream);
   Params p = params_of(a);
   p.cu_q = cu_q;
   p.T = T;

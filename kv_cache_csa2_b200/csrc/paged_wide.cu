@@ -1,6 +1,7 @@
-// Attention of one new token per sequence over a paged cache with many query heads
-// per cache head (a shared 512-wide row under 64 heads: 128 flops per byte), on the
-// 5th-generation tensor cores.
+// Attention over a paged cache of a token's many query heads per cache head (a shared
+// 512-wide row under 64 heads: 128 flops per byte), on the 5th-generation tensor
+// cores: one new token per sequence, its keys cut into chunks, or a prompt, one CTA
+// per token (all its rows see the same keys).
 //
 // A CTA takes up to NH query heads of one cache head and a run of key tiles of 128
 // tokens.  Keys stand on the M side, heads on the N side, so that a cached row is
@@ -71,6 +72,8 @@ struct Params {
   float2* part_ml;
   float scale2;                      // |scale| * log2(e), at least the smallest normal
   uint32_t flip;                     // 0x80008000 for a negative scale
+  const int32_t* cu_q;               // prompt: [B + 1]; null: decode
+  int T;                             // prompt: rows of q
   int Hq, G, row_tiles, window, sinks, chunk, chunks;
   int box;                           // rows of a TMA box
   PagedView kv;
@@ -110,12 +113,41 @@ __global__ void __launch_bounds__(Lay<D, NH>::THREADS, 1)
   float* red = reinterpret_cast<float*>(smem + L::RED);
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int b = blockIdx.z, chunk = blockIdx.x;
+  int b = blockIdx.z, token = blockIdx.z;              // sequence, row of q
+  const int chunk = p.cu_q ? 0 : blockIdx.x;
   const int kvh = blockIdx.y / p.row_tiles, h0 = NH * (blockIdx.y % p.row_tiles);
   const int rows = min(NH, p.G - h0);
   pdl_wait();
-  const int len = length_of(p.kv, b, threadIdx.x == 0);
-  const AlignedTiles at(len - 1, p.window, p.sinks);
+  int pos;
+  if (p.cu_q) {
+    // the sequence of this token (late tokens see most and start first)
+    token = p.T - 1 - static_cast<int>(blockIdx.x);
+    int n = 0, from = 0;
+    b = -1;
+    for (int s0 = 0; s0 < p.kv.B && b < 0; s0 += 32) {
+      int c0 = 0, c1 = 0;
+      if (s0 + lane < p.kv.B) {
+        c0 = __ldg(p.cu_q + s0 + lane);
+        c1 = __ldg(p.cu_q + s0 + lane + 1);
+        if (c0 < 0 || c1 < c0 || c1 > p.T) {
+          if (warp == 0) raise_dev_error(p.kv.err, DEVERR_BOUNDS);
+          c0 = c1 = 0;
+        }
+      }
+      const uint32_t hit = __ballot_sync(0xffffffffu, token >= c0 && token < c1);
+      if (hit) {
+        const int src = __ffs(hit) - 1;
+        b = s0 + src;
+        from = __shfl_sync(0xffffffffu, c0, src);
+        n = __shfl_sync(0xffffffffu, c1, src) - from;
+      }
+    }
+    if (b < 0) return;                                 // a row of no sequence
+    pos = length_of(p.kv, b, threadIdx.x == 0) - n + (token - from);
+  } else {
+    pos = length_of(p.kv, b, threadIdx.x == 0) - 1;
+  }
+  const AlignedTiles at(pos, p.window, p.sinks);
   const int per = p.chunk / KT;
   const int first = chunk * per;
   if (chunk > 0 && first >= at.tiles) return;
@@ -144,7 +176,7 @@ __global__ void __launch_bounds__(Lay<D, NH>::THREADS, 1)
       const int r = i / (D / 8), c = i % (D / 8);
       uint4 v = make_uint4(0, 0, 0, 0);
       if (r < rows) {
-        v = __ldg(reinterpret_cast<const uint4*>(p.q + b * p.q_token + (kvh * p.G + h0 + r) * p.q_head) + c);
+        v = __ldg(reinterpret_cast<const uint4*>(p.q + token * p.q_token + (kvh * p.G + h0 + r) * p.q_head) + c);
         v.x ^= p.flip;
         v.y ^= p.flip;
         v.z ^= p.flip;
@@ -433,7 +465,7 @@ __global__ void __launch_bounds__(Lay<D, NH>::THREADS, 1)
       shift[h] = tiles > 0 ? (s0 + s1) + (s2 + s3) : 0.0f;             // l
     }
     bar_of<N>();
-    const int64_t row0 = static_cast<int64_t>(b) * p.Hq + kvh * p.G + h0;
+    const int64_t row0 = static_cast<int64_t>(token) * p.Hq + kvh * p.G + h0;
     const bool partial = p.chunks > 1 && at.tiles > per;
 #pragma unroll 1
     for (int i = 0; i < D / 128 * (HW / 16) && ok; ++i) {
@@ -510,16 +542,26 @@ bool paged_wide_applies(const PagedAttn& a) {
   return a.fmt != CSA2_KV_FP4 && a.kv.page_shift >= 3 && a.kv.n_pages > 0 && a.D == 512;
 }
 
-csa2_status launch_paged_wide(const PagedAttn& a, int chunk, int chunks, float* part_o, float2* part_ml,
-                              cudaStream_t stream) {
-  Params p = {};
+// A CTA per token pays when its heads fill most of the 64 and it sees several tiles;
+// else the 16-row tiles of paged_attn.cu, which take several tokens at once, are
+// faster.  Measured (us, here / there): 512 tokens behind 1000, 64 heads over one
+// 512-wide row, window 2048: 142 / 237; 1000 tokens, 64 heads over one 256-wide row:
+// 175 / 414; 512 behind 1000, 16 heads over one 512-wide row: 91 / 75; 60 tokens, 64
+// heads, window 128: 39 / 26.
+bool paged_wide_prompt_applies(const PagedAttn& a) {
+  const int64_t seen = a.window > 0 ? std::min<int64_t>(a.kv.capacity, static_cast<int64_t>(a.window) + a.sinks) : a.kv.capacity;
+  return a.fmt != CSA2_KV_FP4 && a.kv.page_shift >= 3 && a.kv.n_pages > 0 && (a.D == 512 || a.D == 256) && a.G >= 32 &&
+         seen >= 512;
+}
+
+namespace {
+
+csa2_status launch(const PagedAttn& a, Params& p, dim3 grid, cudaStream_t stream) {
   p.q = static_cast<const uint16_t*>(a.q);
   p.q_token = a.q_token;
   p.q_head = a.q_head;
   p.out = static_cast<uint16_t*>(a.out);
   p.lse = a.lse;
-  p.part_o = part_o;
-  p.part_ml = part_ml;
   const float s = a.scale * kLog2e;
   p.flip = s < 0.0f ? 0x80008000u : 0u;
   p.scale2 = std::max(s < 0.0f ? -s : s, 1.1754944e-38f);
@@ -529,8 +571,6 @@ csa2_status launch_paged_wide(const PagedAttn& a, int chunk, int chunks, float* 
   p.row_tiles = (a.G + nh - 1) / nh;
   p.window = a.window;
   p.sinks = a.sinks;
-  p.chunk = chunk;
-  p.chunks = chunks;
   p.kv = a.kv;
   const bool sh = a.kv.v == a.kv.k;
   const int page = 1 << a.kv.page_shift;
@@ -539,13 +579,35 @@ csa2_status launch_paged_wide(const PagedAttn& a, int chunk, int chunks, float* 
   for (int i = 0; i < (sh ? 1 : 2); ++i)
     CSA2_TRY(make_tensor_map_paged(&maps[i], i ? a.kv.v : a.kv.k, a.D, a.kv.heads, a.kv.head_stride, page,
                                    a.kv.token_stride, a.kv.n_pages, a.kv.page_stride, p.box));
-  const dim3 grid(static_cast<unsigned>(chunks), static_cast<unsigned>(a.kv.heads * p.row_tiles),
-                  static_cast<unsigned>(a.kv.B));
-#define CSA2_WIDE_N(T_, N_) (sh ? run<T_, 512, N_, true>(p, grid, maps, stream) : run<T_, 512, N_, false>(p, grid, maps, stream))
-#define CSA2_WIDE(T_) (nh == 16 ? CSA2_WIDE_N(T_, 16) : CSA2_WIDE_N(T_, 64))
+  grid.y = static_cast<unsigned>(a.kv.heads * p.row_tiles);
+#define CSA2_WIDE_N(T_, D_, N_) (sh ? run<T_, D_, N_, true>(p, grid, maps, stream) : run<T_, D_, N_, false>(p, grid, maps, stream))
+#define CSA2_WIDE_D(T_, D_) (nh == 16 ? CSA2_WIDE_N(T_, D_, 16) : CSA2_WIDE_N(T_, D_, 64))
+#define CSA2_WIDE(T_) (a.D == 256 ? CSA2_WIDE_D(T_, 256) : CSA2_WIDE_D(T_, 512))
   return a.fmt == CSA2_KV_F16 ? CSA2_WIDE(__half) : CSA2_WIDE(__nv_bfloat16);
 #undef CSA2_WIDE
+#undef CSA2_WIDE_D
 #undef CSA2_WIDE_N
+}
+
+}  // namespace
+
+csa2_status launch_paged_wide(const PagedAttn& a, int chunk, int chunks, float* part_o, float2* part_ml,
+                              cudaStream_t stream) {
+  Params p = {};
+  p.part_o = part_o;
+  p.part_ml = part_ml;
+  p.chunk = chunk;
+  p.chunks = chunks;
+  return launch(a, p, dim3(static_cast<unsigned>(chunks), 1, static_cast<unsigned>(a.kv.B)), stream);
+}
+
+csa2_status launch_paged_wide_prompt(const PagedAttn& a, const int32_t* cu_q, int64_t T, cudaStream_t stream) {
+  Params p = {};
+  p.cu_q = cu_q;
+  p.T = static_cast<int>(T);
+  p.chunk = KT;
+  p.chunks = 1;
+  return launch(a, p, dim3(static_cast<unsigned>(T)), stream);
 }
 
 }  // namespace csa2

@@ -328,6 +328,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_window_kernel(const Params 
         };
         int page = page_of(0);
         uint32_t fixes = 0;                            // tiles with rows to zero so far
+        int issued = 0;                                // tiles whose boxes complete on their own barrier
         for (int tile = 0; tile < (group == 0 ? wk.tiles : 0) && ok; ++tile) {
           const int next = page_of(tile + 1);
           const int st = tile % ring, t0 = wk.tile_start(tile), a = t0 + br;
@@ -362,6 +363,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_window_kernel(const Params 
             tma_load_page(dst + (lane % BLKS) * L::BLK + br * 128, half ? &v_map : &k_map, bar_at, (lane % BLKS) * 64, kvh,
                           a & ((1 << p.kv.page_shift) - 1), page);
           __syncwarp();
+          if (!rows) issued = tile + 1;
           if (rows) {
             ok = wait(fix_bar, fixes & 1);
             ++fixes;
@@ -379,6 +381,11 @@ __global__ void __launch_bounds__(kThreads, 1) paged_window_kernel(const Params 
             if (lane == 0) mbar_arrive(fulls + st);
           }
           page = next;
+        }
+        if (!ok) {
+          // copies in flight land before the block's shared memory goes
+          volatile int never = 0;
+          for (int t = max(0, issued - ring); t < issued; ++t) wait_phase(fulls + t % ring, (t / ring) & 1, &never, p.kv.err);
         }
       } else {
         // block u % 4 of tile u / 4, three warps in turn

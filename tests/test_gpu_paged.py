@@ -275,7 +275,8 @@ def test_window(kind, D, page, heads, G, shared, layout, window, sinks):
                   sinks, 61, tail=3)
 
 
-@pytest.mark.parametrize("kind,D,heads,G,window,sinks", [("bf16", 128, 2, 8, 128, 4), ("f16", 64, 1, 4, 0, 0),
+@pytest.mark.parametrize("kind,D,heads,G,window,sinks", [("bf16", 512, 1, 64, 0, 0), ("f16", 256, 2, 40, 600, 9),
+                                                         ("bf16", 128, 2, 8, 128, 4), ("f16", 64, 1, 4, 0, 0),
                                                          ("bf16", 128, 1, 1, 300, 130)])
 def test_window_longer(kind, D, heads, G, window, sinks):
     _window_check(kind, [700, 3, 411], [700, 900, 1000], 64, heads, G, D, False, "dense", window, sinks, 71)
@@ -292,7 +293,7 @@ def test_window_rows_before_the_start_see_nothing():
     P.check_attn(out[4:], lse[4:], want, P.f64(q[4:]), host[0][0], 0.125, torch.bfloat16, 5)
 
 
-@pytest.mark.parametrize("kind,D,G,window", [("bf16", 128, 8, 0), ("f16", 64, 3, 90), ("bf16", 512, 16, 50)])
+@pytest.mark.parametrize("kind,D,G,window", [("bf16", 512, 64, 0), ("bf16", 128, 8, 0), ("f16", 64, 3, 90), ("bf16", 512, 16, 50)])
 def test_window_bits_do_not_depend_on_batch_or_cut(kind, D, G, window):
     cache, q, cu, scale, out, lse = _window_check(kind, [203, 340], [203, 400], 16, 1, G, D, True, "dense", window, 3, 81)
     # the second sequence alone, its last 77 tokens as a chunk of their own
