@@ -11,13 +11,14 @@
 // with warp-level products: at 16 rows the arithmetic is 16 multiply-adds per
 // byte, far below what they deliver.
 //
-// FP4 rows stay packed in shared memory; a thread's fragment is made of whole
-// code words (8 channels of a token), which are turned to bf16 in registers: the
-// channels of a dot product may come in any order as long as q's come in the same
-// one, and the output's channel order falls out as 16 neighbours per thread.  A
-// code's magnitude bits placed at a bf16's exponent border read as value * 2^-126;
-// one exact product with scale * 2^63 gives the value * 2^-63, and the missing
-// 2^63 goes into the score scale (keys) and the final division (values).
+// FP4 rows stay packed in shared memory; a thread's fragment is made of whole code
+// words (8 channels of a token), which become f16 pairs in registers by the hardware's
+// E2M1 conversion and one product with the scale: a code times a scale has five
+// significant bits between 2^-10 and 2^12, exact in f16.  (Integer steps to bf16 cost
+// 26 instructions a word against 19.)  The channels of a dot product may come in any
+// order as long as q's come in the same one.  q's rows are brought to f16 by a power
+// of two that puts their largest value into [1, 2); what a smaller value loses below
+// 2^-25 of it is less than the f32 sum's own rounding.
 #include <algorithm>
 
 #include "launchers.h"
@@ -56,22 +57,23 @@ __device__ __forceinline__ uint32_t lds32(uint32_t a) {
   asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(a));
   return v;
 }
-__device__ __forceinline__ uint32_t lds8(uint32_t a) {
+__device__ __forceinline__ uint32_t lds16(uint32_t a) {
   uint32_t v;
-  asm volatile("{.reg .u16 t; ld.shared.u8 t, [%1]; cvt.u32.u16 %0, t;}" : "=r"(v) : "r"(a));
+  asm volatile("{.reg .u16 t; ld.shared.u16 t, [%1]; cvt.u32.u16 %0, t;}" : "=r"(v) : "r"(a));
   return v;
 }
-
-// E4M3 scale code -> bf16 pair of scale * 2^63: its bits at a bf16's exponent
-// border read as scale * 2^-120 (subnormals included); two exact products.
-__device__ __forceinline__ uint32_t scale_2p63(uint32_t code) {
-  const uint32_t b = code << 4;
-  return mul_bf16x2(mul_bf16x2(b | (b << 16), 0x7b807b80u /* 2^120 */), 0x5f005f00u /* 2^63 */);
+// The scale of a 16-channel block, `odd` of two neighbouring ones, as an f16 pair.
+__device__ __forceinline__ uint32_t scale_f16(uint32_t two, bool odd) {
+  const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(two), __NV_E4M3);
+  const uint32_t v = static_cast<uint32_t>(h.x) | (static_cast<uint32_t>(h.y) << 16);
+  return __byte_perm(v, v, odd ? 0x3232 : 0x1010);
 }
-// Codes k and k + 4 of a word (channels k, k + 4 of its eight) as a bf16 pair, times s2.
+// Byte k of a word (channels 2 k and 2 k + 1) as an f16 pair, times a scale.
 __device__ __forceinline__ uint32_t code_pair(uint32_t w, int k, uint32_t s2) {
-  const uint32_t x = w >> (4 * k);
-  return mul_bf16x2(((x & 0x00070007u) << 6) | ((x & 0x00080008u) << 12), s2);
+  uint32_t d;
+  asm("{.reg .b8 b, x, y, z; mov.b32 {b, x, y, z}, %1; cvt.rn.f16x2.e2m1x2 %0, b;}" : "=r"(d) : "r"(w >> (8 * k)));
+  const __half2 r = __hmul2(*reinterpret_cast<__half2*>(&d), *reinterpret_cast<__half2*>(&s2));
+  return *reinterpret_cast<const uint32_t*>(&r);
 }
 
 struct Params {
@@ -89,6 +91,7 @@ struct Params {
 template <class T, int D, bool FP4, bool SHARED>
 __global__ void __launch_bounds__(kThreads) paged_decode_kernel(const Params p) {
   using L = Lay<D, FP4>;
+  using M = typename std::conditional<FP4, __half, T>::type;       // type of the products
   constexpr int KS = L::KS;
   extern __shared__ __align__(16) uint8_t smem[];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -147,8 +150,9 @@ __global__ void __launch_bounds__(kThreads) paged_decode_kernel(const Params p) 
   };
 
   // q fragments.  16-bit rows: the plain order.  FP4: the order of the code words:
-  // thread c4 of a group of 32 channels owns channels 8 c4 .. 8 c4 + 7 as pairs
-  // (0,4) (1,5) of the first step and (2,6) (3,7) of the second.
+  // thread c4 of a group of 32 channels owns channels 8 c4 .. 8 c4 + 7 as the pairs
+  // (0,1) (2,3) of the first step and (4,5) (6,7) of the second.
+  float scale2[2] = {p.scale2, p.scale2};              // per row of the fragment
   uint32_t qa[D / 16][4];
   {
     const uint16_t* q0 = p.q + b * p.q_token + (kvh * p.G + h0 + min(n8, rows - 1)) * p.q_head;
@@ -168,15 +172,37 @@ __global__ void __launch_bounds__(kThreads) paged_decode_kernel(const Params p) 
         uint4 a = make_uint4(0, 0, 0, 0), e = a;
         if (ok0) a = __ldg(reinterpret_cast<const uint4*>(q0 + g * 32) + c4);
         if (ok1) e = __ldg(reinterpret_cast<const uint4*>(q1 + g * 32) + c4);
-        // words hold channels (0,1) (2,3) (4,5) (6,7); wanted (0,4) (1,5) (2,6) (3,7)
-        qa[2 * g][0] = __byte_perm(a.x, a.z, 0x5410);
-        qa[2 * g][2] = __byte_perm(a.x, a.z, 0x7632);
-        qa[2 * g + 1][0] = __byte_perm(a.y, a.w, 0x5410);
-        qa[2 * g + 1][2] = __byte_perm(a.y, a.w, 0x7632);
-        qa[2 * g][1] = __byte_perm(e.x, e.z, 0x5410);
-        qa[2 * g][3] = __byte_perm(e.x, e.z, 0x7632);
-        qa[2 * g + 1][1] = __byte_perm(e.y, e.w, 0x5410);
-        qa[2 * g + 1][3] = __byte_perm(e.y, e.w, 0x7632);
+        qa[2 * g][0] = a.x;
+        qa[2 * g][2] = a.y;
+        qa[2 * g + 1][0] = a.z;
+        qa[2 * g + 1][2] = a.w;
+        qa[2 * g][1] = e.x;
+        qa[2 * g][3] = e.y;
+        qa[2 * g + 1][1] = e.z;
+        qa[2 * g + 1][3] = e.w;
+      }
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        uint32_t top = 0;                              // largest |bf16| of the row, as bits
+#pragma unroll
+        for (int k = 0; k < D / 16; ++k)
+#pragma unroll
+          for (int x = 0; x < 2; ++x) {
+            const uint32_t v = qa[k][u + 2 * x] & 0x7fff7fffu;
+            top = max(top, max(v & 0xffffu, v >> 16));
+          }
+        top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+        top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
+        const uint32_t eb = min(max(top >> 7, 1u), 253u);            // its biased exponent
+        const float down = __uint_as_float((254u - eb) << 23);
+        scale2[u] *= __uint_as_float(eb << 23);
+#pragma unroll
+        for (int k = 0; k < D / 16; ++k)
+#pragma unroll
+          for (int x = 0; x < 2; ++x) {
+            const float2 f = Num<__nv_bfloat16>::up(qa[k][u + 2 * x]);
+            qa[k][u + 2 * x] = Num<__half>::down(f.x * down, f.y * down);
+          }
       }
     }
   }
@@ -185,7 +211,6 @@ __global__ void __launch_bounds__(kThreads) paged_decode_kernel(const Params p) 
 #pragma unroll
   for (int i = 0; i < D / 8; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.0f;
   float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.0f, 0.0f};
-  const float scale2 = FP4 ? p.scale2 * 0x1p63f : p.scale2;
 
   // the ring: STAGES - 1 slices of this warp ahead
   uint32_t present[L::STAGES];
@@ -224,8 +249,8 @@ __global__ void __launch_bounds__(kThreads) paged_decode_kernel(const Params p) 
         for (int i = 0; i < NT; ++i) {                 // 8 tokens x 32 channels
           uint32_t bb[4];
           ldsm4(bb, kb + (i * 8 + (lane & 7)) * L::ROW + k * 32 + (lane >> 3) * 16);
-          mma16816<T>(sc[i], qa[k], bb[0], bb[1]);
-          mma16816<T>(sc[i], qa[k + 1], bb[2], bb[3]);
+          mma16816<M>(sc[i], qa[k], bb[0], bb[1]);
+          mma16816<M>(sc[i], qa[k + 1], bb[2], bb[3]);
         }
       }
     } else {
@@ -235,9 +260,9 @@ __global__ void __launch_bounds__(kThreads) paged_decode_kernel(const Params p) 
         for (int i = 0; i < NT; ++i) {
           const int r = i * 8 + n8;
           const uint32_t w = lds32(kb + r * L::ROW + (4 * g + c4) * 4);
-          const uint32_t s2 = scale_2p63(lds8(kb + KS * L::ROW + r * (D / 16) + 2 * g + (c4 >> 1)));
-          mma16816<T>(sc[i], qa[2 * g], code_pair(w, 0, s2), code_pair(w, 1, s2));
-          mma16816<T>(sc[i], qa[2 * g + 1], code_pair(w, 2, s2), code_pair(w, 3, s2));
+          const uint32_t s2 = scale_f16(lds16(kb + KS * L::ROW + r * (D / 16) + 2 * g), c4 >> 1);
+          mma16816<M>(sc[i], qa[2 * g], code_pair(w, 0, s2), code_pair(w, 1, s2));
+          mma16816<M>(sc[i], qa[2 * g + 1], code_pair(w, 2, s2), code_pair(w, 3, s2));
         }
       }
     }
@@ -247,7 +272,7 @@ __global__ void __launch_bounds__(kThreads) paged_decode_kernel(const Params p) 
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
         const bool ok = (mask >> (i * 8 + c4 * 2 + (e & 1))) & 1u;
-        sc[i][e] = ok ? sc[i][e] * scale2 : -INFINITY;
+        sc[i][e] = ok ? sc[i][e] * scale2[e >> 1] : -INFINITY;
         mx[e >> 1] = fmaxf(mx[e >> 1], sc[i][e]);
       }
     float alpha[2];
@@ -271,10 +296,10 @@ __global__ void __launch_bounds__(kThreads) paged_decode_kernel(const Params p) 
     uint32_t pa[KS / 16][4];                           // P as the next product's left operand
 #pragma unroll
     for (int t = 0; t < KS / 16; ++t) {
-      pa[t][0] = Num<T>::down(sc[2 * t][0], sc[2 * t][1]);
-      pa[t][1] = Num<T>::down(sc[2 * t][2], sc[2 * t][3]);
-      pa[t][2] = Num<T>::down(sc[2 * t + 1][0], sc[2 * t + 1][1]);
-      pa[t][3] = Num<T>::down(sc[2 * t + 1][2], sc[2 * t + 1][3]);
+      pa[t][0] = Num<M>::down(sc[2 * t][0], sc[2 * t][1]);
+      pa[t][1] = Num<M>::down(sc[2 * t][2], sc[2 * t][3]);
+      pa[t][2] = Num<M>::down(sc[2 * t + 1][0], sc[2 * t + 1][1]);
+      pa[t][3] = Num<M>::down(sc[2 * t + 1][2], sc[2 * t + 1][3]);
     }
     if (__any_sync(0xffffffffu, alpha[0] != 1.0f || alpha[1] != 1.0f)) {
 #pragma unroll
@@ -292,8 +317,8 @@ __global__ void __launch_bounds__(kThreads) paged_decode_kernel(const Params p) 
         for (int i = 0; i < D / 16; ++i) {             // 16 tokens x 16 channels
           uint32_t bb[4];
           ldsm4t(bb, vb + (t * 16 + (lane & 15)) * L::ROW + (i * 16 + (lane >> 4) * 8) * 2);
-          mma16816<T>(o[2 * i], pa[t], bb[0], bb[1]);
-          mma16816<T>(o[2 * i + 1], pa[t], bb[2], bb[3]);
+          mma16816<M>(o[2 * i], pa[t], bb[0], bb[1]);
+          mma16816<M>(o[2 * i + 1], pa[t], bb[2], bb[3]);
         }
       } else {
         // word n8 of a group of 64 channels, of tokens 2 c4, 2 c4 + 1, 2 c4 + 8, 2 c4 + 9
@@ -304,14 +329,14 @@ __global__ void __launch_bounds__(kThreads) paged_decode_kernel(const Params p) 
           for (int u = 0; u < 4; ++u) {
             const int r = t * 16 + 2 * c4 + (u & 1) + 8 * (u >> 1);
             w[u] = lds32(vb + r * L::ROW + (8 * g + n8) * 4);
-            s2[u] = scale_2p63(lds8(vb + KS * L::ROW + r * (D / 16) + 4 * g + (n8 >> 1)));
+            s2[u] = scale_f16(lds16(vb + KS * L::ROW + r * (D / 16) + 4 * g + 2 * (n8 >> 2)), (n8 >> 1) & 1);
           }
 #pragma unroll
-          for (int k = 0; k < 4; ++k) {                // channels k and k + 4 of the word
+          for (int k = 0; k < 4; ++k) {                // channels 2 k and 2 k + 1 of the word
             const uint32_t x0 = code_pair(w[0], k, s2[0]), x1 = code_pair(w[1], k, s2[1]);
             const uint32_t y0 = code_pair(w[2], k, s2[2]), y1 = code_pair(w[3], k, s2[3]);
-            mma16816<T>(o[8 * g + k], pa[t], __byte_perm(x0, x1, 0x5410), __byte_perm(y0, y1, 0x5410));
-            mma16816<T>(o[8 * g + k + 4], pa[t], __byte_perm(x0, x1, 0x7632), __byte_perm(y0, y1, 0x7632));
+            mma16816<M>(o[8 * g + 2 * k], pa[t], __byte_perm(x0, x1, 0x5410), __byte_perm(y0, y1, 0x5410));
+            mma16816<M>(o[8 * g + 2 * k + 1], pa[t], __byte_perm(x0, x1, 0x7632), __byte_perm(y0, y1, 0x7632));
           }
         }
       }
@@ -368,12 +393,6 @@ __global__ void __launch_bounds__(kThreads) paged_decode_kernel(const Params p) 
       acc.y += f * v.y;
       acc.z += f * v.z;
       acc.w += f * v.w;
-    }
-    if (FP4) {
-      acc.x *= 0x1p63f;
-      acc.y *= 0x1p63f;
-      acc.z *= 0x1p63f;
-      acc.w *= 0x1p63f;
     }
     const int64_t at = static_cast<int64_t>(b) * p.Hq + kvh * p.G + h0 + r;
     if (partial) {

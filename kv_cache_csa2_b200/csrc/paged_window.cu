@@ -287,13 +287,13 @@ __global__ void __launch_bounds__(kThreads, 1) paged_window_kernel(const Params 
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
   constexpr uint32_t O_COL = 256;                      // S / P of tile w at 128 w, O at 256 + 128 w
-  // registers: 128 x 512 threads at launch = 176 x 256 (softmax) + 80 x 256 (the
+  // registers: 128 x 512 threads at launch = 184 x 256 (softmax) + 72 x 256 (the
   // rest); the warps that dequantise FP4 rows need more
   if (warp >= 8) {
     if (FP4)
       asm volatile("setmaxnreg.dec.sync.aligned.u32 112;");
     else
-      asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
+      asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
     if (warp > 9) {
       // ------------------------------------------------------------ loaders
       const int half = (warp - 10) & 1, group = (warp - 10) >> 1;       // keys or values; which of three
@@ -552,7 +552,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_window_kernel(const Params 
     if (FP4)
       asm volatile("setmaxnreg.inc.sync.aligned.u32 144;");
     else
-      asm volatile("setmaxnreg.inc.sync.aligned.u32 176;");
+      asm volatile("setmaxnreg.inc.sync.aligned.u32 184;");
     const int w = warp >> 2, quad = warp & 3;
     const int r = quad * 32 + lane;                    // row of the tile = TMEM lane
     const uint32_t lane_off = static_cast<uint32_t>(quad * 32) << 16;
