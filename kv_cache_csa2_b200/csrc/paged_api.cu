@@ -41,7 +41,7 @@ csa2_status rope_of(const char* fn, const csa2_rope* r, int D, rope::RopeArgs* o
   *out = rope::RopeArgs{nullptr, 0, 0, 0, 0};
   if (!r) return CSA2_OK;
   REQUIRE(r->half > 0 && r->half % 8 == 0 && r->half <= rope::kMaxHalf && r->offset >= 0 && r->offset % 8 == 0 &&
-              r->offset + 2 * r->half <= D,
+              r->offset <= D - 2 * r->half,
           "%s: rotation of channels [%d, %d + 2*%d) of %d: half and offset must be multiples of 8 inside the row", fn,
           r->offset, r->offset, r->half, D);
   REQUIRE(r->inv_freq != nullptr, "%s: rotation without inv_freq", fn);

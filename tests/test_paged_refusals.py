@@ -43,6 +43,13 @@ def test_norm_rope_refusals():
     assert norm(T=0, q=heads(data=0), q_out=heads(data=0)) == 0      # no rows: nothing to do
 
 
+def test_rotation_far_outside_the_row():
+    """offset + 2 * half past 32 bits is still outside the row."""
+    far = 0x7fffffc0
+    assert norm(r=rope(half=32, offset=far)) == 1
+    assert append(r=rope(half=32, offset=far)) == 1
+
+
 def append(dtype=0, k=None, v=None, seq=P, pos=P, T=4, r=None, shared=False, **cache):
     if shared:
         cache["v"] = None
