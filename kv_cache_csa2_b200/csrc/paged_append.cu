@@ -5,6 +5,10 @@
 // and page addresses computed once for all heads, then the (token, head) rows.
 // An FP4 block of 16 channels is the same vector of two neighbouring lanes, so
 // its absolute maximum is one shuffle and each lane packs its own 8 codes.
+// Measured: 8191 tokens of 8 heads x 128 (keys and values), 15.4 us (4.4 TB/s), about one
+// wave, so the place and angles of a CTA's tokens stand at its start in full; 4096
+// shared rows x 512 into FP4, 8.6 us, of which the rounding to FP4 (150 instructions
+// per 16 channels) is the larger part.
 #include <algorithm>
 
 #include "common.cuh"

@@ -10,6 +10,11 @@
 //
 // A decode query's tokens are cut into chunks on several CTAs; chunks > 1 write
 // (O, m, l) partials that paged_combine_kernel joins in chunk order.
+//
+// Takes what the kernels of paged_decode.cu, paged_wide.cu and paged_window.cu do not:
+// latency-bound, as two block barriers per tile stand between the products.  Measured
+// (512 tokens behind 1000, 64 heads over one 512-wide row): 237 us, against 142 on
+// the tensor cores in paged_wide.cu.
 #include <algorithm>
 
 #include "launchers.h"

@@ -10,6 +10,8 @@
 //   S[16 heads, 16 tokens] = q k^T, P = 2^(S - m), O[16 heads, D] += P v
 // with warp-level products: at 16 rows the arithmetic is 16 multiply-adds per
 // byte, far below what they deliver.
+// Measured: 64 ragged sequences of up to 16384 tokens, 64 heads over 8 x 128, 233 us
+// (6.05 TB/s, 0.92 of a plain copy's rate); one sequence of 8192 with its join, 9.0 us.
 //
 // FP4 rows stay packed in shared memory; a thread's fragment is made of whole code
 // words (8 channels of a token), which become f16 pairs in registers by the hardware's
@@ -17,8 +19,11 @@
 // significant bits between 2^-10 and 2^12, exact in f16.  (Integer steps to bf16 cost
 // 26 instructions a word against 19.)  The channels of a dot product may come in any
 // order as long as q's come in the same one.  q's rows are brought to f16 by a power
-// of two that puts their largest value into [1, 2); what a smaller value loses below
-// 2^-25 of it is less than the f32 sum's own rounding.
+// of two that puts their largest value into [1, 2): values down to 2^-14 keep their
+// eight bits, a smaller one moves by at most 2^-25, a quarter step of an f32 at the
+// largest.  Measured: 64 ragged sequences of up to 32768, window 8192 + 4, 32 heads
+// over 4 x 128, 108 us (slices of 16 tokens 122; four CTAs per SM spill, 141).  Bound by
+// the instructions of the decoding, not by the 209 MB (32 us).
 #include <algorithm>
 
 #include "launchers.h"

@@ -31,7 +31,9 @@
 //
 // Bound: 4 D flops per (row, key) on the tensor cores against one exponential,
 // 16 of which an SM does per clock: at D = 128 both take 1024 clocks per pair of
-// 128 x 128 tiles.
+// 128 x 128 tiles.  Measured: 8192 tokens, window 2048 + 4, 32 heads over 4 x 128, 267 us
+// (0.77 Pflop/s); the softmax's latency per 64 keys (1900 clocks against 1280 of
+// products) is what is left, and TMEM has no room for a third row tile.
 #include <algorithm>
 #include <type_traits>
 
