@@ -37,15 +37,16 @@ using rope::Num;
 constexpr int kWarps = 4;
 constexpr int kThreads = kWarps * 32;
 
-template <int D, bool FP4>
+template <int D, bool FP4, int HT>
 struct Lay {
+  static constexpr int ROWS = 8 * HT;                              // query rows of a CTA
   static constexpr int KS = FP4 && D <= 128 ? 32 : 16;             // tokens per slice
   static constexpr int ROW = FP4 ? D / 2 + 16 : 2 * D + 16;        // padded row in shared memory
   static constexpr int SC = FP4 ? KS * (D / 16) : 0;               // a slice's scales
   static constexpr int HALF = KS * ROW + SC;                       // keys (or values) of a slice
-  static constexpr int STAGES = FP4 ? (D <= 128 ? 3 : 6) : D == 64 ? 6 : D == 128 ? 3 : 2;
+  static constexpr int STAGES = FP4 ? (D <= 128 ? (HT == 1 ? 2 : 3) : 6) : D == 64 ? 6 : D == 128 ? 3 : 2;
   static constexpr int warp_bytes(bool shared) { return STAGES * HALF * (shared ? 1 : 2); }
-  static constexpr int MERGE = kWarps * 16 * (D + 4) * 4 + kWarps * 16 * 8;
+  static constexpr int MERGE = kWarps * ROWS * (D + 4) * 4 + kWarps * ROWS * 8;
   static constexpr int bytes(bool shared) {
     return kWarps * warp_bytes(shared) > MERGE ? kWarps * warp_bytes(shared) : MERGE;
   }
@@ -57,23 +58,41 @@ __device__ __forceinline__ void cp_async_4(uint32_t dst, const void* src, uint32
 __device__ __forceinline__ void cp_async_16s(uint32_t dst, const void* src, uint32_t n) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
 }
-__device__ __forceinline__ uint32_t lds32(uint32_t a) {
+// N words, or the N bytes of a word, from shared memory.
+template <int N>
+__device__ __forceinline__ void lds_words(uint32_t (&w)[N], uint32_t a) {
+  if constexpr (N == 1) {
+    asm volatile("ld.shared.u32 %0, [%1];" : "=r"(w[0]) : "r"(a));
+  } else if constexpr (N == 2) {
+    asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(w[0]), "=r"(w[1]) : "r"(a));
+  } else {
+#pragma unroll
+    for (int i = 0; i < N; i += 4)
+      asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                   : "=r"(w[i]), "=r"(w[i + 1]), "=r"(w[i + 2]), "=r"(w[i + 3])
+                   : "r"(a + 4 * i));
+  }
+}
+template <int N>
+__device__ __forceinline__ uint32_t lds_bytes(uint32_t a) {
   uint32_t v;
-  asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(a));
+  if constexpr (N == 1) asm volatile("ld.shared.u8 %0, [%1];" : "=r"(v) : "r"(a));
+  if constexpr (N == 2) asm volatile("ld.shared.u16 %0, [%1];" : "=r"(v) : "r"(a));
+  if constexpr (N == 4) asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(a));
   return v;
 }
-__device__ __forceinline__ uint32_t lds16(uint32_t a) {
-  uint32_t v;
-  asm volatile("{.reg .u16 t; ld.shared.u16 t, [%1]; cvt.u32.u16 %0, t;}" : "=r"(v) : "r"(a));
-  return v;
-}
-// The scale of a 16-channel block, `odd` of two neighbouring ones, as an f16 pair.
-__device__ __forceinline__ uint32_t scale_f16(uint32_t two, bool odd) {
+// Two E4M3 scales (the low bytes) as an f16 pair.
+__device__ __forceinline__ uint32_t scales_f16(uint32_t two) {
   const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(two), __NV_E4M3);
-  const uint32_t v = static_cast<uint32_t>(h.x) | (static_cast<uint32_t>(h.y) << 16);
-  return __byte_perm(v, v, odd ? 0x3232 : 0x1010);
+  return static_cast<uint32_t>(h.x) | (static_cast<uint32_t>(h.y) << 16);
 }
-// Byte k of a word (channels 2 k and 2 k + 1) as an f16 pair, times a scale.
+// The transpose of an 8 x 8 matrix of 16-bit values, one register a lane.
+__device__ __forceinline__ uint32_t transpose8(uint32_t a) {
+  uint32_t d;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(d) : "r"(a));
+  return d;
+}
+// The two codes of byte k of a word as an f16 pair, times a pair of scales.
 __device__ __forceinline__ uint32_t code_pair(uint32_t w, int k, uint32_t s2) {
   uint32_t d;
   asm("{.reg .b8 b, x, y, z; mov.b32 {b, x, y, z}, %1; cvt.rn.f16x2.e2m1x2 %0, b;}" : "=r"(d) : "r"(w >> (8 * k)));
@@ -93,17 +112,17 @@ struct Params {
   PagedView kv;
 };
 
-template <class T, int D, bool FP4, bool SHARED>
-__global__ void __launch_bounds__(kThreads) paged_decode_kernel(const Params p) {
-  using L = Lay<D, FP4>;
+template <class T, int D, bool FP4, bool SHARED, int HT>
+__global__ void __launch_bounds__(kThreads, FP4 && D <= 128 && HT == 1 ? 4 : 1) paged_decode_kernel(const Params p) {
+  using L = Lay<D, FP4, HT>;
   using M = typename std::conditional<FP4, __half, T>::type;       // type of the products
   constexpr int KS = L::KS;
   extern __shared__ __align__(16) uint8_t smem[];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int n8 = lane >> 2, c4 = lane & 3;             // fragment coordinates
   const int b = blockIdx.z, chunk = blockIdx.x;
-  const int kvh = blockIdx.y / p.row_tiles, h0 = 16 * (blockIdx.y % p.row_tiles);
-  const int rows = min(16, p.G - h0);
+  const int kvh = blockIdx.y / p.row_tiles, h0 = L::ROWS * (blockIdx.y % p.row_tiles);
+  const int rows = min(L::ROWS, p.G - h0);
   pdl_wait();
   const int len = length_of(p.kv, b, threadIdx.x == 0);
   const Seen seen(len - 1, len - 1, p.window, p.sinks);
@@ -154,68 +173,76 @@ __global__ void __launch_bounds__(kThreads) paged_decode_kernel(const Params p) 
     return __ballot_sync(0xffffffffu, row >= 0);
   };
 
-  // q fragments.  16-bit rows: the plain order.  FP4: the order of the code words:
-  // thread c4 of a group of 32 channels owns channels 8 c4 .. 8 c4 + 7 as the pairs
-  // (0,1) (2,3) of the first step and (4,5) (6,7) of the second.
-  float scale2[2] = {p.scale2, p.scale2};              // per row of the fragment
+  // 16-bit rows: q is the left operand, rows n8 and n8 + 8 of it this thread's.
+  // FP4: the right one, columns 8 h + n8; thread c4 of a row owns the D / 4 channels
+  // from c4 * D / 4 on, a code word per two steps: its pairs (0,1) (2,3) and (4,5) (6,7).
+  constexpr int NW = D / 32;                           // code words of a thread in a key row
+  constexpr int W = D / 64;                            // and in a value row
   uint32_t qa[D / 16][4];
-  {
+  uint32_t qb[HT][2 * NW][2];
+  float scale2[HT][2];                                 // per row / column of the scores
+#pragma unroll
+  for (int h = 0; h < HT; ++h) scale2[h][0] = scale2[h][1] = p.scale2;
+  if constexpr (!FP4) {
     const uint16_t* q0 = p.q + b * p.q_token + (kvh * p.G + h0 + min(n8, rows - 1)) * p.q_head;
     const uint16_t* q1 = p.q + b * p.q_token + (kvh * p.G + h0 + min(n8 + 8, rows - 1)) * p.q_head;
     const bool ok0 = n8 < rows, ok1 = n8 + 8 < rows;
-    if (!FP4) {
 #pragma unroll
-      for (int k = 0; k < D / 16; ++k) {
-        qa[k][0] = ok0 ? __ldg(reinterpret_cast<const uint32_t*>(q0 + k * 16) + c4) : 0u;
-        qa[k][1] = ok1 ? __ldg(reinterpret_cast<const uint32_t*>(q1 + k * 16) + c4) : 0u;
-        qa[k][2] = ok0 ? __ldg(reinterpret_cast<const uint32_t*>(q0 + k * 16) + 4 + c4) : 0u;
-        qa[k][3] = ok1 ? __ldg(reinterpret_cast<const uint32_t*>(q1 + k * 16) + 4 + c4) : 0u;
+    for (int k = 0; k < D / 16; ++k) {
+      qa[k][0] = ok0 ? __ldg(reinterpret_cast<const uint32_t*>(q0 + k * 16) + c4) : 0u;
+      qa[k][1] = ok1 ? __ldg(reinterpret_cast<const uint32_t*>(q1 + k * 16) + c4) : 0u;
+      qa[k][2] = ok0 ? __ldg(reinterpret_cast<const uint32_t*>(q0 + k * 16) + 4 + c4) : 0u;
+      qa[k][3] = ok1 ? __ldg(reinterpret_cast<const uint32_t*>(q1 + k * 16) + 4 + c4) : 0u;
+    }
+  } else {
+#pragma unroll
+    for (int h = 0; h < HT; ++h) {
+      const int r = 8 * h + n8;
+      const uint16_t* q = p.q + b * p.q_token + (kvh * p.G + h0 + min(r, rows - 1)) * p.q_head + c4 * (D / 4);
+      uint32_t top = 0;                                // largest |bf16| of the row, as bits
+#pragma unroll
+      for (int j = 0; j < NW; ++j) {
+        uint4 a = make_uint4(0, 0, 0, 0);
+        if (r < rows) a = __ldg(reinterpret_cast<const uint4*>(q) + j);
+        qb[h][2 * j][0] = a.x;
+        qb[h][2 * j][1] = a.y;
+        qb[h][2 * j + 1][0] = a.z;
+        qb[h][2 * j + 1][1] = a.w;
+#pragma unroll
+        for (int x = 0; x < 4; ++x) {
+          const uint32_t v = qb[h][2 * j + x / 2][x & 1] & 0x7fff7fffu;
+          top = max(top, max(v & 0xffffu, v >> 16));
+        }
       }
-    } else {
+      top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+      top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
+      const uint32_t eb = min(max(top >> 7, 1u), 253u);              // its biased exponent
+      const float down = __uint_as_float((254u - eb) << 23);
 #pragma unroll
-      for (int g = 0; g < D / 32; ++g) {
-        uint4 a = make_uint4(0, 0, 0, 0), e = a;
-        if (ok0) a = __ldg(reinterpret_cast<const uint4*>(q0 + g * 32) + c4);
-        if (ok1) e = __ldg(reinterpret_cast<const uint4*>(q1 + g * 32) + c4);
-        qa[2 * g][0] = a.x;
-        qa[2 * g][2] = a.y;
-        qa[2 * g + 1][0] = a.z;
-        qa[2 * g + 1][2] = a.w;
-        qa[2 * g][1] = e.x;
-        qa[2 * g][3] = e.y;
-        qa[2 * g + 1][1] = e.z;
-        qa[2 * g + 1][3] = e.w;
-      }
+      for (int j = 0; j < 2 * NW; ++j)
 #pragma unroll
-      for (int u = 0; u < 2; ++u) {
-        uint32_t top = 0;                              // largest |bf16| of the row, as bits
+        for (int x = 0; x < 2; ++x) {
+          const float2 f = Num<__nv_bfloat16>::up(qb[h][j][x]);
+          qb[h][j][x] = Num<__half>::down(f.x * down, f.y * down);
+        }
 #pragma unroll
-        for (int k = 0; k < D / 16; ++k)
-#pragma unroll
-          for (int x = 0; x < 2; ++x) {
-            const uint32_t v = qa[k][u + 2 * x] & 0x7fff7fffu;
-            top = max(top, max(v & 0xffffu, v >> 16));
-          }
-        top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
-        top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
-        const uint32_t eb = min(max(top >> 7, 1u), 253u);            // its biased exponent
-        const float down = __uint_as_float((254u - eb) << 23);
-        scale2[u] *= __uint_as_float(eb << 23);
-#pragma unroll
-        for (int k = 0; k < D / 16; ++k)
-#pragma unroll
-          for (int x = 0; x < 2; ++x) {
-            const float2 f = Num<__nv_bfloat16>::up(qa[k][u + 2 * x]);
-            qa[k][u + 2 * x] = Num<__half>::down(f.x * down, f.y * down);
-          }
-      }
+      for (int e = 0; e < 2; ++e)                      // this thread's columns are heads 2 c4 + e
+        scale2[h][e] *= __uint_as_float(__shfl_sync(0xffffffffu, eb, 4 * (2 * c4 + e)) << 23);
     }
   }
 
-  float o[D / 8][4];
+  // 16-bit rows: o[n tile of 8 channels], rows n8, n8 + 8.  FP4: o[HT * product + h]
+  float o[FP4 ? HT * D / 16 : D / 8][4];
+  constexpr int NO = sizeof(o) / sizeof(o[0]);
 #pragma unroll
-  for (int i = 0; i < D / 8; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.0f;
-  float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.0f, 0.0f};
+  for (int i = 0; i < NO; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.0f;
+  constexpr int HS = FP4 ? HT : 1;                     // pairs of query rows of a thread
+  float m[HS][2], l[HS][2];
+#pragma unroll
+  for (int h = 0; h < HS; ++h) {
+    m[h][0] = m[h][1] = -INFINITY;
+    l[h][0] = l[h][1] = 0.0f;
+  }
 
   // the ring: STAGES - 1 slices of this warp ahead
   uint32_t present[L::STAGES];
@@ -243,11 +270,11 @@ __global__ void __launch_bounds__(kThreads) paged_decode_kernel(const Params p) 
     }
     const uint32_t kb = ring + stage * STAGE, vb = SHARED ? kb : kb + L::HALF;
 
-    constexpr int NT = KS / 8;                         // 8-token tiles of a slice
-    float sc[NT][4];
+    if constexpr (!FP4) {
+      constexpr int NT = KS / 8;                       // 8-token tiles of a slice
+      float sc[NT][4];
 #pragma unroll
-    for (int i = 0; i < NT; ++i) sc[i][0] = sc[i][1] = sc[i][2] = sc[i][3] = 0.0f;
-    if (!FP4) {
+      for (int i = 0; i < NT; ++i) sc[i][0] = sc[i][1] = sc[i][2] = sc[i][3] = 0.0f;
 #pragma unroll
       for (int k = 0; k < D / 16; k += 2) {
 #pragma unroll
@@ -258,66 +285,52 @@ __global__ void __launch_bounds__(kThreads) paged_decode_kernel(const Params p) 
           mma16816<M>(sc[i], qa[k + 1], bb[2], bb[3]);
         }
       }
-    } else {
-#pragma unroll
-      for (int g = 0; g < D / 32; ++g) {
-#pragma unroll
-        for (int i = 0; i < NT; ++i) {
-          const int r = i * 8 + n8;
-          const uint32_t w = lds32(kb + r * L::ROW + (4 * g + c4) * 4);
-          const uint32_t s2 = scale_f16(lds16(kb + KS * L::ROW + r * (D / 16) + 2 * g), c4 >> 1);
-          mma16816<M>(sc[i], qa[2 * g], code_pair(w, 0, s2), code_pair(w, 1, s2));
-          mma16816<M>(sc[i], qa[2 * g + 1], code_pair(w, 2, s2), code_pair(w, 3, s2));
-        }
-      }
-    }
-    float mx[2] = {-INFINITY, -INFINITY};
-#pragma unroll
-    for (int i = 0; i < NT; ++i)
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const bool ok = (mask >> (i * 8 + c4 * 2 + (e & 1))) & 1u;
-        sc[i][e] = ok ? sc[i][e] * scale2[e >> 1] : -INFINITY;
-        mx[e >> 1] = fmaxf(mx[e >> 1], sc[i][e]);
-      }
-    float alpha[2];
-#pragma unroll
-    for (int u = 0; u < 2; ++u) {
-      mx[u] = fmaxf(mx[u], __shfl_xor_sync(0xffffffffu, mx[u], 1));
-      mx[u] = fmaxf(mx[u], __shfl_xor_sync(0xffffffffu, mx[u], 2));
-      const float mn = fmaxf(m[u], mx[u]);
-      const float ref = mn == -INFINITY ? 0.0f : mn;
-      alpha[u] = exp2_approx(m[u] - ref);
-      m[u] = mn;
-      l[u] *= alpha[u];
+      float mx[2] = {-INFINITY, -INFINITY};
 #pragma unroll
       for (int i = 0; i < NT; ++i)
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          sc[i][2 * u + e] = exp2_approx(sc[i][2 * u + e] - ref);
-          l[u] += sc[i][2 * u + e];
+        for (int e = 0; e < 4; ++e) {
+          const bool ok = (mask >> (i * 8 + c4 * 2 + (e & 1))) & 1u;
+          sc[i][e] = ok ? sc[i][e] * p.scale2 : -INFINITY;
+          mx[e >> 1] = fmaxf(mx[e >> 1], sc[i][e]);
         }
-    }
-    uint32_t pa[KS / 16][4];                           // P as the next product's left operand
+      float alpha[2];
 #pragma unroll
-    for (int t = 0; t < KS / 16; ++t) {
-      pa[t][0] = Num<M>::down(sc[2 * t][0], sc[2 * t][1]);
-      pa[t][1] = Num<M>::down(sc[2 * t][2], sc[2 * t][3]);
-      pa[t][2] = Num<M>::down(sc[2 * t + 1][0], sc[2 * t + 1][1]);
-      pa[t][3] = Num<M>::down(sc[2 * t + 1][2], sc[2 * t + 1][3]);
-    }
-    if (__any_sync(0xffffffffu, alpha[0] != 1.0f || alpha[1] != 1.0f)) {
+      for (int u = 0; u < 2; ++u) {
+        mx[u] = fmaxf(mx[u], __shfl_xor_sync(0xffffffffu, mx[u], 1));
+        mx[u] = fmaxf(mx[u], __shfl_xor_sync(0xffffffffu, mx[u], 2));
+        const float mn = fmaxf(m[0][u], mx[u]);
+        const float ref = mn == -INFINITY ? 0.0f : mn;
+        alpha[u] = exp2_approx(m[0][u] - ref);
+        m[0][u] = mn;
+        l[0][u] *= alpha[u];
 #pragma unroll
-      for (int i = 0; i < D / 8; ++i) {
-        o[i][0] *= alpha[0];
-        o[i][1] *= alpha[0];
-        o[i][2] *= alpha[1];
-        o[i][3] *= alpha[1];
+        for (int i = 0; i < NT; ++i)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            sc[i][2 * u + e] = exp2_approx(sc[i][2 * u + e] - ref);
+            l[0][u] += sc[i][2 * u + e];
+          }
       }
-    }
+      uint32_t pa[KS / 16][4];                         // P as the next product's left operand
 #pragma unroll
-    for (int t = 0; t < KS / 16; ++t) {
-      if (!FP4) {
+      for (int t = 0; t < KS / 16; ++t) {
+        pa[t][0] = Num<M>::down(sc[2 * t][0], sc[2 * t][1]);
+        pa[t][1] = Num<M>::down(sc[2 * t][2], sc[2 * t][3]);
+        pa[t][2] = Num<M>::down(sc[2 * t + 1][0], sc[2 * t + 1][1]);
+        pa[t][3] = Num<M>::down(sc[2 * t + 1][2], sc[2 * t + 1][3]);
+      }
+      if (__any_sync(0xffffffffu, alpha[0] != 1.0f || alpha[1] != 1.0f)) {
+#pragma unroll
+        for (int i = 0; i < NO; ++i) {
+          o[i][0] *= alpha[0];
+          o[i][1] *= alpha[0];
+          o[i][2] *= alpha[1];
+          o[i][3] *= alpha[1];
+        }
+      }
+#pragma unroll
+      for (int t = 0; t < KS / 16; ++t)
 #pragma unroll
         for (int i = 0; i < D / 16; ++i) {             // 16 tokens x 16 channels
           uint32_t bb[4];
@@ -325,57 +338,154 @@ __global__ void __launch_bounds__(kThreads) paged_decode_kernel(const Params p) 
           mma16816<M>(o[2 * i], pa[t], bb[0], bb[1]);
           mma16816<M>(o[2 * i + 1], pa[t], bb[2], bb[3]);
         }
-      } else {
-        // word n8 of a group of 64 channels, of tokens 2 c4, 2 c4 + 1, 2 c4 + 8, 2 c4 + 9
+    } else {
+      constexpr int MT = KS / 16;                      // 16-token tiles of a slice
+      float sc[MT][HT][4];
 #pragma unroll
-        for (int g = 0; g < D / 64; ++g) {
-          uint32_t w[4], s2[4];
+      for (int i = 0; i < MT; ++i) {
 #pragma unroll
-          for (int u = 0; u < 4; ++u) {
-            const int r = t * 16 + 2 * c4 + (u & 1) + 8 * (u >> 1);
-            w[u] = lds32(vb + r * L::ROW + (8 * g + n8) * 4);
-            s2[u] = scale_f16(lds16(vb + KS * L::ROW + r * (D / 16) + 4 * g + 2 * (n8 >> 2)), (n8 >> 1) & 1);
+        for (int h = 0; h < HT; ++h) sc[i][h][0] = sc[i][h][1] = sc[i][h][2] = sc[i][h][3] = 0.0f;
+        uint32_t w[2][NW], s2[2];                      // tokens n8 and n8 + 8
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+          const int r = i * 16 + 8 * u + n8;
+          lds_words<NW>(w[u], kb + r * L::ROW + c4 * (D / 8));
+          s2[u] = lds_bytes<D / 64>(kb + KS * L::ROW + r * (D / 16) + c4 * (D / 64));
+        }
+#pragma unroll
+        for (int j = 0; j < NW; ++j) {
+          uint32_t s[2];                               // the scale of word j's block, twice
+#pragma unroll
+          for (int u = 0; u < 2; ++u)
+            s[u] = __byte_perm(scales_f16(s2[u] >> (16 * (j / 4))), 0u, (j / 2) & 1 ? 0x3232 : 0x1010);
+#pragma unroll
+          for (int x = 0; x < 2; ++x) {
+            const uint32_t a[4] = {code_pair(w[0][j], 2 * x, s[0]), code_pair(w[1][j], 2 * x, s[1]),
+                                   code_pair(w[0][j], 2 * x + 1, s[0]), code_pair(w[1][j], 2 * x + 1, s[1])};
+#pragma unroll
+            for (int h = 0; h < HT; ++h) mma16816<M>(sc[i][h], a, qb[h][2 * j + x][0], qb[h][2 * j + x][1]);
+          }
+        }
+      }
+      uint32_t pb[MT][HT][2];                          // P as the next product's right operand
+      bool moved = false;
+      float alpha[HT][2];
+#pragma unroll
+      for (int h = 0; h < HT; ++h) {
+        float mx[2] = {-INFINITY, -INFINITY};
+#pragma unroll
+        for (int i = 0; i < MT; ++i)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const bool ok = (mask >> (i * 16 + n8 + 8 * (e >> 1))) & 1u;
+            sc[i][h][e] = ok ? sc[i][h][e] * scale2[h][e & 1] : -INFINITY;
+            mx[e & 1] = fmaxf(mx[e & 1], sc[i][h][e]);
           }
 #pragma unroll
-          for (int k = 0; k < 4; ++k) {                // channels 2 k and 2 k + 1 of the word
-            const uint32_t x0 = code_pair(w[0], k, s2[0]), x1 = code_pair(w[1], k, s2[1]);
-            const uint32_t y0 = code_pair(w[2], k, s2[2]), y1 = code_pair(w[3], k, s2[3]);
-            mma16816<M>(o[8 * g + 2 * k], pa[t], __byte_perm(x0, x1, 0x5410), __byte_perm(y0, y1, 0x5410));
-            mma16816<M>(o[8 * g + 2 * k + 1], pa[t], __byte_perm(x0, x1, 0x7632), __byte_perm(y0, y1, 0x7632));
+        for (int u = 0; u < 2; ++u) {
+#pragma unroll
+          for (int x = 4; x < 32; x *= 2) mx[u] = fmaxf(mx[u], __shfl_xor_sync(0xffffffffu, mx[u], x));
+          const float mn = fmaxf(m[h][u], mx[u]);
+          const float ref = mn == -INFINITY ? 0.0f : mn;
+          alpha[h][u] = exp2_approx(m[h][u] - ref);
+          moved |= alpha[h][u] != 1.0f;
+          m[h][u] = mn;
+          l[h][u] *= alpha[h][u];
+#pragma unroll
+          for (int i = 0; i < MT; ++i)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              sc[i][h][2 * e + u] = exp2_approx(sc[i][h][2 * e + u] - ref);
+              l[h][u] += sc[i][h][2 * e + u];
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < MT; ++i)
+#pragma unroll
+          for (int e = 0; e < 2; ++e)
+            pb[i][h][e] = transpose8(Num<M>::down(sc[i][h][2 * e], sc[i][h][2 * e + 1]));
+      }
+      if (__any_sync(0xffffffffu, moved)) {
+#pragma unroll
+        for (int i = 0; i < NO; ++i)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) o[i][e] *= alpha[i % HT][e & 1];
+      }
+      // a thread takes W words (8 W channels) of tokens 2 c4, 2 c4 + 1, 2 c4 + 8, 2 c4 + 9;
+      // the codes of two tokens are paired before they are converted
+#pragma unroll
+      for (int t = 0; t < MT; ++t) {
+        uint32_t ev[2][W], od[2][W], s[2][W / 4 + 1];
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+          const int r = t * 16 + 8 * u + 2 * c4;
+          uint32_t x[W], y[W];
+          lds_words<W>(x, vb + r * L::ROW + n8 * (4 * W));
+          lds_words<W>(y, vb + (r + 1) * L::ROW + n8 * (4 * W));
+          constexpr int SN = W == 4 ? 2 : 1;           // scale bytes of a thread
+          const uint32_t at = vb + KS * L::ROW + r * (D / 16) + (W == 1 ? n8 >> 1 : n8 * SN);
+          const uint32_t sx = lds_bytes<SN>(at), sy = lds_bytes<SN>(at + D / 16);
+          s[u][0] = scales_f16(__byte_perm(sx, sy, 0x0040));
+          if (SN == 2) s[u][W / 4] = scales_f16(__byte_perm(sx, sy, 0x0051));
+#pragma unroll
+          for (int j = 0; j < W; ++j) {
+            ev[u][j] = (x[j] & 0x0f0f0f0fu) | ((y[j] << 4) & 0xf0f0f0f0u);
+            od[u][j] = ((x[j] >> 4) & 0x0f0f0f0fu) | (y[j] & 0xf0f0f0f0u);
           }
+        }
+#pragma unroll
+        for (int i = 0; i < D / 16; ++i) {             // channel i of the lower, of the upper rows
+          const int c = W == 1 ? i : i & 7, j = W == 1 ? 0 : 2 * (i / 8), jh = W == 1 ? 0 : j + 1;
+          const int kl = c / 2, kh = W == 1 ? 2 + c / 2 : c / 2;
+          uint32_t a[4];
+#pragma unroll
+          for (int u = 0; u < 2; ++u) {
+            a[2 * u] = code_pair(c & 1 ? od[u][j] : ev[u][j], kl, s[u][i / 8 * (W / 4)]);
+            a[2 * u + 1] = code_pair(c & 1 ? od[u][jh] : ev[u][jh], kh, s[u][i / 8 * (W / 4)]);
+          }
+#pragma unroll
+          for (int h = 0; h < HT; ++h) mma16816<M>(o[HT * i + h], a, pb[t][h][0], pb[t][h][1]);
         }
       }
     }
     stage = stage + 1 == L::STAGES ? 0 : stage + 1;
-  }
-#pragma unroll
-  for (int u = 0; u < 2; ++u) {
-    l[u] += __shfl_xor_sync(0xffffffffu, l[u], 1);
-    l[u] += __shfl_xor_sync(0xffffffffu, l[u], 2);
   }
   // the warps meet: O rows padded by 4 floats, then (m, l)
   sm100::cp_async_wait<0>();
   __syncthreads();
   constexpr int PITCH = D + 4;
   float* so = reinterpret_cast<float*>(smem);
-  float2* sml = reinterpret_cast<float2*>(so + kWarps * 16 * PITCH);
+  float2* sml = reinterpret_cast<float2*>(so + kWarps * L::ROWS * PITCH);
+  if constexpr (!FP4) {
 #pragma unroll
-  for (int u = 0; u < 2; ++u) {
-    const int r = n8 + 8 * u;
-    float* dst = so + (warp * 16 + r) * PITCH;
-    if (!FP4) {
+    for (int u = 0; u < 2; ++u) {
+      const int r = n8 + 8 * u;
+      float* dst = so + (warp * L::ROWS + r) * PITCH;
+      l[0][u] += __shfl_xor_sync(0xffffffffu, l[0][u], 1);
+      l[0][u] += __shfl_xor_sync(0xffffffffu, l[0][u], 2);
 #pragma unroll
       for (int i = 0; i < D / 8; ++i)
         *reinterpret_cast<float2*>(dst + i * 8 + c4 * 2) = make_float2(o[i][2 * u], o[i][2 * u + 1]);
-    } else {
-      // product i of group g: column n is channel 64 g + 8 n + i
-#pragma unroll
-      for (int i = 0; i < D / 8; ++i) {
-        dst[(i / 8) * 64 + 16 * c4 + (i % 8)] = o[i][2 * u];
-        dst[(i / 8) * 64 + 16 * c4 + 8 + (i % 8)] = o[i][2 * u + 1];
-      }
+      if (c4 == 0) sml[warp * L::ROWS + r] = make_float2(m[0][u], l[0][u]);
     }
-    if (c4 == 0) sml[warp * 16 + r] = make_float2(m[u], l[u]);
+  } else {
+#pragma unroll
+    for (int h = 0; h < HT; ++h)
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        const int r = 8 * h + 2 * c4 + u;
+        float* dst = so + (warp * L::ROWS + r) * PITCH + n8 * (8 * W);
+#pragma unroll
+        for (int x = 4; x < 32; x *= 2) l[h][u] += __shfl_xor_sync(0xffffffffu, l[h][u], x);
+#pragma unroll
+        for (int i = 0; i < D / 16; i += 4)            // channels i .. i + 3 of the lower, of the upper rows
+#pragma unroll
+          for (int e = 0; e < 2; ++e)
+            *reinterpret_cast<float4*>(dst + (W == 1 ? 4 * e : 16 * (i / 8) + 8 * e + (i & 7))) =
+                make_float4(o[HT * i + h][2 * e + u], o[HT * (i + 1) + h][2 * e + u], o[HT * (i + 2) + h][2 * e + u],
+                            o[HT * (i + 3) + h][2 * e + u]);
+        if (n8 == 0) sml[warp * L::ROWS + r] = make_float2(m[h][u], l[h][u]);
+      }
   }
   __syncthreads();
   const bool partial = p.chunks > 1 && seen.total > p.chunk;
@@ -384,15 +494,15 @@ __global__ void __launch_bounds__(kThreads) paged_decode_kernel(const Params p) 
     const int r = i / PER, c = i % PER;
     float mx = -INFINITY;
 #pragma unroll
-    for (int w = 0; w < kWarps; ++w) mx = fmaxf(mx, sml[w * 16 + r].x);
+    for (int w = 0; w < kWarps; ++w) mx = fmaxf(mx, sml[w * L::ROWS + r].x);
     const float ref = mx == -INFINITY ? 0.0f : mx;
     float lr = 0.0f;
     float4 acc = make_float4(0, 0, 0, 0);
 #pragma unroll
     for (int w = 0; w < kWarps; ++w) {
-      const float2 ml = sml[w * 16 + r];
+      const float2 ml = sml[w * L::ROWS + r];
       const float f = exp2_approx(ml.x - ref);
-      const float4 v = *reinterpret_cast<const float4*>(so + (w * 16 + r) * PITCH + 4 * c);
+      const float4 v = *reinterpret_cast<const float4*>(so + (w * L::ROWS + r) * PITCH + 4 * c);
       lr += f * ml.y;
       acc.x += f * v.x;
       acc.y += f * v.y;
@@ -412,12 +522,12 @@ __global__ void __launch_bounds__(kThreads) paged_decode_kernel(const Params p) 
   }
 }
 
-template <class T, int D, bool FP4, bool SHARED>
+template <class T, int D, bool FP4, bool SHARED, int HT>
 csa2_status run(const Params& p, dim3 grid, cudaStream_t stream) {
-  using L = Lay<D, FP4>;
+  using L = Lay<D, FP4, HT>;
   static PerDevice<int> opted;
   opted.get(+[]() -> int {
-    cudaFuncSetAttribute(paged_decode_kernel<T, D, FP4, SHARED>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+    cudaFuncSetAttribute(paged_decode_kernel<T, D, FP4, SHARED, HT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                          L::bytes(SHARED));
     return 1;
   });
@@ -430,7 +540,7 @@ csa2_status run(const Params& p, dim3 grid, cudaStream_t stream) {
   cfg.attrs = at;
   cfg.numAttrs = 1;
   begin_launch(stream);
-  const cudaError_t e = cudaLaunchKernelEx(&cfg, paged_decode_kernel<T, D, FP4, SHARED>, p);
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, paged_decode_kernel<T, D, FP4, SHARED, HT>, p);
   note_launch(LK_ATTN, 1, stream);
   if (e != cudaSuccess) {
     cudaGetLastError();
@@ -456,7 +566,10 @@ csa2_status launch_paged_decode_stream(const PagedAttn& a, int chunk, int chunks
   p.scale2 = a.scale * kLog2e;
   p.Hq = a.Hq;
   p.G = a.G;
-  p.row_tiles = (a.G + 15) / 16;
+  // FP4 rows under up to 8 heads take products of 8 (the code conversion is then all
+  // that is left of the work per token); 16-bit rows have 16 query rows either way
+  const int ht = a.fmt == CSA2_KV_FP4 && a.G <= 8 ? 1 : 2;
+  p.row_tiles = (a.G + 8 * ht - 1) / (8 * ht);
   p.window = a.window;
   p.sinks = a.sinks;
   p.chunk = chunk;
@@ -465,12 +578,12 @@ csa2_status launch_paged_decode_stream(const PagedAttn& a, int chunk, int chunks
   const dim3 grid(static_cast<unsigned>(chunks), static_cast<unsigned>(a.kv.heads * p.row_tiles),
                   static_cast<unsigned>(a.kv.B));
   const bool sh = a.kv.v == a.kv.k;
-#define CSA2_STREAM_T(T_, D_, F_) (sh ? run<T_, D_, F_, true>(p, grid, stream) : run<T_, D_, F_, false>(p, grid, stream))
+#define CSA2_STREAM_T(T_, D_, F_, H_) (sh ? run<T_, D_, F_, true, H_>(p, grid, stream) : run<T_, D_, F_, false, H_>(p, grid, stream))
 #define CSA2_STREAM(D_)                                                                       \
   if (a.D == D_)                                                                              \
-    return a.fmt == CSA2_KV_FP4   ? CSA2_STREAM_T(__nv_bfloat16, D_, true)                    \
-           : a.fmt == CSA2_KV_F16 ? CSA2_STREAM_T(__half, D_, false)                          \
-                                  : CSA2_STREAM_T(__nv_bfloat16, D_, false);
+    return a.fmt == CSA2_KV_FP4   ? (ht == 1 ? CSA2_STREAM_T(__nv_bfloat16, D_, true, 1) : CSA2_STREAM_T(__nv_bfloat16, D_, true, 2)) \
+           : a.fmt == CSA2_KV_F16 ? CSA2_STREAM_T(__half, D_, false, 2)                       \
+                                  : CSA2_STREAM_T(__nv_bfloat16, D_, false, 2);
   CSA2_STREAM(64) CSA2_STREAM(128) CSA2_STREAM(256)
 #undef CSA2_STREAM
 #undef CSA2_STREAM_T
