@@ -539,10 +539,13 @@ Split split_of(const PagedAttn& a, int64_t max_len, int chunk) {
     // hold 256 tokens.  Measured (us at chunks of 256 / 1024 / 2048 / 8192): 64
     // ragged sequences up to 16K, 8 cache heads 338 / 243 / 236 / 285; one of 32K, 8
     // heads 46 / 31 / 34 / 108; 64 of 2K, 4 heads 66 / 53 / 49 / 49; one of 8K, one
-    // head 9.6 / 17 / 27 / 90 (128: 9.3, 64: 10.3)
+    // head 9.6 / 17 / 27 / 90 (128: 9.3, 64: 10.3).  FP4 rows under up to 8 heads have
+    // four CTAs per SM and half the work per token: 1024 / 2048, 64 ragged of up to 32K
+    // behind a window of 8192, 4 heads 73.6 / 79.8; of 8K, 4 heads x 64 32.9 / 37.1; 64
+    // of 2K, 4 heads 33.0 / 31.9
     const int64_t n = std::max<int64_t>(1, 2LL * sm_count() / std::max<int64_t>(1, units));
     c = std::max<int64_t>((seen + n - 1) / n, std::min<int64_t>(256, (seen + 63) / 64));
-    c = std::min<int64_t>(2048, std::max<int64_t>(64, (c + 63) / 64 * 64));
+    c = std::min<int64_t>(a.fmt == CSA2_KV_FP4 && a.G <= 8 ? 1024 : 2048, std::max<int64_t>(64, (c + 63) / 64 * 64));
   }
   s.chunk = static_cast<int>(std::min<int64_t>(c, 0x7fffffc0));
   s.chunks = static_cast<int>((seen + s.chunk - 1) / s.chunk);

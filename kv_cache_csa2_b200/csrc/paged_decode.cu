@@ -13,17 +13,23 @@
 // Measured: 64 ragged sequences of up to 16384 tokens, 64 heads over 8 x 128, 233 us
 // (6.05 TB/s, 0.92 of a plain copy's rate); one sequence of 8192 with its join, 9.0 us.
 //
-// FP4 rows stay packed in shared memory; a thread's fragment is made of whole code
-// words (8 channels of a token), which become f16 pairs in registers by the hardware's
+// FP4 rows stay packed in shared memory and become f16 in registers by the hardware's
 // E2M1 conversion and one product with the scale: a code times a scale has five
-// significant bits between 2^-10 and 2^12, exact in f16.  (Integer steps to bf16 cost
-// 26 instructions a word against 19.)  The channels of a dot product may come in any
-// order as long as q's come in the same one.  q's rows are brought to f16 by a power
-// of two that puts their largest value into [1, 2): values down to 2^-14 keep their
-// eight bits, a smaller one moves by at most 2^-25, a quarter step of an f32 at the
-// largest.  Measured: 64 ragged sequences of up to 32768, window 8192 + 4, 32 heads
-// over 4 x 128, 108 us (slices of 16 tokens 122; four CTAs per SM spill, 141).  Bound by
-// the instructions of the decoding, not by the 209 MB (32 us).
+// significant bits between 2^-10 and 2^12, exact in f16.  What bounds it is this
+// arithmetic (the integer pipe), so the products stand the other way round, with
+// columns of 8 heads:
+//   S^T[16 tokens, heads] = k q^T,  P^T turned by movmatrix,  O^T[channels, heads] += v^T P
+// The channels of a dot product and the rows of an output may come in any order, so a
+// thread takes whole runs of a row's codes (16 bytes of keys, 8 of values at 128
+// channels, each with its own scales); the value product wants two tokens of a channel
+// side by side, and their codes are paired before they are converted.  q's rows are
+// brought to f16 by a power of two that puts their largest value into [1, 2): values down to
+// 2^-14 keep their eight bits, a smaller one moves by at most 2^-25, a quarter step of
+// an f32 at the largest.  Measured: 64 ragged sequences of up to 32768, window 8192 + 4,
+// 32 heads over 4 x 128 (209 MB, 32 us at the copy rate): heads as rows 108 us, this way
+// 79, chunks of 1024 tokens 74, bytes of a word by the conversion's own operand instead
+// of shifts 68, row addresses once for keys and values 65; four CTAs per SM.
+
 #include <algorithm>
 
 #include "launchers.h"
@@ -95,7 +101,10 @@ __device__ __forceinline__ uint32_t transpose8(uint32_t a) {
 // The two codes of byte k of a word as an f16 pair, times a pair of scales.
 __device__ __forceinline__ uint32_t code_pair(uint32_t w, int k, uint32_t s2) {
   uint32_t d;
-  asm("{.reg .b8 b, x, y, z; mov.b32 {b, x, y, z}, %1; cvt.rn.f16x2.e2m1x2 %0, b;}" : "=r"(d) : "r"(w >> (8 * k)));
+  if (k == 0) asm("{.reg .b8 b, x, y, z; mov.b32 {b, x, y, z}, %1; cvt.rn.f16x2.e2m1x2 %0, b;}" : "=r"(d) : "r"(w));
+  if (k == 1) asm("{.reg .b8 b, x, y, z; mov.b32 {x, b, y, z}, %1; cvt.rn.f16x2.e2m1x2 %0, b;}" : "=r"(d) : "r"(w));
+  if (k == 2) asm("{.reg .b8 b, x, y, z; mov.b32 {x, y, b, z}, %1; cvt.rn.f16x2.e2m1x2 %0, b;}" : "=r"(d) : "r"(w));
+  if (k == 3) asm("{.reg .b8 b, x, y, z; mov.b32 {x, y, z, b}, %1; cvt.rn.f16x2.e2m1x2 %0, b;}" : "=r"(d) : "r"(w));
   const __half2 r = __hmul2(*reinterpret_cast<__half2*>(&d), *reinterpret_cast<__half2*>(&s2));
   return *reinterpret_cast<const uint32_t*>(&r);
 }
@@ -145,28 +154,30 @@ __global__ void __launch_bounds__(kThreads, FP4 && D <= 128 && HT == 1 ? 4 : 1) 
   // every token of a slice present: one bit per token
   auto issue = [&](int stage, int64_t row) -> uint32_t {
     const uint32_t dst0 = ring + stage * STAGE;
+    constexpr int HALVES = SHARED ? 1 : 2;
+    constexpr int CH = FP4 ? D / 32 : D / 8;           // 16-byte pieces of a row
 #pragma unroll
-    for (int half = 0; half < (SHARED ? 1 : 2); ++half) {
-      const uint8_t* src = half ? p.kv.v : p.kv.k;
-      const uint32_t dst = dst0 + half * L::HALF;
-      constexpr int CH = FP4 ? D / 32 : D / 8;         // 16-byte pieces of a row
+    for (int i = 0; i < KS * CH / 32; ++i) {
+      const int piece = i * 32 + lane, r = piece / CH, c = piece % CH;
+      const int64_t at = __shfl_sync(0xffffffffu, row, r);
+      const int64_t off = at < 0 ? 0 : (FP4 ? at >> 1 : at * 2) + c * 16;
+      const uint32_t n = at < 0 ? 0u : 16u, dst = dst0 + r * L::ROW + c * 16;
 #pragma unroll
-      for (int i = 0; i < KS * CH / 32; ++i) {
-        const int piece = i * 32 + lane, r = piece / CH, c = piece % CH;
+      for (int half = 0; half < HALVES; ++half) cp_async_16s(dst + half * L::HALF, (half ? p.kv.v : p.kv.k) + off, n);
+    }
+    if constexpr (FP4) {
+      constexpr int SB = D / 16;                       // scale bytes of a row: 4, 8 or 16
+      constexpr int W = SB / 4;                        // words (4-byte aligned: strides are multiples of 64)
+#pragma unroll
+      for (int i = 0; i < (KS * W + 31) / 32; ++i) {
+        const int piece = i * 32 + lane, r = (piece / W) & (KS - 1), c = piece % W;
         const int64_t at = __shfl_sync(0xffffffffu, row, r);
-        cp_async_16s(dst + r * L::ROW + c * 16, src + (at < 0 ? 0 : (FP4 ? at / 2 : at * 2) + c * 16),
-                     at < 0 ? 0u : 16u);
-      }
-      if (FP4) {
-        const uint8_t* sc = half ? p.kv.v_scales : p.kv.k_scales;
-        constexpr int SB = D / 16;                     // scale bytes of a row: 4, 8 or 16
-        constexpr int W = SB / 4;                      // words (4-byte aligned: strides are multiples of 64)
+        const int64_t off = at < 0 ? 0 : (at >> 4) + c * 4;
+        const uint32_t n = at < 0 ? 0u : 4u, dst = dst0 + KS * L::ROW + r * SB + c * 4;
+        if (piece < KS * W) {
 #pragma unroll
-        for (int i = 0; i < (KS * W + 31) / 32; ++i) {
-          const int piece = i * 32 + lane, r = (piece / W) & (KS - 1), c = piece % W;
-          const int64_t at = __shfl_sync(0xffffffffu, row, r);
-          if (piece < KS * W)
-            cp_async_4(dst + KS * L::ROW + r * SB + c * 4, sc + (at < 0 ? 0 : at / 16 + c * 4), at < 0 ? 0u : 4u);
+          for (int half = 0; half < HALVES; ++half)
+            cp_async_4(dst + half * L::HALF, (half ? p.kv.v_scales : p.kv.k_scales) + off, n);
         }
       }
     }
@@ -377,10 +388,19 @@ __global__ void __launch_bounds__(kThreads, FP4 && D <= 128 && HT == 1 ? 4 : 1) 
         for (int i = 0; i < MT; ++i)
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
-            const bool ok = (mask >> (i * 16 + n8 + 8 * (e >> 1))) & 1u;
-            sc[i][h][e] = ok ? sc[i][h][e] * scale2[h][e & 1] : -INFINITY;
-            mx[e & 1] = fmaxf(mx[e & 1], sc[i][h][e]);
+            sc[i][h][e] *= scale2[h][e & 1];
           }
+        if (mask != 0xffffffffu) {
+#pragma unroll
+          for (int i = 0; i < MT; ++i)
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              if (!((mask >> (i * 16 + n8 + 8 * (e >> 1))) & 1u)) sc[i][h][e] = -INFINITY;
+        }
+#pragma unroll
+        for (int i = 0; i < MT; ++i)
+#pragma unroll
+          for (int u = 0; u < 2; ++u) mx[u] = max3(mx[u], sc[i][h][u], sc[i][h][2 + u]);
 #pragma unroll
         for (int u = 0; u < 2; ++u) {
 #pragma unroll
