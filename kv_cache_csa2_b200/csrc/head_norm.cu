@@ -5,15 +5,19 @@
 // takes a block of tokens: it requests its first rows, computes the tokens'
 // angles once for all heads into shared memory, and then runs over the
 // (token, head) rows; a group of lanes holds a row, the norm is a shuffle sum.
-// Measured: 8192 tokens of 64 + 8 heads x 128, 57.5 us (5.25 TB/s); 4096 of 64 + 1 heads
-// x 512, 107.5 us (5.08 TB/s).  What bounds it then is instruction issue (77 % of the
-// slots: every product and sum of the rotation rounds by itself) and four CTAs of
-// 64 registers per SM; weights held in registers cost a CTA and were slower.
+// Rows come by cp.async into a thread's own slots, two passes ahead.
+// Measured: 8192 tokens of 64 + 8 heads x 128, 52.2 us (5.79 TB/s, 0.88 of the copy rate;
+// 57.5 with the next row in registers); 4096 of 64 + 1 heads x 512, 98.6 us (5.53 TB/s;
+// 107.5 with 64-bit offsets and rows in registers).  Next to the memory stands instruction
+// issue (every product and sum of the rotation rounds by itself); three or five
+// CTAs per SM (54.4, 55), a stage more (53.3) and the weights in registers are slower.
+
 #include <algorithm>
 
 #include "common.cuh"
 #include "launchers.h"
 #include "paged.h"
+#include "sm100.cuh"
 #include "rope.cuh"
 
 namespace csa2 {
@@ -22,6 +26,7 @@ using namespace rope;
 
 constexpr int kThreads = 256;
 constexpr int kMaxTokens = 8;
+constexpr int kStages = 3;
 
 struct Side {
   const uint16_t* in;
@@ -37,9 +42,15 @@ struct Params {
   int Hq, H, D, items, lanes;        // H = query plus key heads; lanes per row (power of two)
   int step_t, step_h;                // a pass's rows in tokens and heads
   int tokens, rows_cta;              // tokens per CTA, rows per CTA (grid.y cuts a token's heads)
-  float eps;
+  float eps, inv_d;
   RopeArgs rope;
 };
+
+// The offset of row (t, head) in a side's tensor: 32 bits where a CTA's rows allow it.
+template <class O>
+__device__ __forceinline__ O offset_of(int t, int64_t st, int head, int64_t sh) {
+  return static_cast<O>(t) * static_cast<O>(st) + static_cast<O>(head) * static_cast<O>(sh);
+}
 
 __device__ __forceinline__ void scale8(float2 (&x)[4], float inv, const float* w) {
   const float4 a = __ldg(reinterpret_cast<const float4*>(w)), b = __ldg(reinterpret_cast<const float4*>(w) + 1);
@@ -50,9 +61,11 @@ __device__ __forceinline__ void scale8(float2 (&x)[4], float inv, const float* w
   x[3] = mul2(mul2(x[3], i2), make_float2(b.z, b.w));
 }
 
-template <class T>
+// O: the type of offsets among a CTA's rows (64-bit ones cost a quarter of the instructions)
+template <class T, class O>
 __global__ void __launch_bounds__(kThreads, 4) head_norm_kernel(const Params p) {
-  extern __shared__ float4 cs[];                                   // [tokens][half / 2]
+  extern __shared__ uint4 smem[];
+  float4* cs = reinterpret_cast<float4*>(smem);        // angles, [tokens][half / 2]
   const int64_t t0 = static_cast<int64_t>(blockIdx.x) * p.tokens;
   const int nt = static_cast<int>(min(static_cast<int64_t>(p.tokens), p.T - t0));
   const int per_pass = kThreads / p.lanes;
@@ -62,18 +75,31 @@ __global__ void __launch_bounds__(kThreads, 4) head_norm_kernel(const Params p) 
   Item it = item_at(sub, p.D, p.rope.half, p.rope.offset);
   if (sub >= p.items) it.c0 = it.c1 = it.freq = -1;
 
-  uint4 v0, v1;
-  int tl = r / p.H, head = r - tl * p.H;
-  auto request = [&](int row) {
-    v0 = v1 = make_uint4(0, 0, 0, 0);
-    if (row >= r_end) return;
-    const uint16_t* src = head < p.Hq ? p.q.in + (t0 + tl) * p.q.in_t + head * p.q.in_h
-                                      : p.k.in + (t0 + tl) * p.k.in_t + (head - p.Hq) * p.k.in_h;
-    if (it.c0 >= 0) v0 = *reinterpret_cast<const uint4*>(src + it.c0);
-    if (it.c1 >= 0) v1 = *reinterpret_cast<const uint4*>(src + it.c1);
+  const uint16_t *q_in = p.q.in + t0 * p.q.in_t, *k_in = p.k.in + t0 * p.k.in_t;
+  uint16_t *q_out = p.q.out + t0 * p.q.out_t, *k_out = p.k.out + t0 * p.k.out_t;
+  // a thread's own vectors, kStages - 1 passes ahead
+  uint4* ring = smem + p.tokens * (p.rope.half / 2) + threadIdx.x;
+  int stage = 0;
+  int tl = r / p.H, head = r - tl * p.H, tl_a = tl, head_a = head;
+  auto step = [&](int& t, int& h) {                    // the row a pass further
+    t += p.step_t;
+    h += p.step_h;
+    if (h >= p.H) h -= p.H, ++t;
+  };
+  auto request = [&](int row, int stage) {
+    const bool live = row < r_end, q = live ? head_a < p.Hq : p.Hq > 0;
+    const uint16_t* src = (q ? q_in : k_in) + (live ? offset_of<O>(tl_a, q ? p.q.in_t : p.k.in_t,
+                                                                   q ? head_a : head_a - p.Hq,
+                                                                   q ? p.q.in_h : p.k.in_h) : 0);
+    uint4* dst = ring + stage * 2 * kThreads;
+    sm100::cp_async_16(dst, src + max(it.c0, 0), live && it.c0 >= 0 ? 16u : 0u);
+    sm100::cp_async_16(dst + kThreads, src + max(it.c1, 0), live && it.c1 >= 0 ? 16u : 0u);
+    sm100::cp_async_commit();
+    step(tl_a, head_a);
   };
   pdl_wait();
-  request(r);
+#pragma unroll
+  for (int i = 0; i < kStages - 1; ++i) request(r + i * per_pass, i);
   if (p.rope.inv_freq) {
     for (int i = threadIdx.x; i < nt * p.rope.half; i += kThreads) {
       const int t = i / p.rope.half, f = i - t * p.rope.half;
@@ -84,9 +110,12 @@ __global__ void __launch_bounds__(kThreads, 4) head_norm_kernel(const Params p) 
   }
   // all lanes of a warp stay in the loop together (the shuffles need them)
   for (int base = blockIdx.y * p.rows_cta; base < r_end; base += per_pass, r += per_pass) {
+    sm100::cp_async_wait<kStages - 2>();
     float2 x0[4], x1[4];
-    unpack8<T>(v0, x0);
-    unpack8<T>(v1, x1);
+    unpack8<T>(ring[stage * 2 * kThreads], x0);
+    unpack8<T>(ring[stage * 2 * kThreads + kThreads], x1);
+    request(r + (kStages - 1) * per_pass, stage == 0 ? kStages - 1 : stage - 1);
+    stage = stage == kStages - 1 ? 0 : stage + 1;
     const bool live = r < r_end, is_q = head < p.Hq;
     const int my_t = tl, my_h = head;
     const float* w = is_q ? p.q.weight : p.k.weight;
@@ -96,22 +125,20 @@ __global__ void __launch_bounds__(kThreads, 4) head_norm_kernel(const Params p) 
     for (int o = p.lanes >> 1; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
     // a row is read whole by its lanes before any of them stores (the shuffle
     // above), so an output may be its input
-    tl += p.step_t;                                    // the row a pass further
-    head += p.step_h;
-    if (head >= p.H) head -= p.H, ++tl;
-    request(r + per_pass);
+    step(tl, head);
     if (!live) continue;
     if (w) {
-      const float inv = rsqrtf(sum / static_cast<float>(p.D) + p.eps);
+      const float inv = rsqrtf(sum * p.inv_d + p.eps);
       if (it.c0 >= 0) scale8(x0, inv, w + it.c0);
       if (it.c1 >= 0) scale8(x1, inv, w + it.c1);
     }
     if (p.rope.inv_freq) rotate_item(x0, x1, it, p.rope.half, p.rope.interleaved, cs + my_t * (p.rope.half / 2));
-    uint16_t* dst = is_q ? p.q.out + (t0 + my_t) * p.q.out_t + my_h * p.q.out_h
-                         : p.k.out + (t0 + my_t) * p.k.out_t + (my_h - p.Hq) * p.k.out_h;
+    uint16_t* dst = (is_q ? q_out : k_out) + offset_of<O>(my_t, is_q ? p.q.out_t : p.k.out_t,
+                                                          is_q ? my_h : my_h - p.Hq, is_q ? p.q.out_h : p.k.out_h);
     if (it.c0 >= 0) *reinterpret_cast<uint4*>(dst + it.c0) = pack8<T>(x0);
     if (it.c1 >= 0) *reinterpret_cast<uint4*>(dst + it.c1) = pack8<T>(x1);
   }
+  sm100::cp_async_wait<0>();
 }
 
 Side side_of(const HeadRows& in, const HeadRows& out, const float* weight) {
@@ -134,6 +161,7 @@ csa2_status launch_head_norm(csa2_dtype dtype, const HeadRows& q, const float* q
   p.H = q.heads + k.heads;
   p.D = D;
   p.eps = eps;
+  p.inv_d = static_cast<float>(1.0 / D);
   p.rope = rope;
   p.items = items_of(D, rope.half);
   p.lanes = 1;
@@ -156,14 +184,25 @@ csa2_status launch_head_norm(csa2_dtype dtype, const HeadRows& q, const float* q
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(gx), static_cast<unsigned>(ny));
   cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = static_cast<size_t>(p.tokens) * rope.half * sizeof(float2);
+  cfg.dynamicSmemBytes = static_cast<size_t>(p.tokens) * rope.half * sizeof(float2) + kStages * 2 * kThreads * 16;
   cfg.stream = stream;
   cudaLaunchAttribute at[1] = {pdl_attribute()};
   cfg.attrs = at;
   cfg.numAttrs = 1;
   begin_launch(stream);
-  const cudaError_t e = dtype == CSA2_F16 ? cudaLaunchKernelEx(&cfg, head_norm_kernel<__half>, p)
-                                          : cudaLaunchKernelEx(&cfg, head_norm_kernel<__nv_bfloat16>, p);
+  int64_t reach = 0;                                   // the largest offset among a CTA's rows
+  for (const HeadRows* r : {&q, &q_out, &k, &k_out})
+    if (r->heads > 0)
+      reach = std::max(reach, p.tokens > 0x7fffffff / (r->token_stride + 1) || r->heads > 0x7fffffff / (r->head_stride + 1)
+                                  ? int64_t{1} << 32
+                                  : p.tokens * r->token_stride + r->heads * r->head_stride);
+  const bool narrow = reach <= 0x7fffffff;
+  const cudaError_t e =
+      dtype == CSA2_F16
+          ? (narrow ? cudaLaunchKernelEx(&cfg, head_norm_kernel<__half, int32_t>, p)
+                    : cudaLaunchKernelEx(&cfg, head_norm_kernel<__half, int64_t>, p))
+          : (narrow ? cudaLaunchKernelEx(&cfg, head_norm_kernel<__nv_bfloat16, int32_t>, p)
+                    : cudaLaunchKernelEx(&cfg, head_norm_kernel<__nv_bfloat16, int64_t>, p));
   note_launch(LK_OTHER, 1, stream);
   if (e != cudaSuccess) {
     cudaGetLastError();
