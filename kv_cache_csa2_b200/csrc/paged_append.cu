@@ -5,9 +5,9 @@
 // and page addresses computed once for all heads, then the (token, head) rows.
 // An FP4 block of 16 channels is the same vector of two neighbouring lanes, so
 // its absolute maximum is one shuffle and each lane packs its own 8 codes.
-// Measured: 8191 tokens of 8 heads x 128 (keys and values), 15.4 us (4.4 TB/s), about one
-// wave, so the place and angles of a CTA's tokens stand at its start in full; 4096
-// shared rows x 512 into FP4, 8.6 us, of which the rounding to FP4 (150 instructions
+// Measured: 8191 tokens of 8 heads x 128 (keys and values), 14.4 us (4.7 TB/s; 15.5 with
+// one row ahead instead of two), about one wave, so the place and angles of a CTA's tokens
+// stand at its start in full; 4096 shared rows x 512 into FP4, 9.0 us, of which the rounding to FP4 (150 instructions
 // per 16 channels) is the larger part.
 #include <algorithm>
 
@@ -15,6 +15,7 @@
 #include "fp4.cuh"
 #include "paged.h"
 #include "rope.cuh"
+#include "sm100.cuh"
 
 namespace csa2 {
 namespace {
@@ -22,6 +23,7 @@ using namespace rope;
 
 constexpr int kThreads = 256;
 constexpr int kMaxTokens = 8;
+constexpr int kStages = 3;
 
 struct Params {
   const uint16_t *k, *v;
@@ -62,7 +64,8 @@ __device__ __forceinline__ uint32_t pack_half_block(const uint4& v, uint32_t* sc
 
 template <class T, bool FP4>
 __global__ void __launch_bounds__(kThreads) paged_append_kernel(const Params p) {
-  extern __shared__ float4 cs[];                                   // [tokens][half / 2]
+  extern __shared__ uint4 smem[];
+  float4* cs = reinterpret_cast<float4*>(smem);                    // angles, [tokens][half / 2]
   __shared__ int64_t s_row[kMaxTokens];                            // the token's place (head 0), -1: skip
   const int64_t t0 = static_cast<int64_t>(blockIdx.x) * p.tokens;
   const int nt = static_cast<int>(min(static_cast<int64_t>(p.tokens), p.T - t0));
@@ -74,18 +77,28 @@ __global__ void __launch_bounds__(kThreads) paged_append_kernel(const Params p) 
   if (sub >= p.items) it.c0 = it.c1 = it.freq = -1;
   const int hk = p.cache.heads;
 
-  uint4 v0, v1;
-  int tl = r / p.H, head = r - tl * p.H;
-  auto request = [&](int row) {
-    v0 = v1 = make_uint4(0, 0, 0, 0);
-    if (row >= r_end) return;
-    const uint16_t* src = head < hk ? p.k + (t0 + tl) * p.k_t + head * p.k_h
-                                    : p.v + (t0 + tl) * p.v_t + (head - hk) * p.v_h;
-    if (it.c0 >= 0) v0 = __ldg(reinterpret_cast<const uint4*>(src + it.c0));
-    if (it.c1 >= 0) v1 = __ldg(reinterpret_cast<const uint4*>(src + it.c1));
+  // a thread's own vectors, kStages - 1 passes ahead
+  uint4* ring = smem + p.tokens * (p.rope.half / 2) + threadIdx.x;
+  int stage = 0;
+  int tl = r / p.H, head = r - tl * p.H, tl_a = tl, head_a = head;
+  auto step = [&](int& t, int& h) {                    // the row a pass further
+    t += p.step_t;
+    h += p.step_h;
+    if (h >= p.H) h -= p.H, ++t;
+  };
+  auto request = [&](int row, int st) {
+    const bool live = row < r_end, is_k = !live || head_a < hk;
+    const uint16_t* src = is_k ? p.k : p.v;
+    if (live) src += (t0 + tl_a) * (is_k ? p.k_t : p.v_t) + (is_k ? head_a : head_a - hk) * (is_k ? p.k_h : p.v_h);
+    uint4* dst = ring + st * 2 * kThreads;
+    sm100::cp_async_16(dst, src + max(it.c0, 0), live && it.c0 >= 0 ? 16u : 0u);
+    sm100::cp_async_16(dst + kThreads, src + max(it.c1, 0), live && it.c1 >= 0 ? 16u : 0u);
+    sm100::cp_async_commit();
+    step(tl_a, head_a);
   };
   pdl_wait();
-  request(r);
+#pragma unroll
+  for (int i = 0; i < kStages - 1; ++i) request(r + i * per_pass, i);
   if (threadIdx.x < nt) {
     const int64_t t = t0 + threadIdx.x;
     const int s = __ldg(p.seq + t);
@@ -112,13 +125,13 @@ __global__ void __launch_bounds__(kThreads) paged_append_kernel(const Params p) 
   __syncthreads();
   // all lanes of a warp stay in the loop together (the shuffles need them)
   for (int base = blockIdx.y * p.rows_cta; base < r_end; base += per_pass, r += per_pass) {
-    uint4 a = v0, b = v1;
+    sm100::cp_async_wait<kStages - 2>();
+    uint4 a = ring[stage * 2 * kThreads], b = ring[stage * 2 * kThreads + kThreads];
+    request(r + (kStages - 1) * per_pass, stage == 0 ? kStages - 1 : stage - 1);
+    stage = stage == kStages - 1 ? 0 : stage + 1;
     const bool live = r < r_end, is_k = head < hk;
     const int my_t = tl, my_h = is_k ? head : head - hk;
-    tl += p.step_t;                                    // the row a pass further
-    head += p.step_h;
-    if (head >= p.H) head -= p.H, ++tl;
-    request(r + per_pass);
+    step(tl, head);
     if (live && is_k && p.rope.inv_freq && it.freq >= 0) {
       float2 x0[4], x1[4];
       unpack8<T>(a, x0);
@@ -152,6 +165,7 @@ __global__ void __launch_bounds__(kThreads) paged_append_kernel(const Params p) 
       if (it.c1 >= 0) *reinterpret_cast<uint4*>(dst + it.c1) = b;
     }
   }
+  sm100::cp_async_wait<0>();
 }
 
 }  // namespace
@@ -193,7 +207,7 @@ csa2_status launch_paged_append(csa2_dtype dtype, const HeadRows& k, const HeadR
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(gx), static_cast<unsigned>(ny));
   cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = static_cast<size_t>(p.tokens) * rope.half * sizeof(float2);
+  cfg.dynamicSmemBytes = static_cast<size_t>(p.tokens) * rope.half * sizeof(float2) + kStages * 2 * kThreads * 16;
   cfg.stream = stream;
   cudaLaunchAttribute at[1] = {pdl_attribute()};
   cfg.attrs = at;
