@@ -406,8 +406,8 @@ csa2_status csa2_paged_append(csa2_dtype dtype, const csa2_heads* k, const csa2_
  *   out[b,h,:] = sum_j softmax_j(scale * q[b,h] . k[j, h / (Hq / heads)]) v[j, ...]
  *   lse[b,h]   = log sum_j exp(scale * q . k)
  * A sequence of length 0 gives out = 0 and lse = -inf.  Dot products, softmax
- * statistics and sums in f32, the weights rounded to the 16-bit type for the
- * product with the values, out rounded once.  FP4 rows are dequantised exactly.
+ * statistics and sums in f32, the weights rounded to the 16-bit type (FP4: to
+ * f16) for the product with the values, out rounded once.  FP4 rows are dequantised exactly.
  * The visible tokens are cut into chunks that run side by side and are joined
  * in order.  chunk > 0 (a multiple of 64; rows of 512 channels take the next
  * multiple of 128) fixes their length: a query's bits

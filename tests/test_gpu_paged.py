@@ -225,6 +225,33 @@ def test_decode_huge_scores_and_identical_keys():
         assert np.all(np.abs(P.f64(out[b]) - mean) <= P.half_step(torch.bfloat16) * (np.abs(mean) + 1.02 * mag) + 2e-5 * mag)
 
 
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("G", [1, 5, 8, 9, 16, 17])
+@pytest.mark.parametrize("shared,window,sinks,sign", [(False, 0, 0, 1.0), (True, 150, 5, -1.0)])
+def test_decode_fp4_groups_and_magnitudes(D, G, shared, window, sinks, sign):
+    """Query heads that fill the products' columns or not, each of its own magnitude (0 among
+    them), a page that is not in the pool, and a length inside a slice."""
+    lens, page = [700, 33, 18], 16
+    cache, host = P.make_cache("fp4", lens, page, 2, D, shared=shared, seed=151)
+    q = P.rng_normal(152, 3, 2 * G, D)
+    q *= torch.tensor([1.0, 2.0 ** -20, 0.0, 8.0, 2.0 ** -3], device="cuda").repeat(2 * G)[:2 * G, None].to(q.dtype)
+    gone = 2 if window == 0 else 40                                  # a page that is seen
+    cache.table[0, gone] = -3
+    scale = sign * D ** -0.5
+    out, lse = K.csa2_paged_decode_attn(q, cache, scale, window=window, sinks=sinks, chunk=128)
+    with pytest.raises(K.CSA2Error):
+        K.csa2_device_error()
+    qh = P.f64(q)
+    for b, n in enumerate(lens):
+        at = np.arange(n)
+        seen = (n - 1 - at < window) | (at < sinks) if window else at >= 0
+        if b == 0:
+            seen &= at // page != gone
+        k, v = host[b][0][seen], host[b][1][seen]
+        want = O.causal_attn(qh[b:b + 1], [len(k) - 1], k, v, scale)
+        P.check_attn(out[b:b + 1], lse[b:b + 1], want, qh[b:b + 1], k, abs(scale), torch.bfloat16, n, f"seq {b}")
+
+
 def test_decode_bad_table_and_length():
     cache, host = P.make_cache("bf16", [200, 40, 10], 16, 1, 128, seed=51)
     q = P.rng_normal(52, 3, 4, 128)
