@@ -174,6 +174,14 @@ __device__ __forceinline__ void tma_load_page(void* dst, const CUtensorMap* map,
       : "memory");
 }
 
+// The same box into L2 ahead of its load.
+__device__ __forceinline__ void tma_prefetch_page(const CUtensorMap* map, int c, int head, int slot, int page) {
+  asm volatile("cp.async.bulk.prefetch.tensor.4d.L2.global.tile [%0, {%1, %2, %3, %4}];" ::"l"(
+                   reinterpret_cast<uint64_t>(map)),
+               "r"(c), "r"(head), "r"(slot), "r"(page)
+               : "memory");
+}
+
 __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16]) {
   asm volatile(
       "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
@@ -209,6 +217,16 @@ __device__ __forceinline__ bool wait_phase(uint64_t* bar, uint32_t parity, volat
   bool ok = true;
   if (!sm100::mbar_try_wait(bar, parity)) ok = wait_slow(bar, parity, abort, err);
   return __all_sync(0xffffffffu, ok);
+}
+
+// Whether a phase is over, without waiting.
+__device__ __forceinline__ bool phase_over(uint64_t* bar, uint32_t parity) {
+  uint32_t r;
+  asm volatile("{.reg .pred p; mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2; selp.u32 %0, 1, 0, p;}"
+               : "=r"(r)
+               : "r"(sm100::smem_u32(bar)), "r"(parity)
+               : "memory");
+  return r != 0;
 }
 
 // A weight of 0 times a value that is not finite is NaN, so in a tile such a value

@@ -8,22 +8,26 @@
 // read from shared memory as it lies, as key and as value:
 //   S^T[key, head] = K q^T        (M = 128 keys, N = NH, K = D)
 //   O^T[channel, head] += V^T P   (M = 128 channels, N = NH, K = 128 keys)
-//   warps 0-3, 4-7  softmax, one thread per key and half of the heads (all of them,
-//                   warps 0-3 alone, for up to 16): P = 2^(s - ref), row sums kept
-//                   per thread and added up at the end
+//   warps 0-15      softmax, one thread per key and 16 of the heads (warps 0-3 alone
+//                   for up to 16): P = 2^(s - ref), row sums kept per thread and added
+//                   up at the end
 //   one warp        issues the products
 //   three warps     fill a ring of 8 blocks of 64 channels x 128 keys (16 KiB, TMA
 //                   boxes by page); a block of a shared row serves the score and then
 //                   the value product and is refilled as soon as its channels are
-//                   through.  (One warp took 450 clocks a block to issue.)
+//                   through.  (One warp took 450 clocks a block to issue.)  The tile
+//                   behind is asked into L2 meanwhile.
 // A head's reference is its maximum over the first tile and moves (with a rescaled
 // output in TMEM) only when some score has outgrown it by 2^8, so the steady state
 // takes no maximum across keys: one barrier with an OR per tile asks whether any has.
 //
-// HBM-bound: a 128 KiB tile of 512 channels arrives in 5600 clocks at an SM's share
-// of the memory rate; its products take about 3100 (both operands from shared
-// memory), and the softmax stands between them.  Measured: 32 sequences of 65536 tokens,
-// 64 heads over one 512-wide row, 467 us (4.6 TB/s).
+// A 128 KiB tile of 512 channels arrives in 5600 clocks at an SM's share of the memory
+// rate, but it fills shared memory next to q, so a tile is a chain: value products (1750
+// clocks, a pair of blocks free every 440), the next tile's blocks from L2 (3500 at the 37
+// bytes a clock an SM gets), the last pair's score products (650), softmax (1000): 6200.
+// Measured: 32 sequences of 65536 tokens, 64 heads over one 512-wide row, 445 us (4.8 TB/s);
+// without the prefetch into L2 461, with 8 softmax warps 450, half of their exponentials
+// on the multiply-add pipe no change.
 #include <algorithm>
 #include <type_traits>
 
@@ -46,7 +50,7 @@ constexpr float kLazy = 8.0f;
 
 template <int D, int NH>
 struct Lay {
-  static constexpr int SW = NH == 64 ? 8 : 4;          // softmax warps
+  static constexpr int SW = NH == 64 ? 16 : 4;          // softmax warps
   static constexpr int HW = NH * 4 / SW;               // heads per softmax thread
   static constexpr int THREADS = (SW + 1 + kLoaders) * 32;
   static constexpr int DB = D / 64;                    // blocks per tile of keys (or values)
@@ -215,6 +219,14 @@ __global__ void __launch_bounds__(Lay<D, NH>::THREADS, 1)
     bool ok = true;
     for (int tile = 0; tile < tiles && ok; ++tile) {
       const int next = page_of(tile + 1);
+      if (next >= 0) {
+        // the tile behind goes to L2 while this one fills shared memory
+        const int sl = (at.start(first + tile + 1) + br) & ((1 << p.kv.page_shift) - 1);
+        for (int i = lw; i < DB; i += kLoaders) {
+          tma_prefetch_page(&k_map, i * 64, kvh, sl, next);
+          if (!SHARED) tma_prefetch_page(&v_map, i * 64, kvh, sl, next);
+        }
+      }
       const int t0 = at.start(first + tile), a = t0 + br;
       const bool any = mine && some(a, p.box);
       const bool all = any && ((a >= at.lo && a + p.box - 1 <= at.pmax) || a + p.box <= at.ns);
@@ -248,12 +260,8 @@ __global__ void __launch_bounds__(Lay<D, NH>::THREADS, 1)
           uint8_t* const dst = smem + L::RING + st * BLK;
           if (lane == 0) mbar_arrive_expect_tx(to, __popc(boxes) * p.box * 128);
           __syncwarp();
-          for (uint32_t m = boxes; m; m &= m - 1) {
-            const int bx = __ffs(m) - 1;
-            const int pg = __shfl_sync(0xffffffffu, page, bx), sl = __shfl_sync(0xffffffffu, slot_in_page, bx);
-            if (elect_one()) tma_load_page(dst + bx * p.box * 128, half ? &v_map : &k_map, to, i * 64, kvh, sl, pg);
-            __syncwarp();
-          }
+          if (box) tma_load_page(dst + br * 128, half ? &v_map : &k_map, to, i * 64, kvh, slot_in_page, page);
+          __syncwarp();
           if (!fix) {
             issued = u + i + 1;
             continue;
@@ -297,10 +305,17 @@ __global__ void __launch_bounds__(Lay<D, NH>::THREADS, 1)
     uint32_t u = 0;                                    // blocks taken
     bool ok = true;
     for (int tile = 0; tile < tiles && ok; ++tile) {
-      // two blocks at a time: a wait costs about as much as one block's products
+      // two blocks at a time.  The two waits cost 206 clocks even for blocks that are
+      // there, half of their products' time, so one look at all blocks comes first.
+      const uint32_t mine = u + (lane & (DB - 1));
+      uint32_t here = 0;
       for (int i = 0; i < DB && ok; i += 2) {
         const uint32_t st = (u + i) % SLOTS, parity = ((u + i) / SLOTS) & 1;
-        ok = wait(full + st, parity) && wait(full + st + 1, parity);
+        if (((here >> i) & 3u) != 3u) {
+          here = __ballot_sync(0xffffffffu, phase_over(full + mine % SLOTS, (mine / SLOTS) & 1));
+          __syncwarp();
+          if (((here >> i) & 3u) != 3u) ok = wait(full + st, parity) && wait(full + st + 1, parity);
+        }
         tc_fence_after();
         if (ok && elect_one()) {
 #pragma unroll
