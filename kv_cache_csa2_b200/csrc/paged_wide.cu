@@ -561,8 +561,8 @@ bool paged_wide_applies(const PagedAttn& a) {
 // A CTA per token pays when its heads fill most of the 64 and it sees several tiles;
 // else the 16-row tiles of paged_attn.cu, which take several tokens at once, are
 // faster.  Measured (us, here / there): 512 tokens behind 1000, 64 heads over one
-// 512-wide row, window 2048: 142 / 237; 1000 tokens, 64 heads over one 256-wide row:
-// 175 / 414; 512 behind 1000, 16 heads over one 512-wide row: 91 / 75; 60 tokens, 64
+// 512-wide row, window 2048: 113 / 237; 1000 tokens, 64 heads over one 256-wide row:
+// 161 / 414; 512 behind 1000, 16 heads over one 512-wide row: 91 / 75; 60 tokens, 64
 // heads, window 128: 39 / 26.
 bool paged_wide_prompt_applies(const PagedAttn& a) {
   const int64_t seen = a.window > 0 ? std::min<int64_t>(a.kv.capacity, static_cast<int64_t>(a.window) + a.sinks) : a.kv.capacity;
