@@ -62,6 +62,7 @@ csa2_status launch_paged_decode(const PagedAttn& a, int64_t max_len, int chunk, 
 // The decode launch for rows of up to 256 channels (paged_decode.cu); the caller
 // joins the chunks.
 bool paged_decode_stream_applies(const PagedAttn& a);
+int paged_decode_heads(const PagedAttn& a);          // query heads per CTA
 csa2_status launch_paged_decode_stream(const PagedAttn& a, int chunk, int chunks, float* part_o, float2* part_ml,
                                        cudaStream_t stream);
 // Tensor map of 16-bit cache rows as [page][slot][head][channel] with the 128-byte

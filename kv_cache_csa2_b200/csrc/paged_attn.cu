@@ -531,7 +531,8 @@ Split split_of(const PagedAttn& a, int64_t max_len, int chunk) {
     s.chunks = static_cast<int>((tiles + per - 1) / per);
     return s;
   }
-  const int64_t units = static_cast<int64_t>(a.kv.B) * a.kv.heads * ((a.G + 15) / 16);
+  const int nh = paged_decode_heads(a);
+  const int64_t units = static_cast<int64_t>(a.kv.B) * a.kv.heads * ((a.G + nh - 1) / nh);
   int64_t c = chunk;
   if (c == 0) {
     // two CTAs per SM, but no chunk above 2048 tokens, so that long and short

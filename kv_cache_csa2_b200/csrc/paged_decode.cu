@@ -1,6 +1,6 @@
 // Attention of one new token per sequence over a paged cache, rows of 64, 128 or
-// 256 channels: up to 16 query heads of one cache head per CTA, the sequence's
-// visible tokens cut into chunks over CTAs.
+// 256 channels, FP4 rows of 512 too: up to 16 query heads of one cache head per CTA, the
+// sequence's visible tokens cut into chunks over CTAs.
 //
 // HBM-bound: every cached row is read once and meets 16 query rows.  What counts
 // is bytes in flight, so every warp works alone: it streams its own slices of 16
@@ -28,7 +28,9 @@
 // an f32 at the largest.  Measured: 64 ragged sequences of up to 32768, window 8192 + 4,
 // 32 heads over 4 x 128 (209 MB, 32 us at the copy rate): heads as rows 108 us, this way
 // 79, chunks of 1024 tokens 74, bytes of a word by the conversion's own operand instead
-// of shifts 68, row addresses once for keys and values 65; four CTAs per SM.
+// of shifts 68, row addresses once for keys and values 65; four CTAs per SM.  Rows of 512
+// channels take 8 heads per CTA, so 64 heads decode a row 8 times: 32 sequences of 8192,
+// 64 heads over one row 282 us (16-row tiles of paged_attn.cu 653), 8 heads 48 (168).
 
 #include <algorithm>
 
@@ -50,7 +52,7 @@ struct Lay {
   static constexpr int ROW = FP4 ? D / 2 + 16 : 2 * D + 16;        // padded row in shared memory
   static constexpr int SC = FP4 ? KS * (D / 16) : 0;               // a slice's scales
   static constexpr int HALF = KS * ROW + SC;                       // keys (or values) of a slice
-  static constexpr int STAGES = FP4 ? (D <= 128 ? (HT == 1 ? 2 : 3) : 6) : D == 64 ? 6 : D == 128 ? 3 : 2;
+  static constexpr int STAGES = FP4 ? (D <= 128 ? (HT == 1 ? 2 : 3) : D == 256 ? 6 : 3) : D == 64 ? 6 : D == 128 ? 3 : 2;
   static constexpr int warp_bytes(bool shared) { return STAGES * HALF * (shared ? 1 : 2); }
   static constexpr int MERGE = kWarps * ROWS * (D + 4) * 4 + kWarps * ROWS * 8;
   static constexpr int bytes(bool shared) {
@@ -64,7 +66,7 @@ __device__ __forceinline__ void cp_async_4(uint32_t dst, const void* src, uint32
 __device__ __forceinline__ void cp_async_16s(uint32_t dst, const void* src, uint32_t n) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
 }
-// N words, or the N bytes of a word, from shared memory.
+// N words, or N bytes, from shared memory.
 template <int N>
 __device__ __forceinline__ void lds_words(uint32_t (&w)[N], uint32_t a) {
   if constexpr (N == 1) {
@@ -81,10 +83,9 @@ __device__ __forceinline__ void lds_words(uint32_t (&w)[N], uint32_t a) {
 }
 template <int N>
 __device__ __forceinline__ uint32_t lds_bytes(uint32_t a) {
-  uint32_t v;
+  uint32_t v = 0;
   if constexpr (N == 1) asm volatile("ld.shared.u8 %0, [%1];" : "=r"(v) : "r"(a));
   if constexpr (N == 2) asm volatile("ld.shared.u16 %0, [%1];" : "=r"(v) : "r"(a));
-  if constexpr (N == 4) asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(a));
   return v;
 }
 // Two E4M3 scales (the low bytes) as an f16 pair.
@@ -359,25 +360,29 @@ __global__ void __launch_bounds__(kThreads, FP4 && D <= 128 && HT == 1 ? 4 : 1) 
       for (int i = 0; i < MT; ++i) {
 #pragma unroll
         for (int h = 0; h < HT; ++h) sc[i][h][0] = sc[i][h][1] = sc[i][h][2] = sc[i][h][3] = 0.0f;
-        uint32_t w[2][NW], s2[2];                      // tokens n8 and n8 + 8
+        constexpr int NC = NW < 4 ? NW : 4;            // code words at a time
 #pragma unroll
-        for (int u = 0; u < 2; ++u) {
-          const int r = i * 16 + 8 * u + n8;
-          lds_words<NW>(w[u], kb + r * L::ROW + c4 * (D / 8));
-          s2[u] = lds_bytes<D / 64>(kb + KS * L::ROW + r * (D / 16) + c4 * (D / 64));
-        }
+        for (int j0 = 0; j0 < NW; j0 += NC) {
+          uint32_t w[2][NC], s2[2];                    // tokens n8 and n8 + 8
 #pragma unroll
-        for (int j = 0; j < NW; ++j) {
-          uint32_t s[2];                               // the scale of word j's block, twice
+          for (int u = 0; u < 2; ++u) {
+            const int r = i * 16 + 8 * u + n8;
+            lds_words<NC>(w[u], kb + r * L::ROW + c4 * (D / 8) + 4 * j0);
+            s2[u] = scales_f16(lds_bytes<NC / 2>(kb + KS * L::ROW + r * (D / 16) + c4 * (D / 64) + j0 / 2));
+          }
 #pragma unroll
-          for (int u = 0; u < 2; ++u)
-            s[u] = __byte_perm(scales_f16(s2[u] >> (16 * (j / 4))), 0u, (j / 2) & 1 ? 0x3232 : 0x1010);
+          for (int j = 0; j < NC; ++j) {
+            uint32_t s[2];                             // the scale of word j's block, twice
 #pragma unroll
-          for (int x = 0; x < 2; ++x) {
-            const uint32_t a[4] = {code_pair(w[0][j], 2 * x, s[0]), code_pair(w[1][j], 2 * x, s[1]),
-                                   code_pair(w[0][j], 2 * x + 1, s[0]), code_pair(w[1][j], 2 * x + 1, s[1])};
+            for (int u = 0; u < 2; ++u) s[u] = __byte_perm(s2[u], 0u, (j / 2) & 1 ? 0x3232 : 0x1010);
 #pragma unroll
-            for (int h = 0; h < HT; ++h) mma16816<M>(sc[i][h], a, qb[h][2 * j + x][0], qb[h][2 * j + x][1]);
+            for (int x = 0; x < 2; ++x) {
+              const uint32_t a[4] = {code_pair(w[0][j], 2 * x, s[0]), code_pair(w[1][j], 2 * x, s[1]),
+                                     code_pair(w[0][j], 2 * x + 1, s[0]), code_pair(w[1][j], 2 * x + 1, s[1])};
+#pragma unroll
+              for (int h = 0; h < HT; ++h)
+                mma16816<M>(sc[i][h], a, qb[h][2 * (j0 + j) + x][0], qb[h][2 * (j0 + j) + x][1]);
+            }
           }
         }
       }
@@ -438,36 +443,40 @@ __global__ void __launch_bounds__(kThreads, FP4 && D <= 128 && HT == 1 ? 4 : 1) 
       // the codes of two tokens are paired before they are converted
 #pragma unroll
       for (int t = 0; t < MT; ++t) {
-        uint32_t ev[2][W], od[2][W], s[2][W / 4 + 1];
+        constexpr int WC = W < 4 ? W : 4;              // words at a time
 #pragma unroll
-        for (int u = 0; u < 2; ++u) {
-          const int r = t * 16 + 8 * u + 2 * c4;
-          uint32_t x[W], y[W];
-          lds_words<W>(x, vb + r * L::ROW + n8 * (4 * W));
-          lds_words<W>(y, vb + (r + 1) * L::ROW + n8 * (4 * W));
-          constexpr int SN = W == 4 ? 2 : 1;           // scale bytes of a thread
-          const uint32_t at = vb + KS * L::ROW + r * (D / 16) + (W == 1 ? n8 >> 1 : n8 * SN);
-          const uint32_t sx = lds_bytes<SN>(at), sy = lds_bytes<SN>(at + D / 16);
-          s[u][0] = scales_f16(__byte_perm(sx, sy, 0x0040));
-          if (SN == 2) s[u][W / 4] = scales_f16(__byte_perm(sx, sy, 0x0051));
-#pragma unroll
-          for (int j = 0; j < W; ++j) {
-            ev[u][j] = (x[j] & 0x0f0f0f0fu) | ((y[j] << 4) & 0xf0f0f0f0u);
-            od[u][j] = ((x[j] >> 4) & 0x0f0f0f0fu) | (y[j] & 0xf0f0f0f0u);
-          }
-        }
-#pragma unroll
-        for (int i = 0; i < D / 16; ++i) {             // channel i of the lower, of the upper rows
-          const int c = W == 1 ? i : i & 7, j = W == 1 ? 0 : 2 * (i / 8), jh = W == 1 ? 0 : j + 1;
-          const int kl = c / 2, kh = W == 1 ? 2 + c / 2 : c / 2;
-          uint32_t a[4];
+        for (int w0 = 0; w0 < W; w0 += WC) {
+          constexpr int SN = WC == 4 ? 2 : 1;          // their scale bytes
+          uint32_t ev[2][WC], od[2][WC], s[2][SN];
 #pragma unroll
           for (int u = 0; u < 2; ++u) {
-            a[2 * u] = code_pair(c & 1 ? od[u][j] : ev[u][j], kl, s[u][i / 8 * (W / 4)]);
-            a[2 * u + 1] = code_pair(c & 1 ? od[u][jh] : ev[u][jh], kh, s[u][i / 8 * (W / 4)]);
+            const int r = t * 16 + 8 * u + 2 * c4;
+            uint32_t x[WC], y[WC];
+            lds_words<WC>(x, vb + r * L::ROW + n8 * (4 * W) + 4 * w0);
+            lds_words<WC>(y, vb + (r + 1) * L::ROW + n8 * (4 * W) + 4 * w0);
+            const uint32_t at = vb + KS * L::ROW + r * (D / 16) + (n8 * W + w0) / 2;
+            const uint32_t sx = lds_bytes<SN>(at), sy = lds_bytes<SN>(at + D / 16);
+            s[u][0] = scales_f16(__byte_perm(sx, sy, 0x0040));
+            if (SN == 2) s[u][SN - 1] = scales_f16(__byte_perm(sx, sy, 0x0051));
+#pragma unroll
+            for (int j = 0; j < WC; ++j) {
+              ev[u][j] = (x[j] & 0x0f0f0f0fu) | ((y[j] << 4) & 0xf0f0f0f0u);
+              od[u][j] = ((x[j] >> 4) & 0x0f0f0f0fu) | (y[j] & 0xf0f0f0f0u);
+            }
           }
 #pragma unroll
-          for (int h = 0; h < HT; ++h) mma16816<M>(o[HT * i + h], a, pb[t][h][0], pb[t][h][1]);
+          for (int i = 0; i < 4 * WC; ++i) {           // channel i of the lower, of the upper rows
+            const int c = W == 1 ? i : i & 7, j = W == 1 ? 0 : 2 * (i / 8), jh = W == 1 ? 0 : j + 1;
+            const int kl = c / 2, kh = W == 1 ? 2 + c / 2 : c / 2;
+            uint32_t a[4];
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+              a[2 * u] = code_pair(c & 1 ? od[u][j] : ev[u][j], kl, s[u][SN == 2 ? i / 8 : 0]);
+              a[2 * u + 1] = code_pair(c & 1 ? od[u][jh] : ev[u][jh], kh, s[u][SN == 2 ? i / 8 : 0]);
+            }
+#pragma unroll
+            for (int h = 0; h < HT; ++h) mma16816<M>(o[HT * (4 * w0 + i) + h], a, pb[t][h][0], pb[t][h][1]);
+          }
         }
       }
     }
@@ -574,7 +583,10 @@ csa2_status run(const Params& p, dim3 grid, cudaStream_t stream) {
 
 }  // namespace
 
-bool paged_decode_stream_applies(const PagedAttn& a) { return a.D <= 256; }
+// FP4 rows under up to 8 heads take products of 8 columns; 512 channels have registers
+// for no more.  16-bit rows have 16 query rows either way.
+int paged_decode_heads(const PagedAttn& a) { return a.fmt == CSA2_KV_FP4 && (a.G <= 8 || a.D == 512) ? 8 : 16; }
+bool paged_decode_stream_applies(const PagedAttn& a) { return a.D <= 256 || a.fmt == CSA2_KV_FP4; }
 
 csa2_status launch_paged_decode_stream(const PagedAttn& a, int chunk, int chunks, float* part_o, float2* part_ml,
                                        cudaStream_t stream) {
@@ -589,9 +601,7 @@ csa2_status launch_paged_decode_stream(const PagedAttn& a, int chunk, int chunks
   p.scale2 = a.scale * kLog2e;
   p.Hq = a.Hq;
   p.G = a.G;
-  // FP4 rows under up to 8 heads take products of 8 (the code conversion is then all
-  // that is left of the work per token); 16-bit rows have 16 query rows either way
-  const int ht = a.fmt == CSA2_KV_FP4 && a.G <= 8 ? 1 : 2;
+  const int ht = paged_decode_heads(a) / 8;
   p.row_tiles = (a.G + 8 * ht - 1) / (8 * ht);
   p.window = a.window;
   p.sinks = a.sinks;
@@ -608,6 +618,7 @@ csa2_status launch_paged_decode_stream(const PagedAttn& a, int chunk, int chunks
            : a.fmt == CSA2_KV_F16 ? CSA2_STREAM_T(__half, D_, false, 2)                       \
                                   : CSA2_STREAM_T(__nv_bfloat16, D_, false, 2);
   CSA2_STREAM(64) CSA2_STREAM(128) CSA2_STREAM(256)
+  if (a.D == 512) return CSA2_STREAM_T(__nv_bfloat16, 512, true, 1);
 #undef CSA2_STREAM
 #undef CSA2_STREAM_T
   return CSA2_ERR_UNSUPPORTED;

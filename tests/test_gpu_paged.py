@@ -225,7 +225,7 @@ def test_decode_huge_scores_and_identical_keys():
         assert np.all(np.abs(P.f64(out[b]) - mean) <= P.half_step(torch.bfloat16) * (np.abs(mean) + 1.02 * mag) + 2e-5 * mag)
 
 
-@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("D", [64, 128, 256, 512])
 @pytest.mark.parametrize("G", [1, 5, 8, 9, 16, 17])
 @pytest.mark.parametrize("shared,window,sinks,sign", [(False, 0, 0, 1.0), (True, 150, 5, -1.0)])
 def test_decode_fp4_groups_and_magnitudes(D, G, shared, window, sinks, sign):
