@@ -59,7 +59,7 @@ struct PagedAttn {
 size_t paged_decode_workspace(const PagedAttn& a, int64_t max_len, int chunk);
 csa2_status launch_paged_decode(const PagedAttn& a, int64_t max_len, int chunk, void* ws,
                                 cudaStream_t stream);
-// The decode launch for rows of up to 256 channels (paged_decode.cu); the caller
+// The decode launch for rows of up to 256 channels, FP4 of 512 (paged_decode.cu); the caller
 // joins the chunks.
 bool paged_decode_stream_applies(const PagedAttn& a);
 int paged_decode_heads(const PagedAttn& a);          // query heads per CTA
