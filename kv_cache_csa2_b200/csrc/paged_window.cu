@@ -727,6 +727,9 @@ __global__ void __launch_bounds__(kThreads, 1) paged_window_kernel(const Params 
     if (any && ok) {
       ok = wait_phase(all_done + w, 0, abort_flag, p.kv.err);
       tc_fence_after();
+    } else if (ok) {
+      // no product has waited for q, which lands where the outputs pass through
+      ok = wait_phase(q_full, 0, abort_flag, p.kv.err);
     }
     if (ok) {
       const float sum = l.x + l.y;

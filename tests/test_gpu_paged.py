@@ -560,6 +560,20 @@ def test_two_graphs_interleaved_and_two_streams():
             assert torch.equal(o, wo) and torch.equal(l, wl)
 
 
+@pytest.mark.parametrize("G,D", [(4, 64), (8, 128), (3, 128)])
+def test_window_rows_that_see_nothing(G, D):
+    """Many row tiles without a key: zeros, whatever q holds (it lands late in shared memory)."""
+    B, n = 64, 96
+    k = torch.zeros(4, 16, 2, D, dtype=torch.bfloat16, device="cuda")
+    cache = K.PagedKv(k, torch.zeros(B, 2, dtype=torch.int32, device="cuda"), torch.zeros(B, dtype=torch.int32, device="cuda"),
+                      v=torch.ones_like(k))
+    cu = torch.arange(0, B * n + 1, n, dtype=torch.int32, device="cuda")
+    q = torch.ones(B * n, 2 * G, D, dtype=torch.bfloat16, device="cuda")
+    for _ in range(5):
+        out, lse = K.csa2_paged_window_attn(q, cu, cache, 1.0)
+        assert torch.all(out == 0) and torch.all(torch.isneginf(lse))
+
+
 def test_empty_batches_do_nothing():
     k = torch.zeros(4, 16, 2, 64, dtype=torch.bfloat16, device="cuda")
     none = torch.zeros(0, dtype=torch.int32, device="cuda")
