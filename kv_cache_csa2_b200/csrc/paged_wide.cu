@@ -563,11 +563,12 @@ bool paged_wide_applies(const PagedAttn& a) {
 // faster.  Measured (us, here / there): 512 tokens behind 1000, 64 heads over one
 // 512-wide row, window 2048: 113 / 237; 1000 tokens, 64 heads over one 256-wide row:
 // 161 / 414; 512 behind 1000, 16 heads over one 512-wide row: 91 / 75; 60 tokens, 64
-// heads, window 128: 39 / 26.
+// heads, window 128: 39 / 26.  The two round differently, so the rule takes what belongs
+// to the layer (format, pages, width, heads, window) and not the table's width or a
+// batch's lengths: a query's bits stay the same when its table grows.
 bool paged_wide_prompt_applies(const PagedAttn& a) {
-  const int64_t seen = a.window > 0 ? std::min<int64_t>(a.kv.capacity, static_cast<int64_t>(a.window) + a.sinks) : a.kv.capacity;
   return a.fmt != CSA2_KV_FP4 && a.kv.page_shift >= 3 && a.kv.n_pages > 0 && (a.D == 512 || a.D == 256) && a.G >= 32 &&
-         seen >= 512;
+         (a.window == 0 || static_cast<int64_t>(a.window) + a.sinks >= 512);
 }
 
 namespace {
