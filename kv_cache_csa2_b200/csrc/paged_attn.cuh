@@ -26,6 +26,11 @@ __device__ __forceinline__ float exp2_approx(float x) {
   return y;
 }
 
+// The reference that weights 2^(s - reference) of a row with maximum m are taken from, so that
+// the largest is 2^lift.  From 2^22 on m - lift would round by more than the half step by
+// which 2^15 stays finite in f16; there a score's own steps hide what the lift is for.
+__device__ __forceinline__ float lifted(float m, float lift) { return fabsf(m) < 4194304.0f ? m - lift : m; }
+
 __device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t a) {
   asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
                : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(a));

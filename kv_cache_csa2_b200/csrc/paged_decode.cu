@@ -127,7 +127,8 @@ __global__ void __launch_bounds__(kThreads, FP4 && D <= 128 && HT == 1 ? 4 : 1) 
   using L = Lay<D, FP4, HT>;
   using M = typename std::conditional<FP4, __half, T>::type;       // type of the products
   // weights in f16 stand 2^15 above the largest's 1, so that they keep 11 bits down to
-  // 2^-29 of it (f16's last step would else be 2^-24)
+  // 2^-29 of it (f16's last step would else be 2^-24); sums, outputs and references all
+  // count in these lifted units
   constexpr float LIFT = std::is_same<M, __half>::value ? 15.0f : 0.0f;
   constexpr int KS = L::KS;
   extern __shared__ __align__(16) uint8_t smem[];
@@ -315,8 +316,8 @@ __global__ void __launch_bounds__(kThreads, FP4 && D <= 128 && HT == 1 ? 4 : 1) 
         mx[u] = fmaxf(mx[u], __shfl_xor_sync(0xffffffffu, mx[u], 1));
         mx[u] = fmaxf(mx[u], __shfl_xor_sync(0xffffffffu, mx[u], 2));
         const float mn = fmaxf(m[0][u], mx[u]);
-        const float top = mn == -INFINITY ? 0.0f : mn, ref = top - LIFT;
-        alpha[u] = exp2_approx(m[0][u] - top);
+        const float ref = mn == -INFINITY ? 0.0f : lifted(mn, LIFT);
+        alpha[u] = exp2_approx(lifted(m[0][u], LIFT) - ref);
         m[0][u] = mn;
         l[0][u] *= alpha[u];
 #pragma unroll
@@ -414,8 +415,8 @@ __global__ void __launch_bounds__(kThreads, FP4 && D <= 128 && HT == 1 ? 4 : 1) 
 #pragma unroll
           for (int x = 4; x < 32; x *= 2) mx[u] = fmaxf(mx[u], __shfl_xor_sync(0xffffffffu, mx[u], x));
           const float mn = fmaxf(m[h][u], mx[u]);
-          const float top = mn == -INFINITY ? 0.0f : mn, ref = top - LIFT;
-          alpha[h][u] = exp2_approx(m[h][u] - top);
+          const float ref = mn == -INFINITY ? 0.0f : lifted(mn, LIFT);
+          alpha[h][u] = exp2_approx(lifted(m[h][u], LIFT) - ref);
           moved |= alpha[h][u] != 1.0f;
           m[h][u] = mn;
           l[h][u] *= alpha[h][u];
@@ -498,7 +499,7 @@ __global__ void __launch_bounds__(kThreads, FP4 && D <= 128 && HT == 1 ? 4 : 1) 
 #pragma unroll
       for (int i = 0; i < D / 8; ++i)
         *reinterpret_cast<float2*>(dst + i * 8 + c4 * 2) = make_float2(o[i][2 * u], o[i][2 * u + 1]);
-      if (c4 == 0) sml[warp * L::ROWS + r] = make_float2(m[0][u] - LIFT, l[0][u]);
+      if (c4 == 0) sml[warp * L::ROWS + r] = make_float2(lifted(m[0][u], LIFT), l[0][u]);
     }
   } else {
 #pragma unroll
@@ -516,7 +517,7 @@ __global__ void __launch_bounds__(kThreads, FP4 && D <= 128 && HT == 1 ? 4 : 1) 
             *reinterpret_cast<float4*>(dst + (W == 1 ? 4 * e : 16 * (i / 8) + 8 * e + (i & 7))) =
                 make_float4(o[HT * i + h][2 * e + u], o[HT * (i + 1) + h][2 * e + u], o[HT * (i + 2) + h][2 * e + u],
                             o[HT * (i + 3) + h][2 * e + u]);
-        if (n8 == 0) sml[warp * L::ROWS + r] = make_float2(m[h][u] - LIFT, l[h][u]);
+        if (n8 == 0) sml[warp * L::ROWS + r] = make_float2(lifted(m[h][u], LIFT), l[h][u]);
       }
   }
   __syncthreads();

@@ -1,5 +1,6 @@
 """Paged-cache calls in forms that the operator-by-operator tests leave out: tables wider than
-the sequences."""
+the sequences, and scores of any size.  Bounds as in paged_util, but no test here allows f16
+weights a fixed step."""
 import numpy as np
 import pytest
 import torch
@@ -21,6 +22,32 @@ def _ints(*x):
     return torch.tensor(x, dtype=torch.int32, device="cuda")
 
 
+def _check_relative(out, lse, want, q, keys, scale, dt, tokens, what=""):
+    """paged_util's bound with every weight rounded by half a step relative to itself; 2^-25 is the
+    half step of an f16 output below 2^-14."""
+    o, s, mag = want
+    u = P.half_step(dt)
+    ka = np.abs(keys).max(0).repeat(q.shape[1] // keys.shape[1], 0)
+    ds = (q.shape[2] + 8) * 2.0 ** -24 * scale * (np.abs(q) * ka[None]).sum(-1)
+    rel = 2 * ds + 2.0 ** -20 + (tokens / 8 + 64) * 2.0 ** -23 + u * 1.01
+    tol = rel[..., None] * mag + u * np.abs(o) + (2.0 ** -25 if dt == torch.float16 else 0.0)
+    err = np.abs(P.f64(out) - o)
+    assert np.all(err <= tol), f"{what}: out off by {(err / tol).max():.3g} times its bound"
+    ltol = ds + (tokens / 8 + 64) * 2.0 ** -24 + 2.0 ** -20 + 2.0 ** -22 * np.abs(s)
+    assert np.all(np.abs(P.f64(lse) - s) <= ltol), f"{what}: lse"
+
+
+def _paged(rows, page, seed=0):
+    """Rows [n, heads, D] of one sequence as pages in random order, and the table's row."""
+    n, heads, D = rows.shape
+    need = -(-n // page)
+    perm = torch.randperm(need, generator=torch.Generator().manual_seed(seed))
+    pages = torch.full((need, page, heads, D), float("nan"), dtype=rows.dtype, device="cuda")
+    full = torch.cat([rows, torch.full((need * page - n, heads, D), float("nan"), dtype=rows.dtype, device="cuda")])
+    pages[perm.cuda()] = full.view(need, page, heads, D)
+    return pages, perm.int().cuda()
+
+
 # ------------------------------------------------------------------ bits
 
 @pytest.mark.parametrize("kind,D,G,page,window,sinks", [("bf16", 512, 64, 16, 0, 0), ("f16", 512, 33, 64, 0, 0),
@@ -40,3 +67,76 @@ def test_window_bits_do_not_depend_on_the_tables_width(kind, D, G, page, window,
     assert torch.equal(got[0][0], got[1][0]) and torch.equal(got[0][1], got[1][1])
     want = O.causal_attn(P.f64(q), np.arange(300), *host[0], D ** -0.5, window, sinks)
     P.check_attn(*got[0], want, P.f64(q), host[0][0], D ** -0.5, cache.dtype, 300)
+
+
+# ------------------------------------------------------------------ scores of any size
+
+@pytest.mark.parametrize("low,offset", [(float("-inf"), 300.0), (-65504.0, 0.0)])
+@pytest.mark.parametrize("D,G,page", [(64, 8, 16), (128, 4, 64), (256, 2, 16), (512, 3, 4)])
+@pytest.mark.parametrize("prompt", [False, True])
+def test_first_tokens_that_weigh_nothing(D, G, page, low, offset, prompt):
+    """The first 140 tokens score -inf (the rest about -300) or 10^8 below the rest: the answer is the
+    softmax over the rest, to the precision of the rest's scores."""
+    L, T, scale, dt = 700, 12 if prompt else 1, D ** -0.5, torch.float16
+    g = torch.Generator(device="cuda").manual_seed(23)
+    k = torch.randn(L, 1, D, generator=g, device="cuda")
+    k[..., 0] = 0
+    k[..., 1] = -8.0
+    k[:140, :, 0] = low
+    k = k.half()
+    v = torch.randn(L, 1, D, generator=g, device="cuda").half()
+    q = torch.randn(T, G, D, generator=g, device="cuda") * 0.5
+    q[..., 0] = 30000.0
+    q[..., 1] = offset / (8.0 * scale)
+    q = q.half()
+    kp, table = _paged(k, page)
+    vp, _ = _paged(v, page)
+    cache = K.PagedKv(kp, table[None], _ints(L), v=vp)
+    if prompt:
+        out, lse = K.csa2_paged_window_attn(q, _ints(0, T), cache, scale)
+    else:
+        out, lse = K.csa2_paged_decode_attn(q, cache, scale)
+    qh, kh = P.f64(q), P.f64(k[140:])
+    want = O.causal_attn(qh, np.arange(L - 140 - T, L - 140), kh, P.f64(v[140:]), scale)
+    _check_relative(out, lse, want, qh, kh, scale, dt, L)
+
+
+@pytest.mark.parametrize("size", [0, 20, 22, 23, 24, 26])
+@pytest.mark.parametrize("kind", ["bf16", "f16", "fp4"])
+@pytest.mark.parametrize("D,G,page", [(64, 8, 16), (128, 3, 64), (256, 2, 16), (512, 2, 4)])
+def test_equal_scores_of_any_size(kind, D, G, page, size):
+    """Tokens with the same key weigh the same, however large its score (1.37 * 2^size in base 2, both
+    signs): the answer is the mean of the values.  Every token's score is one and the same number, so
+    its error leaves the weights alone and shows in lse only."""
+    n, T, scale = 700, 9, D ** -0.5
+    top = 2688.0 if kind == "fp4" else 32768.0
+    dt = P.DT[kind]
+    k = torch.zeros(n, 1, D, device="cuda")
+    k[..., 0] = top
+    v = P.rng_normal(27, n, 1, D, dt=dt) + 1
+    kp, table = _paged(k.to(dt), page)
+    vp, _ = _paged(v, page)
+    sc = [None, None]
+    if kind == "fp4":
+        kp, vp = torch.nan_to_num(kp), torch.nan_to_num(vp)
+        (kp, sc[0]), (vp, sc[1]) = K.csa2_fp4_pack(kp), K.csa2_fp4_pack(vp)
+        v = K.csa2_fp4_unpack(vp, sc[1])[table.long()].flatten(0, 1)[:n]
+    cache = K.PagedKv(kp, table[None], _ints(n), v=vp, k_scales=sc[0], v_scales=sc[1])
+    q = torch.zeros(T, G, D, device="cuda")
+    q[..., 0] = 1.37 * 2.0 ** size / (scale * top * np.log2(np.e))
+    q[:, ::2] *= -1
+    q = q.to(dt)
+    u, vh = P.half_step(dt), P.f64(v)[:, 0]
+    score = P.f64(q)[..., 0] * top * scale
+    def check(out, lse, at, seen):
+        mean, mag = vh[:seen].mean(0), np.abs(vh[:seen]).mean(0)
+        tol = (2.0 ** -20 + (n / 8 + 64) * 2.0 ** -23 + u * 1.01) * mag + u * np.abs(mean) + 2.0 ** -25
+        assert np.all(np.abs(P.f64(out) - mean) <= tol), f"token {at}"
+        want = score[at] + np.log(seen)
+        assert np.all(np.abs(P.f64(lse) - want) <= 2.0 ** -15 + 2.0 ** -21 * np.abs(want)), f"token {at}: lse"
+
+    out, lse = K.csa2_paged_decode_attn(q[:1], cache, scale)
+    check(out[0], lse[0], 0, n)
+    out, lse = K.csa2_paged_window_attn(q, _ints(0, T), cache, scale)
+    for t in range(T):
+        check(out[t], lse[t], t, n - T + 1 + t)
