@@ -58,7 +58,7 @@ struct Lay {
   static constexpr int RING = 0;
   static constexpr int Q = RING + SLOTS * BLK;
   static constexpr int P = Q + DB * QB;                // [128 keys][64 heads]
-  static constexpr int REF = P + BLK;                  // -reference[NH], shift[NH]
+  static constexpr int REF = P + BLK;                  // -reference[NH], factor[NH]
   static constexpr int RED = REF + 2 * NH * 4;         // [4][NH]
   static constexpr int BAR = RED + 4 * NH * 4;
   static constexpr int NBAR = 2 * SLOTS + 3 + kLoaders;
@@ -114,7 +114,7 @@ __global__ void __launch_bounds__(Lay<D, NH>::THREADS, 1)
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + L::MISC);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + L::MISC + 4);
   float* ref = reinterpret_cast<float*>(smem + L::REF);
-  float* shift = ref + NH;
+  float* factor = ref + NH;
   float* red = reinterpret_cast<float*>(smem + L::RED);
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -364,66 +364,72 @@ __global__ void __launch_bounds__(Lay<D, NH>::THREADS, 1)
     if (threadIdx.x < NH) ref[threadIdx.x] = 0.0f;     // -reference: none so far
     bar_of<N>();
     const float4* const mine = reinterpret_cast<const float4*>(ref + hb);
-    bool ok = true, started = false;                   // started: some key was seen
+    bool ok = true, started = false;                   // started: every head has a reference
+    bool set = false;                                  // head threadIdx.x has one
     for (int tile = 0; tile < tiles && ok; ++tile) {
       ok = wait(s_full, tile & 1);
       tc_fence_after();
       float x[HW];
-      if (ok) {
-        if constexpr (HW == 32) {
-          tmem_ld32(s_at, *reinterpret_cast<uint32_t(*)[32]>(x));
-        } else {
-          tmem_ld16(s_at, *reinterpret_cast<uint32_t(*)[16]>(x));
-        }
+      auto scores = [&]() {
+        tmem_ld16(s_at, *reinterpret_cast<uint32_t(*)[16]>(x));
         tmem_wait_ld();
-      }
+      };
+      if (ok) scores();
       const int j = at.start(first + tile) + key;
       const uint32_t here = *reinterpret_cast<volatile uint32_t*>(bits + (tile % kBits) * 4 + (warp & 3));
       const bool seen = ok && j <= at.pmax && (j >= at.lo || j < at.ns) && ((here >> lane) & 1u);
-      // x - reference; a key that is not seen weighs nothing
+      // x - reference, rounded once, and the largest; a key that is not seen weighs nothing
       const float2 sc = make_float2(p.scale2, p.scale2);
-      float top = -INFINITY;
+      auto refer = [&]() -> float {
+        float top = -INFINITY;
 #pragma unroll
-      for (int h = 0; h < HW; h += 4) {
-        const float4 r = mine[h / 4];
-        const float2 a = fma2(make_float2(x[h], x[h + 1]), sc, make_float2(r.x, r.y));
-        const float2 c = fma2(make_float2(x[h + 2], x[h + 3]), sc, make_float2(r.z, r.w));
-        x[h] = seen ? a.x : -INFINITY;
-        x[h + 1] = seen ? a.y : -INFINITY;
-        x[h + 2] = seen ? c.x : -INFINITY;
-        x[h + 3] = seen ? c.y : -INFINITY;
-        top = max3(top, x[h], x[h + 1]);
-        top = max3(top, x[h + 2], x[h + 3]);
-      }
+        for (int h = 0; h < HW; h += 4) {
+          const float4 r = mine[h / 4];
+          const float2 a = fma2(make_float2(x[h], x[h + 1]), sc, make_float2(r.x, r.y));
+          const float2 c = fma2(make_float2(x[h + 2], x[h + 3]), sc, make_float2(r.z, r.w));
+          x[h] = seen ? a.x : -INFINITY;
+          x[h + 1] = seen ? a.y : -INFINITY;
+          x[h + 2] = seen ? c.x : -INFINITY;
+          x[h + 3] = seen ? c.y : -INFINITY;
+          top = max3(top, x[h], x[h + 1]);
+          top = max3(top, x[h + 2], x[h + 3]);
+        }
+        return top;
+      };
+      const float top = refer();
       if (any_of<N>(!started || !ok || top > kLazy)) {
         if (any_of<N>(!ok)) {                          // all leave together
           ok = false;
           break;
         }
-        // every head's maximum over the tile; the heads that outgrew their reference
-        // move to it (on the first tile that shows anything, all of them)
-        const bool first_seen = !started && any_of<N>(seen);
+        // every head's maximum over the tile; the heads that outgrew their reference, or
+        // have none and see a score above -inf, move to it.  The scores are then taken
+        // from the new one: what a far reference rounded away is not in x any more.
+        scores();
 #pragma unroll
         for (int h = 0; h < HW; ++h) {
-          const float m = attn::warp_max_f32(x[h]);
+          const float m = attn::warp_max_f32(seen ? x[h] * p.scale2 : -INFINITY);
           if (lane == 0) red[(warp & 3) * NH + hb + h] = m;
         }
         bar_of<N>();
         if (threadIdx.x < NH) {
           const int h = threadIdx.x;
           const float m = fmaxf(fmaxf(red[h], red[NH + h]), fmaxf(red[2 * NH + h], red[3 * NH + h]));
-          shift[h] = m > kLazy || (first_seen && m > -INFINITY) ? m : 0.0f;
-          ref[h] -= shift[h];
+          const float was = ref[h];
+          const bool move = set ? m + was > kLazy : m > -INFINITY;
+          if (move) ref[h] = -m;
+          factor[h] = move && set ? exp2_approx(-m - was) : 1.0f;   // nothing weighed before: nothing to rescale
+          set |= move;
         }
-        bar_of<N>();
+        started = !any_of<N>(threadIdx.x < rows && !set);
+        scores();
+        refer();
 #pragma unroll
-        for (int h = 0; h < HW; ++h) x[h] -= shift[hb + h];
-        if (started) {
-#pragma unroll
-          for (int h = 0; h < HW; h += 2) {
-            l[h / 2].x *= exp2_approx(-shift[hb + h]);
-            l[h / 2].y *= exp2_approx(-shift[hb + h + 1]);
-          }
+        for (int h = 0; h < HW; h += 2) {
+          l[h / 2].x *= factor[hb + h];
+          l[h / 2].y *= factor[hb + h + 1];
+        }
+        if (tile > 0) {
           // the value products of the tile before ended before this tile's scores did
 #pragma unroll 1
           for (int i = 0; i < D / 128 * (HW / 16); ++i) {
@@ -433,13 +439,11 @@ __global__ void __launch_bounds__(Lay<D, NH>::THREADS, 1)
             tmem_ld16(to, v);
             tmem_wait_ld();
 #pragma unroll
-            for (int e = 0; e < 16; ++e)
-              v[e] = __float_as_uint(__uint_as_float(v[e]) * exp2_approx(-shift[hb + c + e]));
+            for (int e = 0; e < 16; ++e) v[e] = __float_as_uint(__uint_as_float(v[e]) * factor[hb + c + e]);
             tmem_st16(to, v);
           }
           tmem_wait_st();
         }
-        started |= first_seen;
       }
       uint8_t* const prow = smem + L::P;
 #pragma unroll
@@ -478,7 +482,7 @@ __global__ void __launch_bounds__(Lay<D, NH>::THREADS, 1)
         s2 += sums[(i + 2) * (NH + 1) + h];
         s3 += sums[(i + 3) * (NH + 1) + h];
       }
-      shift[h] = tiles > 0 ? (s0 + s1) + (s2 + s3) : 0.0f;             // l
+      factor[h] = tiles > 0 ? (s0 + s1) + (s2 + s3) : 0.0f;            // l
     }
     bar_of<N>();
     const int64_t row0 = static_cast<int64_t>(token) * p.Hq + kvh * p.G + h0;
@@ -499,7 +503,7 @@ __global__ void __launch_bounds__(Lay<D, NH>::THREADS, 1)
         if (partial) {
           p.part_o[(row * p.chunks + chunk) * D + db * 128 + key] = o;
         } else {
-          const float s = shift[c + e];
+          const float s = factor[c + e];
           const float inv = s > 0.0f ? 1.0f / s : (s == 0.0f ? 0.0f : s);
           p.out[row * D + db * 128 + key] = static_cast<uint16_t>(Num<T>::down(o * inv, 0.0f) & 0xffffu);
         }
@@ -507,7 +511,7 @@ __global__ void __launch_bounds__(Lay<D, NH>::THREADS, 1)
     }
     if (threadIdx.x < rows && ok) {
       const int h = threadIdx.x;
-      const float s = shift[h], m = -ref[h];
+      const float s = factor[h], m = -ref[h];
       if (partial)
         p.part_ml[(row0 + h) * p.chunks + chunk] = make_float2(s == 0.0f ? -INFINITY : m, s);
       else if (p.lse)

@@ -72,9 +72,10 @@ def test_window_bits_do_not_depend_on_the_tables_width(kind, D, G, page, window,
 # ------------------------------------------------------------------ scores of any size
 
 @pytest.mark.parametrize("low,offset", [(float("-inf"), 300.0), (-65504.0, 0.0)])
-@pytest.mark.parametrize("D,G,page", [(64, 8, 16), (128, 4, 64), (256, 2, 16), (512, 3, 4)])
-@pytest.mark.parametrize("prompt", [False, True])
-def test_first_tokens_that_weigh_nothing(D, G, page, low, offset, prompt):
+@pytest.mark.parametrize("D,G,page", [(64, 8, 16), (128, 4, 64), (256, 2, 16), (256, 40, 16), (512, 4, 16), (512, 16, 64),
+                                      (512, 64, 64), (512, 3, 4)])
+@pytest.mark.parametrize("prompt,chunk", [(True, 0), (False, 0), (False, 768)])
+def test_first_tokens_that_weigh_nothing(D, G, page, low, offset, prompt, chunk):
     """The first 140 tokens score -inf (the rest about -300) or 10^8 below the rest: the answer is the
     softmax over the rest, to the precision of the rest's scores."""
     L, T, scale, dt = 700, 12 if prompt else 1, D ** -0.5, torch.float16
@@ -95,7 +96,7 @@ def test_first_tokens_that_weigh_nothing(D, G, page, low, offset, prompt):
     if prompt:
         out, lse = K.csa2_paged_window_attn(q, _ints(0, T), cache, scale)
     else:
-        out, lse = K.csa2_paged_decode_attn(q, cache, scale)
+        out, lse = K.csa2_paged_decode_attn(q, cache, scale, chunk=chunk)
     qh, kh = P.f64(q), P.f64(k[140:])
     want = O.causal_attn(qh, np.arange(L - 140 - T, L - 140), kh, P.f64(v[140:]), scale)
     _check_relative(out, lse, want, qh, kh, scale, dt, L)
@@ -103,7 +104,8 @@ def test_first_tokens_that_weigh_nothing(D, G, page, low, offset, prompt):
 
 @pytest.mark.parametrize("size", [0, 20, 22, 23, 24, 26])
 @pytest.mark.parametrize("kind", ["bf16", "f16", "fp4"])
-@pytest.mark.parametrize("D,G,page", [(64, 8, 16), (128, 3, 64), (256, 2, 16), (512, 2, 4)])
+@pytest.mark.parametrize("D,G,page", [(64, 8, 16), (128, 3, 64), (256, 2, 16), (256, 40, 16), (512, 4, 16), (512, 64, 64),
+                                      (512, 2, 4)])
 def test_equal_scores_of_any_size(kind, D, G, page, size):
     """Tokens with the same key weigh the same, however large its score (1.37 * 2^size in base 2, both
     signs): the answer is the mean of the values.  Every token's score is one and the same number, so
@@ -135,8 +137,9 @@ def test_equal_scores_of_any_size(kind, D, G, page, size):
         want = score[at] + np.log(seen)
         assert np.all(np.abs(P.f64(lse) - want) <= 2.0 ** -15 + 2.0 ** -21 * np.abs(want)), f"token {at}: lse"
 
-    out, lse = K.csa2_paged_decode_attn(q[:1], cache, scale)
-    check(out[0], lse[0], 0, n)
+    for chunk in (0, 384):
+        out, lse = K.csa2_paged_decode_attn(q[:1], cache, scale, chunk=chunk)
+        check(out[0], lse[0], 0, n)
     out, lse = K.csa2_paged_window_attn(q, _ints(0, T), cache, scale)
     for t in range(T):
         check(out[t], lse[t], t, n - T + 1 + t)
