@@ -9,7 +9,7 @@
 //   S^T[key, head] = K q^T        (M = 128 keys, N = NH, K = D)
 //   O^T[channel, head] += V^T P   (M = 128 channels, N = NH, K = 128 keys)
 //   warps 0-15      softmax, one thread per key and 16 of the heads (warps 0-3 alone
-//                   for up to 16): P = 2^(s - ref), row sums kept per thread and added
+//                   for up to 16): P = 2^(s - ref) (f16: lifted by 2^7), row sums kept per thread and added
 //                   up at the end
 //   one warp        issues the products
 //   three warps     fill a ring of 8 blocks of 64 channels x 128 keys (16 KiB, TMA
@@ -47,6 +47,10 @@ constexpr int SLOTS = 8;
 constexpr int BLK = KT * 128;                          // 64 channels of 128 keys
 constexpr int kBits = 8;
 constexpr float kLazy = 8.0f;
+// f16 weights stand 2^7 above the reference's 1, so that they keep 11 bits down to 2^-21 of
+// it (f16's last step would else be 2^-24); 2^7 and the lag of 2^8 stay finite.
+template <class T>
+constexpr float lift_of() { return std::is_same<T, __half>::value ? 7.0f : 0.0f; }
 
 template <int D, int NH>
 struct Lay {
@@ -105,6 +109,7 @@ __global__ void __launch_bounds__(Lay<D, NH>::THREADS, 1)
     paged_wide_kernel(const Params p, const __grid_constant__ CUtensorMap k_map, const __grid_constant__ CUtensorMap v_map) {
   using L = Lay<D, NH>;
   constexpr int DB = L::DB, SW = L::SW, HW = L::HW;
+  constexpr float LIFT = lift_of<T>(), LAG = kLazy + LIFT;         // the largest log2 of a weight
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint64_t* bar = reinterpret_cast<uint64_t*>(smem + L::BAR);
@@ -397,7 +402,7 @@ __global__ void __launch_bounds__(Lay<D, NH>::THREADS, 1)
         return top;
       };
       const float top = refer();
-      if (any_of<N>(!started || !ok || top > kLazy)) {
+      if (any_of<N>(!started || !ok || top > LAG)) {
         if (any_of<N>(!ok)) {                          // all leave together
           ok = false;
           break;
@@ -416,9 +421,10 @@ __global__ void __launch_bounds__(Lay<D, NH>::THREADS, 1)
           const int h = threadIdx.x;
           const float m = fmaxf(fmaxf(red[h], red[NH + h]), fmaxf(red[2 * NH + h], red[3 * NH + h]));
           const float was = ref[h];
-          const bool move = set ? m + was > kLazy : m > -INFINITY;
-          if (move) ref[h] = -m;
-          factor[h] = move && set ? exp2_approx(-m - was) : 1.0f;   // nothing weighed before: nothing to rescale
+          const bool move = set ? m + was > LAG : m > -INFINITY;
+          const float now = -lifted(m, LIFT);
+          if (move) ref[h] = now;
+          factor[h] = move && set ? exp2_approx(now - was) : 1.0f;  // nothing weighed before: nothing to rescale
           set |= move;
         }
         started = !any_of<N>(threadIdx.x < rows && !set);

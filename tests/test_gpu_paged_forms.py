@@ -1,6 +1,6 @@
 """Paged-cache calls in forms that the operator-by-operator tests leave out: tables wider than
-the sequences, and scores of any size.  Bounds as in paged_util, but no test here allows f16
-weights a fixed step."""
+the sequences, f16 weights far below a row's largest, and scores of any size.  Bounds as in
+paged_util, but no test here allows f16 weights a fixed step."""
 import numpy as np
 import pytest
 import torch
@@ -67,6 +67,47 @@ def test_window_bits_do_not_depend_on_the_tables_width(kind, D, G, page, window,
     assert torch.equal(got[0][0], got[1][0]) and torch.equal(got[0][1], got[1][1])
     want = O.causal_attn(P.f64(q), np.arange(300), *host[0], D ** -0.5, window, sinks)
     P.check_attn(*got[0], want, P.f64(q), host[0][0], D ** -0.5, cache.dtype, 300)
+
+
+# ------------------------------------------------------------------ f16 weights
+
+def _dominated(D, heads, G, page, L, T, seed):
+    """A cache whose first token outweighs each other one by 2^16 to 2^20, by query head, and has a
+    zero value row; every other token of a head weighs the same, so that a rounding of the weights
+    does not average out."""
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    Hq, scale, c = heads * G, D ** -0.5, 16.0
+    w = (torch.randn(1, heads, D, generator=g, device="cuda") * 0.3).half()
+    w[..., 0] = 0
+    k = w.repeat(L, 1, 1)
+    k[0, :, 0] = c
+    v = (torch.rand(L, heads, D, generator=g, device="cuda") + 0.5).half()
+    v[0] = 0
+    q = (torch.randn(T, Hq, D, generator=g, device="cuda") * 0.5).half()
+    order = torch.linspace(16.2, 19.9, Hq, device="cuda") + torch.rand(T, Hq, generator=g, device="cuda") * 0.1
+    q[..., 0] = (order / (scale * c * np.log2(np.e))).half()
+    kp, table = _paged(k, page, seed)
+    vp, _ = _paged(v, page, seed)
+    cache = K.PagedKv(kp, table[None], _ints(L), v=vp)
+    return cache, q, P.f64(k), P.f64(v), scale
+
+
+@pytest.mark.parametrize("D,G,page", [(64, 8, 16), (128, 16, 16), (256, 3, 32), (512, 64, 64), (512, 16, 16)])
+@pytest.mark.parametrize("chunk", [0, 256])
+def test_decode_f16_weights_far_below_the_largest(D, G, page, chunk):
+    cache, q, k, v, scale = _dominated(D, 2, G, page, 1000, 1, 17)
+    out, lse = K.csa2_paged_decode_attn(q, cache, scale, chunk=chunk)
+    want = O.causal_attn(P.f64(q), [999], k, v, scale)
+    _check_relative(out, lse, want, P.f64(q), k, scale, torch.float16, 1000)
+
+
+@pytest.mark.parametrize("D,G,page", [(256, 40, 16), (512, 64, 64)])
+@pytest.mark.parametrize("window,sinks", [(0, 0), (600, 1)])
+def test_window_f16_weights_far_below_the_largest(D, G, page, window, sinks):
+    cache, q, k, v, scale = _dominated(D, 2, G, page, 1000, 20, 18)
+    out, lse = K.csa2_paged_window_attn(q, _ints(0, 20), cache, scale, window=window, sinks=sinks)
+    want = O.causal_attn(P.f64(q), np.arange(980, 1000), k, v, scale, window, sinks)
+    _check_relative(out, lse, want, P.f64(q), k, scale, torch.float16, 1000)
 
 
 # ------------------------------------------------------------------ scores of any size
