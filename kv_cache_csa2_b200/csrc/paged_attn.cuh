@@ -30,6 +30,10 @@ __device__ __forceinline__ float exp2_approx(float x) {
 // the largest is 2^lift.  From 2^22 on m - lift would round by more than the half step by
 // which 2^15 stays finite in f16; there a score's own steps hide what the lift is for.
 __device__ __forceinline__ float lifted(float m, float lift) { return fabsf(m) < 4194304.0f ? m - lift : m; }
+// Where a reference may lag by 2^8, f16 weights stand 2^7 above its 1, so that they keep 11
+// bits down to 2^-21 of it (f16's last step would else be 2^-24); the two together stay finite.
+template <class T>
+constexpr float lift_of() { return std::is_same<T, __half>::value ? 7.0f : 0.0f; }
 
 __device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t a) {
   asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"

@@ -47,10 +47,6 @@ constexpr int SLOTS = 8;
 constexpr int BLK = KT * 128;                          // 64 channels of 128 keys
 constexpr int kBits = 8;
 constexpr float kLazy = 8.0f;
-// f16 weights stand 2^7 above the reference's 1, so that they keep 11 bits down to 2^-21 of
-// it (f16's last step would else be 2^-24); 2^7 and the lag of 2^8 stay finite.
-template <class T>
-constexpr float lift_of() { return std::is_same<T, __half>::value ? 7.0f : 0.0f; }
 
 template <int D, int NH>
 struct Lay {

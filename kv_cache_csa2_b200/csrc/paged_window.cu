@@ -596,7 +596,8 @@ __global__ void __launch_bounds__(kThreads, 1) paged_window_kernel(const Params 
     // tokens [win, pos] and [0, sink_end) are visible
     const int win = p.window > 0 ? pos - p.window + 1 : 0;
     const int sink_end = min(p.sinks, pos + 1);
-    float m = -INFINITY;
+    constexpr float LIFT = lift_of<T>();
+    float m = -INFINITY;                               // the reference (none yet: -inf)
     float2 l = make_float2(0.0f, 0.0f);
     uint32_t phase = 0, pv_phase = 0;                  // bit h: parity of s_full[w][h], of pv_done[w][h]
     int last = 0;                                      // half handed on last
@@ -604,11 +605,12 @@ __global__ void __launch_bounds__(kThreads, 1) paged_window_kernel(const Params 
     // The reference stays while the maximum has not outgrown it; else the output so
     // far is rescaled, once the products of the half handed on last have ended.
     auto refer = [&](float top) -> float {
-      const bool grow = top > m + kLazy || (m == -INFINITY && top > -INFINITY);
+      const bool grow = top > m + (kLazy + LIFT) || (m == -INFINITY && top > -INFINITY);
+      const float now = lifted(top, LIFT);
       if (__any_sync(0xffffffffu, grow)) {
         const bool scale_o = grow && m > -INFINITY;
         if (__any_sync(0xffffffffu, scale_o)) {
-          const float f = scale_o ? exp2_approx(m - top) : 1.0f;
+          const float f = scale_o ? exp2_approx(m - now) : 1.0f;
           l.x *= f;
           l.y *= f;
           ok = wait_phase(pv_done + 2 * w + last, ((pv_phase >> last) & 1) ^ 1, abort_flag, p.kv.err);
@@ -625,7 +627,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_window_kernel(const Params 
             }
           }
         }
-        if (grow) m = top;
+        if (grow) m = now;
       }
       return m == -INFINITY ? 0.0f : m;
     };

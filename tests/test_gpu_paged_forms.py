@@ -101,7 +101,7 @@ def test_decode_f16_weights_far_below_the_largest(D, G, page, chunk):
     _check_relative(out, lse, want, P.f64(q), k, scale, torch.float16, 1000)
 
 
-@pytest.mark.parametrize("D,G,page", [(256, 40, 16), (512, 64, 64)])
+@pytest.mark.parametrize("D,G,page", [(64, 8, 16), (128, 4, 64), (128, 3, 4), (256, 40, 16), (512, 64, 64)])
 @pytest.mark.parametrize("window,sinks", [(0, 0), (600, 1)])
 def test_window_f16_weights_far_below_the_largest(D, G, page, window, sinks):
     cache, q, k, v, scale = _dominated(D, 2, G, page, 1000, 20, 18)
