@@ -61,6 +61,8 @@ __global__ void __launch_bounds__(kThreads) paged_attn_kernel(const Params p) {
   using L = Lay<D>;
   constexpr int KT = L::KT, NK = KT / 4;               // keys per tile, and per warp in the scores
   constexpr int NC = D / 4;                            // channels per warp in the output
+  // f16 weights stand 2^15 above the largest's 1 (see paged_decode.cu)
+  constexpr float LIFT = std::is_same<T, __half>::value ? 15.0f : 0.0f;
   extern __shared__ __align__(16) uint8_t smem[];
   const bool shared_kv = p.kv.v == p.kv.k;
   uint8_t* sK = smem + L::K;
@@ -256,8 +258,8 @@ __global__ void __launch_bounds__(kThreads) paged_attn_kernel(const Params p) {
     for (int u = 0; u < 2; ++u) {
       const int r = (lane >> 2) + 8 * u;
       const float mn = fmaxf(m[u], fmaxf(fmaxf(sRed[r], sRed[16 + r]), fmaxf(sRed[32 + r], sRed[48 + r])));
-      ref[u] = mn == -INFINITY ? 0.0f : mn;            // nothing seen yet: every weight is 0
-      alpha[u] = exp2_approx(m[u] - ref[u]);
+      ref[u] = mn == -INFINITY ? 0.0f : lifted(mn, LIFT);          // nothing seen yet: every weight is 0
+      alpha[u] = exp2_approx(lifted(m[u], LIFT) - ref[u]);
       m[u] = mn;
       l[u] *= alpha[u];
     }
@@ -317,7 +319,7 @@ __global__ void __launch_bounds__(kThreads) paged_attn_kernel(const Params p) {
 #pragma unroll
       for (int i = 0; i < NC / 8; ++i)
         *reinterpret_cast<float2*>(po + warp * NC + i * 8 + (lane & 3) * 2) = make_float2(o[i][2 * u], o[i][2 * u + 1]);
-      if (warp == 0 && (lane & 3) == 0) p.part_ml[at * p.chunks + chunk] = make_float2(m[u], lr);
+      if (warp == 0 && (lane & 3) == 0) p.part_ml[at * p.chunks + chunk] = make_float2(lifted(m[u], LIFT), lr);
     } else {
       const float inv = lr > 0.0f ? 1.0f / lr : (lr == 0.0f ? 0.0f : lr);
       uint16_t* po = p.out + at * D;
@@ -334,7 +336,7 @@ __global__ void __launch_bounds__(kThreads) paged_attn_kernel(const Params p) {
         *reinterpret_cast<uint32_t*>(po + warp * NC + i * 8 + (lane & 3) * 2) =
             Num<T>::down(o[i][2 * u] * inv, o[i][2 * u + 1] * inv);
       if (p.lse && warp == 0 && (lane & 3) == 0)
-        p.lse[at] = lr == 0.0f ? -INFINITY : (m[u] + log2f(lr)) * kLn2;
+        p.lse[at] = lr == 0.0f ? -INFINITY : (lifted(m[u], LIFT) + log2f(lr)) * kLn2;
     }
   }
   if (!FP4 && !decode) {

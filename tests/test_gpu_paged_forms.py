@@ -92,7 +92,7 @@ def _dominated(D, heads, G, page, L, T, seed):
     return cache, q, P.f64(k), P.f64(v), scale
 
 
-@pytest.mark.parametrize("D,G,page", [(64, 8, 16), (128, 16, 16), (256, 3, 32), (512, 64, 64), (512, 16, 16)])
+@pytest.mark.parametrize("D,G,page", [(64, 8, 16), (128, 16, 16), (256, 3, 32), (512, 64, 64), (512, 16, 16), (512, 5, 4)])
 @pytest.mark.parametrize("chunk", [0, 256])
 def test_decode_f16_weights_far_below_the_largest(D, G, page, chunk):
     cache, q, k, v, scale = _dominated(D, 2, G, page, 1000, 1, 17)
@@ -101,7 +101,8 @@ def test_decode_f16_weights_far_below_the_largest(D, G, page, chunk):
     _check_relative(out, lse, want, P.f64(q), k, scale, torch.float16, 1000)
 
 
-@pytest.mark.parametrize("D,G,page", [(64, 8, 16), (128, 4, 64), (128, 3, 4), (256, 40, 16), (512, 64, 64)])
+@pytest.mark.parametrize("D,G,page", [(64, 8, 16), (128, 4, 64), (128, 3, 4), (256, 2, 16), (256, 40, 16), (512, 4, 16),
+                                      (512, 64, 64)])
 @pytest.mark.parametrize("window,sinks", [(0, 0), (600, 1)])
 def test_window_f16_weights_far_below_the_largest(D, G, page, window, sinks):
     cache, q, k, v, scale = _dominated(D, 2, G, page, 1000, 20, 18)
