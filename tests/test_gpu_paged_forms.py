@@ -1,6 +1,7 @@
 """Paged-cache calls in forms that the operator-by-operator tests leave out: tables wider than
-the sequences, f16 weights far below a row's largest, and scores of any size.  Bounds as in
-paged_util, but no test here allows f16 weights a fixed step."""
+the sequences, f16 weights far below a row's largest, scores of any size, pages longer than a
+tile of tokens, offsets past 32 bits, and a side stream for every call.  Bounds follow
+paged_util; _check_relative leaves out its allowance for the fixed step of small f16 weights."""
 import numpy as np
 import pytest
 import torch
@@ -185,3 +186,115 @@ def test_equal_scores_of_any_size(kind, D, G, page, size):
     out, lse = K.csa2_paged_window_attn(q, _ints(0, T), cache, scale)
     for t in range(T):
         check(out[t], lse[t], t, n - T + 1 + t)
+
+
+# ------------------------------------------------------------------ long pages
+
+def _long_pages(kind, D, heads, G, shared, page, window, sinks, lens, news):
+    cache, host = P.make_cache(kind, lens, page, heads, D, shared=shared, seed=33, spare=0)
+    q = P.rng_normal(34, len(lens), heads * G, D, dt=cache.dtype)
+    out, lse = K.csa2_paged_decode_attn(q, cache, D ** -0.5, window=window, sinks=sinks)
+    qh = P.f64(q)
+    for b, n in enumerate(lens):
+        want = O.causal_attn(qh[b:b + 1], [n - 1], *host[b], D ** -0.5, window, sinks)
+        P.check_attn(out[b:b + 1], lse[b:b + 1], want, qh[b:b + 1], host[b][0], D ** -0.5, cache.dtype, n, f"decode {b}")
+    q = P.rng_normal(35, sum(news), heads * G, D, dt=cache.dtype)
+    cu = np.concatenate([[0], np.cumsum(news)])
+    out, lse = K.csa2_paged_window_attn(q, _ints(*cu), cache, D ** -0.5, window=window, sinks=sinks)
+    qh = P.f64(q)
+    for b, n in enumerate(lens):
+        sl = slice(cu[b], cu[b + 1])
+        want = O.causal_attn(qh[sl], np.arange(n - news[b], n), *host[b], D ** -0.5, window, sinks)
+        P.check_attn(out[sl], lse[sl], want, qh[sl], host[b][0], D ** -0.5, cache.dtype, n, f"prompt {b}")
+
+
+@pytest.mark.parametrize("kind", ["bf16", "f16", "fp4"])
+@pytest.mark.parametrize("D,heads,G,shared", [(64, 2, 4, False), (128, 1, 8, True), (256, 1, 33, False), (512, 1, 64, True),
+                                              (512, 2, 3, False)])
+@pytest.mark.parametrize("page,window,sinks", [(256, 0, 0), (1024, 300, 140)])
+def test_pages_longer_than_a_tile(kind, D, heads, G, shared, page, window, sinks):
+    _long_pages(kind, D, heads, G, shared, page, window, sinks, [1, 300, 1290], [1, 40, 9])
+
+
+@pytest.mark.parametrize("D,G", [(64, 4), (512, 64)])
+def test_the_longest_pages(D, G):
+    _long_pages("bf16", D, 1, G, True, 65536, 0, 0, [700], [50])
+
+
+@pytest.mark.parametrize("kind", ["bf16", "fp4"])
+def test_append_to_pages_longer_than_a_tile(kind):
+    page, D, T = 1024, 64, 70
+    rows = P.rng_normal(36, T, 2, D)
+    lens = torch.zeros(2, dtype=torch.int32, device="cuda")
+    table = _ints(2, 0, 1, 3).view(2, 2)
+    w = D // 2 if kind == "fp4" else D
+    k = torch.zeros(4, page, 2, w, dtype=torch.uint8 if kind == "fp4" else torch.bfloat16, device="cuda")
+    s = torch.zeros(4, page, 2, D // 16, dtype=torch.uint8, device="cuda") if kind == "fp4" else None
+    cache = K.PagedKv(k, table, lens, k_scales=s)
+    seq = (torch.arange(T, device="cuda") % 2).int()
+    pos = (torch.arange(T, device="cuda") // 2 * 37 + 500).int()     # over the page border
+    K.csa2_paged_append(cache, rows, None, seq, pos)
+    at = table[seq.long(), pos.long() // page].long(), pos.long() % page
+    if kind == "fp4":
+        codes, scales = K.csa2_fp4_pack(rows)
+        assert torch.equal(k[at], codes) and torch.equal(s[at], scales)
+        assert int((s != 0).sum()) == int((scales != 0).sum())
+    else:
+        assert torch.equal(k[at], rows) and int((k != 0).sum()) == int((rows != 0).sum())
+
+
+# ------------------------------------------------------------------ offsets past 32 bits
+
+@pytest.mark.parametrize("T,H,ts,hs", [(6, 2, (1 << 29) + 64, 128), (2, 6, 128, (1 << 29) + 64)])
+def test_norm_rope_offsets_past_32_bits(T, H, ts, hs):
+    """Rows of one CTA that lie more than 2^31 elements apart, token by token or head by head."""
+    D = 64
+    span = (T - 1) * ts + (H - 1) * hs + D
+    assert span > 1 << 31
+    buf = torch.empty(span, dtype=torch.bfloat16, device="cuda")
+    x = buf.as_strided((T, H, D), (ts, hs, 1))
+    rows = P.rng_normal(41, T, H, D)
+    x.copy_(rows)
+    pos = torch.arange(T, dtype=torch.int32, device="cuda") + 5
+    w = torch.rand(D, device="cuda") + 0.5
+    rope = K.Rope((10000.0 ** (-torch.arange(32, dtype=torch.float64) / 32)).float().cuda())
+    want = K.csa2_qk_norm_rope(rows, rows, pos, q_weight=w, k_weight=w, rope=rope)
+    q, _ = K.csa2_qk_norm_rope(x, rows, pos, q_weight=w, k_weight=w, rope=rope)
+    _, k = K.csa2_qk_norm_rope(rows, x, pos, q_weight=w, k_weight=w, rope=rope)
+    assert torch.equal(q, want[0]) and torch.equal(k, want[1])
+    K.csa2_qk_norm_rope(x, None, pos, q_weight=w, rope=rope, q_out=x)             # in place
+    assert torch.equal(x.contiguous(), want[0])
+
+
+# ------------------------------------------------------------------ streams
+
+def test_every_call_on_a_side_stream():
+    """`stream` with every other argument away from its default: the same results as without."""
+    T, Hq, Hk, D = 120, 8, 2, 128
+    x = P.rng_normal(51, T, Hq + 2 * Hk, D, dt=torch.float16)
+    pos = torch.arange(T, dtype=torch.int32, device="cuda")
+    seq = (pos >= 70).int()
+    at = torch.where(seq == 1, pos - 70, pos)
+    w = [torch.rand(D, device="cuda") + 0.5 for _ in range(2)]
+    rope = K.Rope((10000.0 ** (-torch.arange(16, dtype=torch.float64) / 16)).float().cuda(), offset=64, interleaved=True)
+    side = torch.cuda.Stream()
+
+    def layer(s):
+        kv = [torch.zeros(10, 16, Hk, D, dtype=torch.float16, device="cuda") for _ in range(2)]
+        cache = K.PagedKv(kv[0], torch.arange(10, dtype=torch.int32, device="cuda").flip(0).view(2, 5).contiguous(),
+                          _ints(70, 50), v=kv[1])
+        cu, outs = _ints(0, 70, 120), (torch.zeros(T, Hq, D, dtype=torch.float16, device="cuda"), torch.zeros(T, Hq, device="cuda"))
+        qk = torch.zeros(T, Hq, D, dtype=torch.float16, device="cuda"), torch.zeros(T, Hk, D, dtype=torch.float16, device="cuda")
+        torch.cuda.synchronize()
+        q, k = K.csa2_qk_norm_rope(x[:, :Hq], x[:, Hq:Hq + Hk], at, q_weight=w[0], k_weight=w[1], eps=0.25, rope=rope,
+                                   q_out=qk[0], k_out=qk[1], stream=s)
+        assert q is qk[0] and k is qk[1]
+        K.csa2_paged_append(cache, k, x[:, Hq + Hk:], seq, at, rope=rope, stream=s)
+        a = K.csa2_paged_window_attn(q, cu, cache, 0.07, window=30, sinks=3, out=outs[0], lse=outs[1], stream=s)
+        assert a[0] is outs[0] and a[1] is outs[1]
+        d = K.csa2_paged_decode_attn(q[:2], cache, 0.07, window=30, sinks=3, chunk=64, stream=s)
+        torch.cuda.synchronize()
+        return q, k, *kv, *a, *d
+
+    for want, got in zip(layer(None), layer(side)):
+        assert torch.equal(want, got)
