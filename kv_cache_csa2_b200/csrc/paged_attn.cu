@@ -12,7 +12,9 @@
 // (O, m, l) partials that paged_combine_kernel joins in chunk order.
 //
 // Takes what the kernels of paged_decode.cu, paged_wide.cu and paged_window.cu do not:
-// latency-bound, as two block barriers per tile stand between the products.  Measured
+// prompts over rows of 256 and 512 channels (FP4, few heads, short windows, pages below 8
+// tokens), and single tokens over 16-bit rows of 512 in pages below 8 tokens.
+// Latency-bound, as two block barriers per tile stand between the products.  Measured
 // (512 tokens behind 1000, 64 heads over one 512-wide row): 237 us, against 113 on
 // the tensor cores in paged_wide.cu.
 #include <algorithm>
@@ -43,7 +45,10 @@ struct Params {
 };
 
 template <int D>
-constexpr int tile_keys() { return D <= 256 ? 64 : 32; }
+constexpr int tile_keys() { return D == 256 ? 64 : 32; }
+// whether single tokens come here
+template <int D, bool FP4>
+constexpr bool decodes() { return D == 512 && !FP4; }
 
 template <int D>
 struct Lay {
@@ -76,7 +81,7 @@ __global__ void __launch_bounds__(kThreads) paged_attn_kernel(const Params p) {
   // which rows
   int b, n_b, kvh, chunk = 0;
   int64_t r0, q_row0;
-  const bool decode = p.cu_q == nullptr;
+  const bool decode = decodes<D, FP4>() && p.cu_q == nullptr;
   if (decode) {
     b = blockIdx.z;
     n_b = 1;
@@ -490,7 +495,7 @@ csa2_status dispatch(const PagedAttn& a, const Params& p, dim3 grid, cudaStream_
     return a.fmt == CSA2_KV_FP4   ? run<__nv_bfloat16, D_, true>(p, grid, stream)        \
            : a.fmt == CSA2_KV_F16 ? run<__half, D_, false>(p, grid, stream)              \
                                   : run<__nv_bfloat16, D_, false>(p, grid, stream);
-  CSA2_PAGED(64) CSA2_PAGED(128) CSA2_PAGED(256) CSA2_PAGED(512)
+  CSA2_PAGED(256) CSA2_PAGED(512)
 #undef CSA2_PAGED
   return CSA2_ERR_UNSUPPORTED;
 }

@@ -51,7 +51,8 @@ constexpr float kLazy = 8.0f;
 template <int D, int NH>
 struct Lay {
   static constexpr int SW = NH == 64 ? 16 : 4;          // softmax warps
-  static constexpr int HW = NH * 4 / SW;               // heads per softmax thread
+  static constexpr int HW = 16;                        // heads per softmax thread
+  static_assert(SW * HW == 4 * NH, "a thread per key and 16 heads");
   static constexpr int THREADS = (SW + 1 + kLoaders) * 32;
   static constexpr int DB = D / 64;                    // blocks per tile of keys (or values)
   static constexpr int QB = NH * 128;                  // 64 channels of q
@@ -434,14 +435,13 @@ __global__ void __launch_bounds__(Lay<D, NH>::THREADS, 1)
         if (tile > 0) {
           // the value products of the tile before ended before this tile's scores did
 #pragma unroll 1
-          for (int i = 0; i < D / 128 * (HW / 16); ++i) {
-            const int c = i % (HW / 16) * 16;
-            const uint32_t to = o_at + i / (HW / 16) * 64 + c;
+          for (int i = 0; i < D / 128; ++i) {
+            const uint32_t to = o_at + i * 64;
             uint32_t v[16];
             tmem_ld16(to, v);
             tmem_wait_ld();
 #pragma unroll
-            for (int e = 0; e < 16; ++e) v[e] = __float_as_uint(__uint_as_float(v[e]) * factor[hb + c + e]);
+            for (int e = 0; e < 16; ++e) v[e] = __float_as_uint(__uint_as_float(v[e]) * factor[hb + e]);
             tmem_st16(to, v);
           }
           tmem_wait_st();
@@ -490,22 +490,21 @@ __global__ void __launch_bounds__(Lay<D, NH>::THREADS, 1)
     const int64_t row0 = static_cast<int64_t>(token) * p.Hq + kvh * p.G + h0;
     const bool partial = p.chunks > 1 && at.tiles > per;
 #pragma unroll 1
-    for (int i = 0; i < D / 128 * (HW / 16) && ok; ++i) {
-      const int db = i / (HW / 16), c = hb + i % (HW / 16) * 16;
+    for (int db = 0; db < D / 128 && ok; ++db) {
       uint32_t v[16];
       if (tiles > 0) {
-        tmem_ld16(tmem + lane_off + O_COL + db * 64 + c, v);
+        tmem_ld16(o_at + db * 64, v);
         tmem_wait_ld();
       }
 #pragma unroll
       for (int e = 0; e < 16; ++e) {
-        if (c + e >= rows) break;
+        if (hb + e >= rows) break;
         const float o = tiles > 0 ? __uint_as_float(v[e]) : 0.0f;
-        const int64_t row = row0 + c + e;
+        const int64_t row = row0 + hb + e;
         if (partial) {
           p.part_o[(row * p.chunks + chunk) * D + db * 128 + key] = o;
         } else {
-          const float s = factor[c + e];
+          const float s = factor[hb + e];
           const float inv = s > 0.0f ? 1.0f / s : (s == 0.0f ? 0.0f : s);
           p.out[row * D + db * 128 + key] = static_cast<uint16_t>(Num<T>::down(o * inv, 0.0f) & 0xffffu);
         }
@@ -604,11 +603,11 @@ csa2_status launch(const PagedAttn& a, Params& p, dim3 grid, cudaStream_t stream
                                    a.kv.token_stride, a.kv.n_pages, a.kv.page_stride, p.box));
   grid.y = static_cast<unsigned>(a.kv.heads * p.row_tiles);
 #define CSA2_WIDE_N(T_, D_, N_) (sh ? run<T_, D_, N_, true>(p, grid, maps, stream) : run<T_, D_, N_, false>(p, grid, maps, stream))
-#define CSA2_WIDE_D(T_, D_) (nh == 16 ? CSA2_WIDE_N(T_, D_, 16) : CSA2_WIDE_N(T_, D_, 64))
-#define CSA2_WIDE(T_) (a.D == 256 ? CSA2_WIDE_D(T_, 256) : CSA2_WIDE_D(T_, 512))
+  // rows of 256 channels come here as prompts only, which have more than 16 heads
+#define CSA2_WIDE(T_) \
+  (a.D == 256 ? CSA2_WIDE_N(T_, 256, 64) : nh == 16 ? CSA2_WIDE_N(T_, 512, 16) : CSA2_WIDE_N(T_, 512, 64))
   return a.fmt == CSA2_KV_F16 ? CSA2_WIDE(__half) : CSA2_WIDE(__nv_bfloat16);
 #undef CSA2_WIDE
-#undef CSA2_WIDE_D
 #undef CSA2_WIDE_N
 }
 
