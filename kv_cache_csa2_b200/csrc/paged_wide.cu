@@ -530,7 +530,7 @@ __global__ void __launch_bounds__(Lay<D, NH>::THREADS, 1)
 }
 
 template <class T, int D, int NH, bool SHARED>
-csa2_status run(const Params& p, dim3 grid, const CUtensorMap (&maps)[2], cudaStream_t stream) {
+csa2_status run(const char* fn, const Params& p, dim3 grid, const CUtensorMap (&maps)[2], cudaStream_t stream) {
   using L = Lay<D, NH>;
   static PerDevice<int> opted;
   opted.get(+[]() -> int {
@@ -550,9 +550,9 @@ csa2_status run(const Params& p, dim3 grid, const CUtensorMap (&maps)[2], cudaSt
   note_launch(LK_ATTN, 1, stream);
   if (e != cudaSuccess) {
     cudaGetLastError();
-    return fail(CSA2_ERR_CUDA, "csa2_paged_decode_attn: launch failed: %s", cudaGetErrorString(e));
+    return fail(CSA2_ERR_CUDA, "%s: launch failed: %s", fn, cudaGetErrorString(e));
   }
-  return check_launch("csa2_paged_decode_attn");
+  return check_launch(fn);
 }
 
 }  // namespace
@@ -578,7 +578,7 @@ bool paged_wide_prompt_applies(const PagedAttn& a) {
 
 namespace {
 
-csa2_status launch(const PagedAttn& a, Params& p, dim3 grid, cudaStream_t stream) {
+csa2_status launch(const char* fn, const PagedAttn& a, Params& p, dim3 grid, cudaStream_t stream) {
   p.q = static_cast<const uint16_t*>(a.q);
   p.q_token = a.q_token;
   p.q_head = a.q_head;
@@ -602,7 +602,7 @@ csa2_status launch(const PagedAttn& a, Params& p, dim3 grid, cudaStream_t stream
     CSA2_TRY(make_tensor_map_paged(&maps[i], i ? a.kv.v : a.kv.k, a.D, a.kv.heads, a.kv.head_stride, page,
                                    a.kv.token_stride, a.kv.n_pages, a.kv.page_stride, p.box));
   grid.y = static_cast<unsigned>(a.kv.heads * p.row_tiles);
-#define CSA2_WIDE_N(T_, D_, N_) (sh ? run<T_, D_, N_, true>(p, grid, maps, stream) : run<T_, D_, N_, false>(p, grid, maps, stream))
+#define CSA2_WIDE_N(T_, D_, N_) (sh ? run<T_, D_, N_, true>(fn, p, grid, maps, stream) : run<T_, D_, N_, false>(fn, p, grid, maps, stream))
   // rows of 256 channels come here as prompts only, which have more than 16 heads
 #define CSA2_WIDE(T_) \
   (a.D == 256 ? CSA2_WIDE_N(T_, 256, 64) : nh == 16 ? CSA2_WIDE_N(T_, 512, 16) : CSA2_WIDE_N(T_, 512, 64))
@@ -620,7 +620,7 @@ csa2_status launch_paged_wide(const PagedAttn& a, int chunk, int chunks, float* 
   p.part_ml = part_ml;
   p.chunk = chunk;
   p.chunks = chunks;
-  return launch(a, p, dim3(static_cast<unsigned>(chunks), 1, static_cast<unsigned>(a.kv.B)), stream);
+  return launch("csa2_paged_decode_attn", a, p, dim3(static_cast<unsigned>(chunks), 1, static_cast<unsigned>(a.kv.B)), stream);
 }
 
 csa2_status launch_paged_wide_prompt(const PagedAttn& a, const int32_t* cu_q, int64_t T, cudaStream_t stream) {
@@ -629,7 +629,7 @@ csa2_status launch_paged_wide_prompt(const PagedAttn& a, const int32_t* cu_q, in
   p.T = static_cast<int>(T);
   p.chunk = KT;
   p.chunks = 1;
-  return launch(a, p, dim3(static_cast<unsigned>(T)), stream);
+  return launch("csa2_paged_window_attn", a, p, dim3(static_cast<unsigned>(T)), stream);
 }
 
 }  // namespace csa2
