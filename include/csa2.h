@@ -366,6 +366,7 @@ csa2_status csa2_qk_norm_rope(csa2_dtype dtype, const csa2_heads* q, const float
  *   max_len a bound of lens[] the caller knows, or 0: max_pages * page_size.
  *           It only sets into how many chunks a decode launch is cut; a longer
  *           sequence is still attended whole (its last chunk takes the rest).
+ *           Chunks made for a bound far above the lengths leave SMs idle.
  * page_size is a power of two up to 65536.  A length outside [0, max_pages *
  * page_size] or a table entry outside [0, n_pages) that a call needs is
  * recorded as CSA2_ERR_BOUNDS; the length is clamped, the page's tokens are
@@ -407,10 +408,12 @@ csa2_status csa2_paged_append(csa2_dtype dtype, const csa2_heads* k, const csa2_
  *   lse[b,h]   = log sum_j exp(scale * q . k)
  * A sequence of length 0 gives out = 0 and lse = -inf.  Dot products, softmax
  * statistics and sums in f32, the weights rounded to the 16-bit type (FP4: to
- * f16) for the product with the values, out rounded once.  FP4 rows are dequantised exactly.
+ * f16) for the product with the values, out rounded once.  FP4 rows are dequantised
+ * exactly; q meets them in f16 after a power of two per row, so channels below 2^-14
+ * of the row's largest move by up to 2^-25 of it.
  * The visible tokens are cut into chunks that run side by side and are joined
- * in order.  chunk > 0 (a multiple of 64; rows of 512 channels take the next
- * multiple of 128) fixes their length: a query's bits
+ * in order.  chunk > 0 (a multiple of 64; 16-bit rows of 512 channels in pages of
+ * at least 8 tokens take the next multiple of 128) fixes their length: a query's bits
  * then depend on its own sequence only (lens[b] <= max_len); chunk = 0 lets the library choose it
  * from B, heads and max_len.
  *   q    rows of the cache's 16-bit type (bf16 for FP4), heads a multiple of
@@ -432,8 +435,10 @@ csa2_status csa2_paged_decode_attn(const csa2_heads* q, const csa2_paged_kv* cac
  * keys and values of all of them already appended).  Each query sees tokens as
  * in csa2_paged_decode_attn from its own position; a query whose position would
  * be negative (more rows than lens[b]) sees nothing.  Rows outside every
- * sequence (behind cu_q[B]) are left as they were.  The bits of a query do not
- * depend on the other sequences or on where the prompt was cut into chunks.
+ * sequence (behind cu_q[B]) are left as they were.  The weights round to the 16-bit type
+ * (FP4: to bf16).  The bits of a query do not depend on the other sequences, on the
+ * table's width or on where the prompt was cut into chunks, as long as the values that it
+ * and the rest of its chunk see are finite.
  * Up to 524288 visible tokens, a value that is not finite reaches only the queries that see its token (a
  * query that sees one may have channels turn NaN in which its values are finite).
  *   q    rows of the cache's 16-bit type    cu_q int32 [B + 1], ascending, cu_q[B] <= T
