@@ -41,11 +41,12 @@ struct Params {
 // codes of this lane's half, and the block's scale.
 __device__ __forceinline__ uint32_t pack_half_block(const uint4& v, uint32_t* scale) {
   const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-  uint32_t amax = 0;                                  // |bf16| bits order like the values
+  uint32_t amax = 0;                                  // |bf16| bits order like the values; NaN is passed over
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
-    amax = max(amax, w[j] & 0x7fffu);
-    amax = max(amax, (w[j] >> 16) & 0x7fffu);
+    const uint32_t lo = w[j] & 0x7fffu, hi = (w[j] >> 16) & 0x7fffu;
+    if (lo <= 0x7f80u) amax = max(amax, lo);
+    if (hi <= 0x7f80u) amax = max(amax, hi);
   }
   amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
   const uint32_t sc = fp4::scale_code_for(__uint_as_float(amax << 16));

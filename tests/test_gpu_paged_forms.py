@@ -243,6 +243,29 @@ def test_append_to_pages_longer_than_a_tile(kind):
         assert torch.equal(k[at], rows) and int((k != 0).sum()) == int((rows != 0).sum())
 
 
+# ------------------------------------------------------------------ values that are not finite
+
+@pytest.mark.parametrize("D,heads", [(64, 2), (512, 1)])
+def test_append_fp4_of_rows_that_are_not_finite(D, heads):
+    """A NaN takes no part in its block's scale, an infinity saturates it: csa2_fp4_pack of the row."""
+    T, page = 40, 16
+    rows = P.rng_normal(61, T, heads, D)
+    g = torch.Generator(device="cuda").manual_seed(62)
+    for i, x in enumerate((float("nan"), float("inf"), float("-inf"))):
+        at = torch.rand(rows.shape, generator=g, device="cuda") < 0.02
+        rows[at] = x
+    rows[7] = float("nan")
+    rows.view(torch.int16)[8, 0, :16] = -1                           # NaN with the sign and every payload bit
+    codes, scales = K.csa2_fp4_pack(rows)
+    k = torch.zeros(3, page, heads, D // 2, dtype=torch.uint8, device="cuda")
+    s = torch.zeros(3, page, heads, D // 16, dtype=torch.uint8, device="cuda")
+    cache = K.PagedKv(k, _ints(2, 0, 1)[None], _ints(0), k_scales=s)
+    pos = torch.arange(T, dtype=torch.int32, device="cuda")
+    K.csa2_paged_append(cache, rows, None, torch.zeros_like(pos), pos)
+    at = cache.table[0][pos.long() // page].long(), pos.long() % page
+    assert torch.equal(s[at], scales) and torch.equal(k[at], codes)
+
+
 # ------------------------------------------------------------------ offsets past 32 bits
 
 @pytest.mark.parametrize("T,H,ts,hs", [(6, 2, (1 << 29) + 64, 128), (2, 6, 128, (1 << 29) + 64)])
