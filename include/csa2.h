@@ -388,7 +388,8 @@ typedef struct {
  * as it is) and of v go to token pos[t] of sequence seq[t].  The result is
  * rounded once to the cache's 16-bit type; an FP4 cache takes csa2_fp4_pack of
  * that rounded row.  seq[t] = -1 skips the row (a padded batch).  cache->lens
- * is not read.  Two rows of one call must not name the same token.
+ * is not read.  Two rows of one call must not name the same token, and the cache's
+ * rows must not overlap one another.
  *   k, v   dtype rows, heads == cache->heads, D == cache->dim; v NULL for a
  *          shared cache (cache->v NULL)
  *   seq, pos int32 [T]

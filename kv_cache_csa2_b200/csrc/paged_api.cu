@@ -1,5 +1,7 @@
 // The C ABI of the head and paged-cache calls (include/csa2.h, part p): argument
 // validation, strides filled in, dispatch to the launchers.
+#include <algorithm>
+
 #include "common.cuh"
 #include "paged.h"
 
@@ -34,6 +36,23 @@ csa2_status distinct_rows(const char* fn, const char* name, const HeadRows& r, i
   const bool token_major = (H <= 1 || h >= D) && (T <= 1 || t >= (H - 1) * h + D);
   const bool head_major = (T <= 1 || t >= D) && (H <= 1 || h >= (T - 1) * t + D);
   REQUIRE(token_major || head_major, "%s: %s rows overlap (strides %lld, %lld)", fn, name, (long long)t, (long long)h);
+  return CSA2_OK;
+}
+
+// The rows of a cache that is written must not overlap one another: taken from the smallest
+// stride up, each dimension steps over all that lies within.
+csa2_status distinct_cache_rows(const char* fn, const csa2_paged_kv* c, const PagedView& v) {
+  struct Dim {
+    int64_t n, stride;
+  } d[3] = {{c->heads, v.head_stride}, {c->page_size, v.token_stride}, {c->n_pages, v.page_stride}};
+  std::sort(d, d + 3, [](const Dim& a, const Dim& b) { return a.stride < b.stride; });
+  int64_t extent = c->dim;
+  for (const Dim& x : d) {
+    if (x.n <= 1) continue;
+    REQUIRE(x.stride >= extent, "%s: cache rows overlap (strides %lld, %lld, %lld)", fn, (long long)v.page_stride,
+            (long long)v.token_stride, (long long)v.head_stride);
+    extent += (x.n - 1) * x.stride;
+  }
   return CSA2_OK;
 }
 
@@ -177,6 +196,7 @@ csa2_status csa2_paged_append(csa2_dtype dtype, const csa2_heads* k, const csa2_
   REQUIRE(T >= 0, "%s: T=%lld is negative", fn, (long long)T);
   PagedView view;
   CSA2_TRY(view_of(fn, cache, &view, nullptr));
+  CSA2_TRY(distinct_cache_rows(fn, cache, view));
   const bool fp4 = cache->fmt == CSA2_KV_FP4;
   REQUIRE((dtype == CSA2_F16) == (cache->fmt == CSA2_KV_F16), "%s: dtype %d does not match cache format %d", fn,
           int(dtype), int(cache->fmt));
