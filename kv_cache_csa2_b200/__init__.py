@@ -652,10 +652,18 @@ def _attn_out(q, out, lse):
     return out, lse
 
 
+def _fits(name, *counts):
+    """Counts that a 32-bit argument would cut to other counts are refused."""
+    for x in counts:
+        if not -0x80000000 <= x <= 0x7fffffff:
+            raise ValueError(f"{name}: {x} is past 32 bits")
+
+
 def csa2_paged_decode_attn(q, cache, scale: float, window: int = 0, sinks: int = 0, chunk: int = 0, out=None, lse=None,
                            stream=None):
     """Attention of one new token per sequence (q [B, Hq, D], at position lens[b] - 1)
     over a PagedKv: the last `window` tokens (0: all) and the first `sinks`."""
+    _fits("csa2_paged_decode_attn", window, sinks, chunk)
     dev = cache.device
     _same_device(csa2_paged_decode_attn, dev, q, out, lse)
     if stream is not None or dev != _torch().cuda.current_device():
@@ -679,6 +687,7 @@ def csa2_paged_window_attn(q, cu_q, cache, scale: float, window: int = 0, sinks:
                            stream=None):
     """Causal attention of a prompt chunk: sequence b's new tokens are rows
     cu_q[b]..cu_q[b+1] of q [T, Hq, D], the last at position lens[b] - 1."""
+    _fits("csa2_paged_window_attn", window, sinks)
     dev = cache.device
     _same_device(csa2_paged_window_attn, dev, q, cu_q, out, lse)
     if stream is not None or dev != _torch().cuda.current_device():
