@@ -289,6 +289,39 @@ def test_norm_rope_offsets_past_32_bits(T, H, ts, hs):
     assert torch.equal(x.contiguous(), want[0])
 
 
+@pytest.mark.parametrize("kind,D,G,page", [("bf16", 512, 64, 64), ("f16", 512, 4, 16), ("bf16", 512, 3, 4), ("bf16", 256, 8, 16),
+                                           ("bf16", 128, 8, 16), ("fp4", 128, 4, 64), ("fp4", 512, 20, 64)])
+def test_cache_past_32_bits(kind, D, G, page):
+    """A pool of more than 2^31 channels (FP4: 2^32 channels, 2^31 bytes of codes) with the sequences in
+    its last pages and its first: append, single tokens and a prompt."""
+    far = (1 << (32 if kind == "fp4" else 31)) // (page * D)
+    n_pages, n, new = far + 40, 130, 9
+    dt, need = P.DT[kind], -(-n // page)
+    empty = lambda w, t: torch.empty(n_pages, page, 1, w, dtype=t, device="cuda")
+    fp4 = kind == "fp4"
+    table = torch.stack([torch.arange(n_pages - need, n_pages), torch.arange(need)]).int().cuda()
+    cache = K.PagedKv(empty(D // 2 if fp4 else D, torch.uint8 if fp4 else dt), table, _ints(n, n),
+                      k_scales=empty(D // 16, torch.uint8) if fp4 else None)
+    rows = P.rng_normal(71, 2 * n, 1, D, dt=dt)
+    seq = (torch.arange(2 * n, device="cuda") // n).int()
+    pos = (torch.arange(2 * n, device="cuda") % n).int()
+    K.csa2_paged_append(cache, rows, None, seq, pos)
+    kept = K.csa2_fp4_unpack(*K.csa2_fp4_pack(rows)) if fp4 else rows
+    host = P.f64(kept).reshape(2, n, 1, D)
+    scale = D ** -0.5
+    q = P.rng_normal(72, 2, G, D, dt=dt)
+    out, lse = K.csa2_paged_decode_attn(q, cache, scale)
+    qp = P.rng_normal(73, 2 * new, G, D, dt=dt)
+    outp, lsep = K.csa2_paged_window_attn(qp, _ints(0, new, 2 * new), cache, scale)
+    for b in range(2):
+        h = host[b]
+        want = O.causal_attn(P.f64(q[b:b + 1]), [n - 1], h, h, scale)
+        P.check_attn(out[b:b + 1], lse[b:b + 1], want, P.f64(q[b:b + 1]), h, scale, dt, n, f"single token {b}")
+        sl = slice(b * new, (b + 1) * new)
+        want = O.causal_attn(P.f64(qp[sl]), np.arange(n - new, n), h, h, scale)
+        P.check_attn(outp[sl], lsep[sl], want, P.f64(qp[sl]), h, scale, dt, n, f"prompt {b}")
+
+
 # ------------------------------------------------------------------ streams
 
 def test_every_call_on_a_side_stream():
