@@ -366,7 +366,8 @@ csa2_status csa2_qk_norm_rope(csa2_dtype dtype, const csa2_heads* q, const float
  *   max_len a bound of lens[] the caller knows, or 0: max_pages * page_size.
  *           It only sets into how many chunks a decode launch is cut; a longer
  *           sequence is still attended whole (its last chunk takes the rest).
- *           Chunks made for a bound far above the lengths leave SMs idle.
+ *           Chunks made for a bound far above the lengths leave SMs idle, and
+ *           scratch grows with the bound: give it where the table is long.
  * page_size is a power of two up to 65536.  A length outside [0, max_pages *
  * page_size] or a table entry outside [0, n_pages) that a call needs is
  * recorded as CSA2_ERR_BOUNDS; the length is clamped, the page's tokens are

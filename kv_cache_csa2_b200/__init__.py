@@ -492,7 +492,8 @@ class PagedKv:
     page_size, heads, D] bf16 / f16 with adjacent channels, or uint8 FP4 codes
     [n_pages, page_size, heads, D/2] with scales [n_pages, page_size, heads, D/16];
     table int32 [B, max_pages], lens int32 [B] (device; the program updates them
-    in place).  max_len: a bound of lens it knows (0: what the table holds)."""
+    in place).  max_len: a bound of lens it knows (0: what the table holds); a
+    decode call is cut into chunks by it, so give it where the table is long."""
 
     def __init__(self, k, table, lens, v=None, k_scales=None, v_scales=None, max_len: int = 0):
         torch = _torch()

@@ -7,8 +7,9 @@
 // (token, head) rows; a group of lanes holds a row, the norm is a shuffle sum.
 // Rows come by cp.async into a thread's own slots, two passes ahead.
 // Measured: 8192 tokens of 64 + 8 heads x 128, 52.2 us (5.79 TB/s, 0.88 of the copy rate;
-// 57.5 with the next row in registers); 4096 of 64 + 1 heads x 512, 98.6 us (5.53 TB/s;
-// 107.5 with 64-bit offsets and rows in registers).  Next to the memory stands instruction
+// 57.5 with the next row in registers; on another card 53.9); 4096 of 64 + 1 heads x 512, 98.6
+// us (5.53 TB/s; 107.5 with 64-bit offsets and rows in registers; on another card 101.7).  Run
+// for seconds, at the power limit's 1760 MHz, 60.5 and 113.  Next to the memory stands instruction
 // issue (every product and sum of the rotation rounds by itself); three or five
 // CTAs per SM (54.4, 55), a stage more (53.3) and the weights in registers are slower.
 

@@ -7,7 +7,7 @@
 // its absolute maximum is one shuffle and each lane packs its own 8 codes.
 // Measured: 8191 tokens of 8 heads x 128 (keys and values), 14.4 us (4.7 TB/s; 15.5 with
 // one row ahead instead of two), about one wave, so the place and angles of a CTA's tokens
-// stand at its start in full; 4096 shared rows x 512 into FP4, 9.0 us, of which the rounding to FP4 (150 instructions
+// stand at its start in full; 4096 shared rows x 512 into FP4, 9.2 us, of which the rounding to FP4 (150 instructions
 // per 16 channels) is the larger part.
 #include <algorithm>
 

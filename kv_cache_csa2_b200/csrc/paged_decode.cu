@@ -11,7 +11,8 @@
 // with warp-level products: at 16 rows the arithmetic is 16 multiply-adds per
 // byte, far below what they deliver.
 // Measured: 64 ragged sequences of up to 16384 tokens, 64 heads over 8 x 128, 233 us
-// (6.05 TB/s, 0.92 of a plain copy's rate); one sequence of 8192 with its join, 9.0 us.
+// (6.05 TB/s, 0.92 of a plain copy's rate; 250 run for seconds, at the power limit's 1570
+// MHz); one sequence of 8192 with its join, 8.9 us.
 //
 // FP4 rows stay packed in shared memory and become f16 in registers by the hardware's
 // E2M1 conversion and one product with the scale: a code times a scale has five

@@ -17,17 +17,18 @@
 //                   the value product and is refilled as soon as its channels are
 //                   through.  (One warp took 450 clocks a block to issue.)  The tile
 //                   behind is asked into L2 meanwhile.
-// A head's reference is its maximum over the first tile and moves (with a rescaled
-// output in TMEM) only when some score has outgrown it by 2^8, so the steady state
+// A head's reference is its maximum over the first tile that shows it a score above -inf, and
+// moves (with a rescaled output in TMEM) only when some score has outgrown it by 2^8, so the steady state
 // takes no maximum across keys: one barrier with an OR per tile asks whether any has.
 //
 // A 128 KiB tile of 512 channels arrives in 5600 clocks at an SM's share of the memory
 // rate, but it fills shared memory next to q, so a tile is a chain: value products (1750
 // clocks, a pair of blocks free every 440), the next tile's blocks from L2 (3500 at the 37
 // bytes a clock an SM gets), the last pair's score products (650), softmax (1000): 6200.
-// Measured: 32 sequences of 65536 tokens, 64 heads over one 512-wide row, 445 us (4.8 TB/s);
+// Measured: 32 sequences of 65536 tokens, 64 heads over one 512-wide row, 441 us (4.9 TB/s);
 // without the prefetch into L2 461, with 8 softmax warps 450, half of their exponentials
-// on the multiply-add pipe no change.
+// on the multiply-add pipe no change.  That is at 1965 MHz: run for seconds, the card is at
+// its power limit, the clock at 1640 MHz and the time at 512 us, so clocks bound it.
 #include <algorithm>
 #include <type_traits>
 
@@ -570,7 +571,9 @@ bool paged_wide_applies(const PagedAttn& a) {
 // 161 / 414; 512 behind 1000, 16 heads over one 512-wide row: 91 / 75; 60 tokens, 64
 // heads, window 128: 39 / 26.  The two round differently, so the rule takes what belongs
 // to the layer (format, pages, width, heads, window) and not the table's width or a
-// batch's lengths: a query's bits stay the same when its table grows.
+// batch's lengths: a query's bits stay the same when its table grows.  Short prompts without
+// a window pay for that: one of 60 tokens, 64 heads x 512, 23 / 13; 150 tokens 43 / 40; 300
+// tokens 68 / 99.
 bool paged_wide_prompt_applies(const PagedAttn& a) {
   return a.fmt != CSA2_KV_FP4 && a.kv.page_shift >= 3 && a.kv.n_pages > 0 && (a.D == 512 || a.D == 256) && a.G >= 32 &&
          (a.window == 0 || static_cast<int64_t>(a.window) + a.sinks >= 512);

@@ -32,8 +32,10 @@
 // Bound: 4 D flops per (row, key) on the tensor cores against one exponential,
 // 16 of which an SM does per clock: at D = 128 both take 1024 clocks per pair of
 // 128 x 128 tiles.  Measured: 8192 tokens, window 2048 + 4, 32 heads over 4 x 128, 267 us
-// (0.77 Pflop/s); the softmax's latency per 64 keys (1900 clocks against 1280 of
-// products) is what is left, and TMEM has no room for a third row tile.
+// (0.77 Pflop/s; 282 us run for seconds, at the power limit's 1850 MHz); the softmax's latency
+// per 64 keys (1900 clocks against 1280 of products) is what is left, and TMEM has no room
+// for a third row tile.  The launch's 128 registers a thread cost 20 bytes of spill stores
+// and 100 to 116 of loads (8 and 32, 12 and 72 or none with FP4 rows).
 #include <algorithm>
 #include <type_traits>
 
